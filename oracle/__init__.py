@@ -22,6 +22,10 @@ from .lora_oracle import (  # noqa: F401
     stacked_forward,
     decode_fp8_e4m3,
     lora_forward_fp8w,
+    decode_mxfp4,
+    quantize_mxfp4,
+    lora_forward_mxfp4w,
+    expert_routing,
     dora_column_scale,
     dora_forward,
     dora_factored_forward,

@@ -317,6 +317,87 @@ def lora_forward_fp8w(X, Wq, w_scale, A, B, row_slot, slot_rank, slot_alpha, r_m
 
 
 # ---------------------------------------------------------------------------
+# MXFP4 operands and expert routing
+# ---------------------------------------------------------------------------
+_E2M1 = (0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0)
+
+
+def decode_mxfp4(codes, scales) -> np.ndarray:
+    """Exact float64 values of OCP MXFP4 rows: codes uint8 [..., d / 2] (element
+    2c of a row is the low half of byte c; bit 3 of a code is its sign, the rest
+    picks one of eight magnitudes) and E8M0 scales uint8 [..., d / 32], 2^(b -
+    127) for 32 consecutive elements, 255 = NaN."""
+    c = np.asarray(codes, dtype=np.uint8).astype(np.int64)
+    c = np.stack([c & 15, c >> 4], axis=-1).reshape(*c.shape[:-1], -1)
+    v = np.array(_E2M1)[c & 7] * np.where(c & 8, -1.0, 1.0)
+    b = np.asarray(scales, dtype=np.uint8).astype(np.int64)
+    s = np.where(b == 255, np.nan, np.ldexp(1.0, b - 127))
+    return v * np.repeat(s, 32, axis=-1)
+
+
+def quantize_mxfp4(x):
+    """MXFP4 codes and scales of float64 rows, by the format's definition: per 32
+    elements the scale exponent floor(log2 amax) - 2, not below -127, and per
+    element the nearest of the sixteen values, of two equally near the one with
+    the even code.  A block with an infinity or NaN: scale 255, codes 0."""
+    x = np.asarray(x, dtype=np.float64)
+    rows, d = x.shape
+    codes = np.zeros((rows, d), dtype=np.uint8)
+    scales = np.zeros((rows, d // 32), dtype=np.uint8)
+    for i in range(rows):
+        for g in range(d // 32):
+            blk = x[i, 32 * g:32 * g + 32]
+            if not np.all(np.isfinite(blk)):
+                scales[i, g] = 255
+                continue
+            amax = np.max(np.abs(blk))
+            e = -127 if amax == 0 else max(-127, int(np.frexp(amax)[1]) - 1 - 2)
+            scales[i, g] = e + 127
+            for c in range(32):
+                m = abs(blk[c]) / 2.0 ** e
+                best = min(range(8), key=lambda k: (abs(m - _E2M1[k]), k & 1))
+                codes[i, 32 * g + c] = best | (8 if np.signbit(blk[c]) else 0)
+    return codes[:, 0::2] | (codes[:, 1::2] << 4), scales
+
+
+def lora_forward_mxfp4w(X, Wq, w_scale, A, B, row_slot, slot_rank, slot_alpha, r_max: int,
+                        dtype: str, rows: Optional[Iterable[int]] = None):
+    """``lora_forward`` with the base weight given as MXFP4 codes and scales."""
+    W64 = decode_mxfp4(Wq, w_scale)
+    zero_w = np.zeros(W64.shape, dtype=np.uint16 if dtype == "bf16" else np.float32)
+    _, dY, H = lora_forward(X, zero_w, A, B, row_slot, slot_rank, slot_alpha, r_max, dtype,
+                            rows=rows)
+    X64 = decode(X, dtype)
+    idx = list(range(X64.shape[0])) if rows is None else [int(i) for i in rows]
+    return X64[idx] @ W64.T + dY, dY, H
+
+
+def expert_routing(expert_ids, n_experts: int) -> Dict[str, np.ndarray]:
+    """Choices by expert, plainly: for each expert in turn, its choices in
+    order.  ids outside [0, n_experts) are dropped, and counted in status unless
+    they are -1."""
+    ids = np.asarray(expert_ids)
+    flat = ids.reshape(-1)
+    order = [[] for _ in range(n_experts)]
+    position = np.full(flat.shape, -1, dtype=np.int32)
+    bad = 0
+    for c, e in enumerate(flat):
+        if 0 <= e < n_experts:
+            order[e].append(c)
+        elif e != -1:
+            bad += 1
+    offsets = np.zeros(n_experts + 1, dtype=np.int32)
+    sorted_choice = []
+    for e in range(n_experts):
+        for c in order[e]:
+            position[c] = len(sorted_choice)
+            sorted_choice.append(c)
+        offsets[e + 1] = len(sorted_choice)
+    return {"expert_offsets": offsets, "sorted_choice": np.array(sorted_choice, dtype=np.int32),
+            "choice_position": position.reshape(ids.shape), "status": bad}
+
+
+# ---------------------------------------------------------------------------
 # DoRA: magnitude times normalised direction
 # ---------------------------------------------------------------------------
 # The ybb.press multi-LoRA serving article, section 9.2 (DoRA), writes the

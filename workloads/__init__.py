@@ -399,6 +399,15 @@ def make_fp8_weight(seed: int, d_out: int, d_in: int, w_std: float = 0.02):
     return codes, scale.astype(np.float32)
 
 
+def make_mxfp4(seed: int, rows: int, d: int, lo: int = 118, hi: int = 123):
+    """An MXFP4 matrix: random codes uint8 [rows, d / 2] (all sixteen values)
+    and scale bytes [rows, d / 32] uniform in [lo, hi]; the default spread gives
+    values about the size of the bf16 workloads' W."""
+    rng = _rng(np.random.SeedSequence([seed, 0x4F]))
+    return (rng.integers(0, 256, size=(rows, d // 2), dtype=np.uint8),
+            rng.integers(lo, hi + 1, size=(rows, d // 32)).astype(np.uint8))
+
+
 def make_magnitude(seed: int, n_slots: int, d_out: int, scale: float, p_plain: float = 0.25,
                    plain_slots=None):
     """DoRA magnitude vectors, one per slot: float32 [d_out] drawn uniform in
