@@ -382,6 +382,150 @@ lora_status lora_linear_fused_fp8w(const void *X, int64_t ldx, const void *Wq, i
                                    int64_t ldy, void *stream);
 
 /*
+ * MXFP4, the OCP microscaling 4-bit format: the quantized base weight at half
+ * a byte per weight (adapter-batching page, section "Quantized Base Model 与
+ * LoRA 的 Dtype 边界", as for FP8 above).  32 consecutive values of a row share
+ * one E8M0 scale byte b (2^(b - 127); 255 is NaN) and hold an E2M1 code each
+ * (sign, then 0, 0.5, 1, 1.5, 2, 3, 4, 6); element 2c of a row is the low half
+ * of byte c.  An MXFP4 matrix of n rows of d values, d % 32 == 0, is
+ *   codes  uint8 [n][ldq], ldq bytes a row: >= d / 2, a multiple of 16
+ *   scales uint8 [n][lds], lds bytes a row: >= d / 32, a multiple of 4
+ * both 16-byte aligned, ld at most LORA_MAX_LD.  Scale bytes of a row past
+ * d / 32 are read (up to the next multiple of 4) but never used.
+ *
+ * lora_mxfp4_quantize: per block, b = max(0, floor(log2 amax) + 125) and each
+ * code is x / 2^(b - 127) rounded to nearest, ties to the even code, magnitudes
+ * past 6 to 6.  A block with an infinity or NaN gets scale 255 and codes 0.
+ * X [n_rows][d] of `dtype`; bytes past d / 2 and d / 32 of a row are not
+ * written.  lora_mxfp4_dequantize: the codes' values (exact in fp32, and in
+ * bf16; scales of 2^126 and more may pass the type's range: infinity).
+ * n_rows == 0 is a no-op.  Errors: LORA_ERR_DTYPE; n_rows < 0, d <= 0 or an ld
+ * below its width (LORA_ERR_SHAPE); d % 32, an ld or a pointer off its
+ * alignment (LORA_ERR_ALIGN); NULL.
+ */
+lora_status lora_mxfp4_quantize(const void *X, int64_t ldx, int32_t n_rows, int32_t d,
+                                int32_t dtype, void *Xq, int64_t ldq, void *x_scale, int64_t lds,
+                                void *stream);
+lora_status lora_mxfp4_dequantize(const void *Xq, int64_t ldq, const void *x_scale, int64_t lds,
+                                  int32_t n_rows, int32_t d, int32_t dtype, void *X, int64_t ldx,
+                                  void *stream);
+
+/*
+ * Base product with an MXFP4 weight and bf16 activations, Y = X dq(Wq)^T:
+ * Wq, w_scale an MXFP4 matrix of d_out rows of d_in values, X [n][d_in] and
+ * Y [n][d_out] bf16.  Codes are widened with their scale to bf16 in registers
+ * (exact), multiplied on MFMA and accumulated in fp32, with one rounding.
+ * lora_linear_fused_mxfp4w adds each row's LoRA term as lora_linear_fused_fp8w
+ * does: from the unquantized activations, in fp32, before the one rounding;
+ * rows of base-only and rank-0 segments equal lora_base_gemm_mxfp4w's output
+ * bit for bit.  bf16 pools only (LORA_ERR_DTYPE).  A NaN scale makes NaN of
+ * every output of its weight row.
+ */
+lora_status lora_base_gemm_mxfp4w(const void *X, int64_t ldx, const void *Wq, int64_t ldw,
+                                  const void *w_scale, int64_t ldws, void *Y, int64_t ldy,
+                                  int32_t n_rows, int32_t d_in, int32_t d_out, void *stream);
+lora_status lora_linear_fused_mxfp4w(const void *X, int64_t ldx, const void *Wq, int64_t ldw,
+                                     const void *w_scale, int64_t ldws, const float *H,
+                                     const lora_segments *seg, const lora_pool *pool, void *Y,
+                                     int64_t ldy, void *stream);
+
+/*
+ * Base product of two MXFP4 matrices, Y = dq(Xq) dq(Wq)^T (activations from
+ * lora_mxfp4_quantize): the codes and scales go to the matrix cores as they
+ * are, products accumulate in fp32, Y [n_rows][d_out] is bf16 and rounded once.
+ * The low-rank term of the unquantized activations is added by lora_expand.
+ */
+lora_status lora_base_gemm_mxfp4(const void *Xq, int64_t ldx, const void *x_scale, int64_t ldxs,
+                                 const void *Wq, int64_t ldw, const void *w_scale, int64_t ldws,
+                                 void *Y, int64_t ldy, int32_t n_rows, int32_t d_in,
+                                 int32_t d_out, void *stream);
+
+/*
+ * Mixture-of-experts layouts (adapter-batching page, "Adapter 不是一块连续 Weight":
+ * MoE layers among the target modules).  A router names top_k experts per
+ * token; choice c = i * top_k + j is token i's j-th.  Host fields: n_tokens,
+ * top_k (1 .. LORA_MAX_TOP_K), n_experts (1 .. LORA_MAX_EXPERTS), with
+ * n_tokens * top_k at most LORA_MAX_CHOICES.  Device arrays, written by
+ * lora_experts_sort and read by the other calls:
+ *   expert_offsets [n_experts + 1]     expert e = sorted rows [off[e], off[e + 1])
+ *   sorted_choice  [n_tokens * top_k]  sorted row -> choice (rows past
+ *                                      expert_offsets[n_experts]: untouched)
+ *   choice_position[n_tokens * top_k]  choice -> sorted row, -1 = dropped
+ *   status         [1]                 choices dropped for a bad id
+ *   workspace      lora_experts_workspace() bytes (NULL allowed when that is 0)
+ */
+#define LORA_MAX_EXPERTS 1024
+#define LORA_MAX_TOP_K 64
+#define LORA_MAX_CHOICES (1 << 30)
+typedef struct {
+  int32_t n_tokens;
+  int32_t top_k;
+  int32_t n_experts;
+  int32_t *expert_offsets;
+  int32_t *sorted_choice;
+  int32_t *choice_position;
+  int32_t *status;
+  int32_t *workspace;
+} lora_experts;
+
+/* Bytes of device workspace lora_experts_sort needs for a batch (0 for
+ * decode-sized ones; -1 for sizes out of range). */
+int64_t lora_experts_workspace(int32_t n_tokens, int32_t top_k, int32_t n_experts);
+
+/*
+ * Group the batch's choices by expert (the sibling of lora_build_segments):
+ * experts in ascending order, an expert's choices in ascending order.
+ * expert_ids: device int32 [n_tokens][top_k].  -1 drops a choice (a padded
+ * token's, or one past an expert's capacity); any other id outside
+ * [0, n_experts) drops it too and counts it in *status.  The same expert may be
+ * named twice by a token.  No host synchronisation, no float arithmetic; the
+ * result does not depend on the order of execution.  n_tokens == 0 writes zero
+ * offsets and status.
+ */
+lora_status lora_experts_sort(const int32_t *expert_ids, const lora_experts *ex, void *stream);
+
+/* Token rows into sorted order: Xs[p] = X[sorted_choice[p] / top_k].
+ * X [n_tokens][d], Xs [n_tokens * top_k][d] of `dtype` (bf16 or fp32), d a
+ * positive multiple of 8.  Rows of Xs past expert_offsets[n_experts] are left
+ * as they were.  Its gradient: lora_experts_combine of dXs with weights NULL. */
+lora_status lora_experts_gather(const void *X, int64_t ldx, const lora_experts *ex, int32_t d,
+                                int32_t dtype, void *Xs, int64_t ldxs, void *stream);
+
+/* Sorted rows back to their tokens: Y[i] = sum_j weights[i][j] Ys[position of
+ * (i, j)] over the token's choices that were not dropped, j ascending, in fp32
+ * with one rounding; a token with none gets zeros.  weights: device fp32
+ * [n_tokens][top_k], or NULL for ones.  Ys, Y as Xs, X above. */
+lora_status lora_experts_combine(const void *Ys, int64_t ldys, const float *weights,
+                                 const lora_experts *ex, int32_t d, int32_t dtype, void *Y,
+                                 int64_t ldy, void *stream);
+
+/* Gradients of lora_experts_combine: dYs[p] = weights[i][j] dY[i] for the
+ * choice (i, j) at sorted row p (rows past expert_offsets[n_experts] are left as
+ * they were) and d_weights[i][j] = <dY[i], Ys[p]> (0 for a dropped choice; fp32
+ * sums in a fixed order).  dYs or d_weights may be NULL to leave it out, not
+ * both (LORA_ERR_NULL); Ys may be NULL when d_weights is. */
+lora_status lora_experts_combine_backward(const void *dY, int64_t lddy, const void *Ys,
+                                          int64_t ldys, const float *weights,
+                                          const lora_experts *ex, int32_t d, int32_t dtype,
+                                          void *dYs, int64_t lddys, float *d_weights,
+                                          void *stream);
+
+/*
+ * The experts' products on MXFP4 weights: for every sorted row p of expert e,
+ *   Y[p] = X[row] dq(Wq_e)^T,   row = sorted_choice[p] / top_k  (gathered != 0)
+ *                               row = p                          (gathered == 0)
+ * with X [n_tokens][d_in] (gathered) or [n_tokens * top_k][d_in] and
+ * Y [n_tokens * top_k][d_out] bf16; rows of Y past expert_offsets[n_experts] are
+ * left as they were.  Wq [n_experts][d_out][ldw] and w_scale
+ * [n_experts][d_out][ldws] are the experts' MXFP4 matrices one after the other.
+ * Arithmetic as lora_base_gemm_mxfp4w.  Errors as there.
+ */
+lora_status lora_experts_gemm_mxfp4w(const void *X, int64_t ldx, int32_t gathered,
+                                     const lora_experts *ex, const void *Wq, int64_t ldw,
+                                     const void *w_scale, int64_t ldws, void *Y, int64_t ldy,
+                                     int32_t d_in, int32_t d_out, void *stream);
+
+/*
  * The whole layer in one call: lora_build_segments, lora_shrink and
  * lora_linear_fused together (adapter-batching page, sections "一个混合
  * Batch 的数学形式" and "Segmented Kernel 需要哪些 Metadata"; its section

@@ -11,6 +11,11 @@ Entry points carry the C names:
 * ``lora_expand(H, seg, pool, Y)``            (Y += ...)
 * ``lora_base_gemm(X, W, Y)``                 (Y = X W^T)
 * ``lora_linear_fused(X, W, H, seg, pool, Y)``  (Y = X W^T + LoRA)
+* ``lora_mxfp4_quantize(X, Xq, x_scale)``      (and ``lora_mxfp4_dequantize``)
+* ``lora_base_gemm_mxfp4w(X, Wq, w_scale, Y)``  (``lora_linear_fused_mxfp4w``,
+  ``lora_base_gemm_mxfp4``: MXFP4 operands)
+* ``lora_experts_sort(expert_ids, ex)``         (``_gather``, ``_combine``,
+  ``_combine_backward``, ``_gemm_mxfp4w``: expert routing)
 
 If the library is missing the import still succeeds, but every entry point
 raises ``RuntimeError``: there is no fallback path.
@@ -35,6 +40,7 @@ STATIC_MAX_ROWS = 32768
 STATIC_MAX_H = 1 << 21
 LAYER_ONE_LAUNCH_ROWS = 512
 LAYER_SYNC_BYTES = 4096
+MAX_EXPERTS, MAX_TOP_K, MAX_CHOICES = 1024, 64, 1 << 30
 
 _c_int32_p = ctypes.POINTER(ctypes.c_int32)
 
@@ -73,6 +79,19 @@ class LoraSegmentsC(ctypes.Structure):
     ]
 
 
+class LoraExpertsC(ctypes.Structure):
+    _fields_ = [
+        ("n_tokens", ctypes.c_int32),
+        ("top_k", ctypes.c_int32),
+        ("n_experts", ctypes.c_int32),
+        ("expert_offsets", ctypes.c_void_p),
+        ("sorted_choice", ctypes.c_void_p),
+        ("choice_position", ctypes.c_void_p),
+        ("status", ctypes.c_void_p),
+        ("workspace", ctypes.c_void_p),
+    ]
+
+
 class LoraError(RuntimeError):
     def __init__(self, code: int, msg: str):
         super().__init__(f"liblora status {code}: {msg}")
@@ -99,6 +118,17 @@ EXPORTS = (
     "lora_linear_fused_static",
     "lora_layer_fused",
     "lora_layer_fused_fp8w",
+    "lora_mxfp4_quantize",
+    "lora_mxfp4_dequantize",
+    "lora_base_gemm_mxfp4w",
+    "lora_linear_fused_mxfp4w",
+    "lora_base_gemm_mxfp4",
+    "lora_experts_workspace",
+    "lora_experts_sort",
+    "lora_experts_gather",
+    "lora_experts_combine",
+    "lora_experts_combine_backward",
+    "lora_experts_gemm_mxfp4w",
 )
 
 
@@ -147,6 +177,31 @@ def lib() -> ctypes.CDLL:
     L.lora_layer_fused.argtypes = [vp, vp, i64, vp, i64, PP, SP, vp, vp, i64, vp, vp]
     L.lora_layer_fused_fp8w.restype = i32
     L.lora_layer_fused_fp8w.argtypes = [vp, vp, i64, vp, i64, vp, PP, SP, vp, vp, i64, vp, vp]
+    EP = ctypes.POINTER(LoraExpertsC)
+    L.lora_mxfp4_quantize.restype = i32
+    L.lora_mxfp4_quantize.argtypes = [vp, i64, i32, i32, i32, vp, i64, vp, i64, vp]
+    L.lora_mxfp4_dequantize.restype = i32
+    L.lora_mxfp4_dequantize.argtypes = [vp, i64, vp, i64, i32, i32, i32, vp, i64, vp]
+    L.lora_base_gemm_mxfp4w.restype = i32
+    L.lora_base_gemm_mxfp4w.argtypes = [vp, i64, vp, i64, vp, i64, vp, i64, i32, i32, i32, vp]
+    L.lora_linear_fused_mxfp4w.restype = i32
+    L.lora_linear_fused_mxfp4w.argtypes = [vp, i64, vp, i64, vp, i64, vp, SP, PP, vp, i64, vp]
+    L.lora_base_gemm_mxfp4.restype = i32
+    L.lora_base_gemm_mxfp4.argtypes = [vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, i32, i32, i32,
+                                       vp]
+    L.lora_experts_workspace.restype = i64
+    L.lora_experts_workspace.argtypes = [i32, i32, i32]
+    L.lora_experts_sort.restype = i32
+    L.lora_experts_sort.argtypes = [vp, EP, vp]
+    L.lora_experts_gather.restype = i32
+    L.lora_experts_gather.argtypes = [vp, i64, EP, i32, i32, vp, i64, vp]
+    L.lora_experts_combine.restype = i32
+    L.lora_experts_combine.argtypes = [vp, i64, vp, EP, i32, i32, vp, i64, vp]
+    L.lora_experts_combine_backward.restype = i32
+    L.lora_experts_combine_backward.argtypes = [vp, i64, vp, i64, vp, EP, i32, i32, vp, i64, vp, vp]
+    L.lora_experts_gemm_mxfp4w.restype = i32
+    L.lora_experts_gemm_mxfp4w.argtypes = [vp, i64, i32, EP, vp, i64, vp, i64, vp, i64, i32, i32,
+                                           vp]
     if L.lora_abi_version() != ABI_VERSION:
         raise RuntimeError("liblora ABI version mismatch")
     _lib = L
@@ -603,3 +658,228 @@ def lora_linear_fused_static(row_slot: torch.Tensor, X: torch.Tensor, W: torch.T
         raise ValueError("shapes: row_slot [n], X [n, d_in], W [d_out, d_in], Y [n, d_out]")
     _check(lib().lora_linear_fused_static(_ptr(row_slot), _ptr(X), _ld(X), _ptr(W), _ld(W), pool.c,
                                           n, _ptr(Y), _ld(Y), _stream(stream)))
+
+
+# ---------------------------------------------------------------------------
+# MXFP4 operands
+# ---------------------------------------------------------------------------
+def _launch_stream(stream, *tensors):
+    """The call's stream, after checking that every tensor is on its device (a
+    kernel would fault on another's memory)."""
+    s = torch.cuda.current_stream() if stream is None else stream
+    for t in tensors:
+        if t is not None and t.device != s.device:
+            raise ValueError(f"tensor on {t.device}, the call's stream is on {s.device}")
+    return ctypes.c_void_p(s.cuda_stream)
+
+
+def mxfp4_empty(n_rows: int, d: int, device="cuda"):
+    """Room for an MXFP4 matrix: codes uint8 [n_rows, d / 2] and scales uint8
+    [n_rows, d / 32], with rows padded to 16 and 4 bytes."""
+    if d % 32:
+        raise ValueError("d must be a multiple of 32")
+    u8 = dict(dtype=torch.uint8, device=device)
+    return (torch.empty((n_rows, d // 2), **u8),
+            torch.empty((n_rows, (d // 32 + 3) // 4 * 4), **u8)[:, :d // 32])
+
+
+def _check_mxfp4(q: torch.Tensor, scale: torch.Tensor, rows: int, d: int, what: str) -> None:
+    if q.dtype != torch.uint8 or scale.dtype != torch.uint8:
+        raise ValueError(f"{what}: uint8 E2M1 codes and E8M0 scales")
+    if d % 32 or tuple(q.shape) != (rows, d // 2) or tuple(scale.shape) != (rows, d // 32):
+        raise ValueError(f"{what}: codes [{rows}, d / 2] and scales [{rows}, d / 32], d % 32 == 0")
+
+
+def _ldb(t: torch.Tensor, unit: int) -> int:
+    """Bytes a row of a uint8 matrix; a single row (or none) may have any
+    stride, and needs no more than its width."""
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError("expected a row-major 2-D tensor")
+    return t.stride(0) if t.shape[0] > 1 else (t.shape[1] + unit - 1) // unit * unit
+
+
+def lora_mxfp4_quantize(X: torch.Tensor, Xq: torch.Tensor, x_scale: torch.Tensor,
+                        stream=None) -> None:
+    """Rows of X (bf16 or float32) to MXFP4 codes and scales (``mxfp4_empty``)."""
+    n, d = X.shape
+    _check_mxfp4(Xq, x_scale, n, d, "Xq, x_scale")
+    st = _launch_stream(stream, X, Xq, x_scale)
+    _check(lib().lora_mxfp4_quantize(_ptr(X), _ld(X), n, d, _dtype_code(X.dtype), _ptr(Xq),
+                                     _ldb(Xq, 16), _ptr(x_scale), _ldb(x_scale, 4),
+                                     st))
+
+
+def lora_mxfp4_dequantize(Xq: torch.Tensor, x_scale: torch.Tensor, X: torch.Tensor,
+                          stream=None) -> None:
+    """The values of MXFP4 codes and scales, into X (bf16 or float32)."""
+    n, d = X.shape
+    _check_mxfp4(Xq, x_scale, n, d, "Xq, x_scale")
+    st = _launch_stream(stream, Xq, x_scale, X)
+    _check(lib().lora_mxfp4_dequantize(_ptr(Xq), _ldb(Xq, 16), _ptr(x_scale), _ldb(x_scale, 4), n,
+                                       d, _dtype_code(X.dtype), _ptr(X), _ld(X), st))
+
+
+def lora_base_gemm_mxfp4w(X: torch.Tensor, Wq: torch.Tensor, w_scale: torch.Tensor,
+                          Y: torch.Tensor, stream=None) -> None:
+    """Y = X dq(Wq)^T with an MXFP4 weight [d_out, d_in]; X, Y bf16."""
+    if X.dtype != torch.bfloat16 or Y.dtype != torch.bfloat16:
+        raise ValueError("X and Y must be bf16")
+    n, d_in = X.shape
+    d_out = Wq.shape[0]
+    _check_mxfp4(Wq, w_scale, d_out, d_in, "Wq, w_scale")
+    if tuple(Y.shape) != (n, d_out):
+        raise ValueError("shapes: X [n, d_in], Wq [d_out, d_in / 2], Y [n, d_out]")
+    st = _launch_stream(stream, X, Wq, w_scale, Y)
+    _check(lib().lora_base_gemm_mxfp4w(_ptr(X), _ld(X), _ptr(Wq), _ldb(Wq, 16), _ptr(w_scale),
+                                       _ldb(w_scale, 4), _ptr(Y), _ld(Y), n, d_in, d_out,
+                                       st))
+
+
+def lora_linear_fused_mxfp4w(X: torch.Tensor, Wq: torch.Tensor, w_scale: torch.Tensor,
+                             H: torch.Tensor, seg: Segments, pool: Pool, Y: torch.Tensor,
+                             stream=None) -> None:
+    """lora_linear_fused with an MXFP4 base weight (Wq, w_scale)."""
+    if not (X.dtype == Y.dtype == pool.dtype == torch.bfloat16):
+        raise ValueError("X and Y must be bf16, as the pool")
+    _check_mxfp4(Wq, w_scale, pool.d_out, pool.d_in, "Wq, w_scale")
+    if tuple(X.shape) != (seg.n_rows, pool.d_in) or tuple(Y.shape) != (seg.n_rows, pool.d_out):
+        raise ValueError("shapes: X [n, d_in], Wq [d_out, d_in / 2], Y [n, d_out]")
+    if H.dtype != torch.float32 or tuple(H.shape) != (seg.n_rows, pool.r_max) or not H.is_contiguous():
+        raise ValueError("H: contiguous float32 [n_rows, r_max]")
+    st = _launch_stream(stream, X, Wq, w_scale, H, Y)
+    _check(lib().lora_linear_fused_mxfp4w(_ptr(X), _ld(X), _ptr(Wq), _ldb(Wq, 16), _ptr(w_scale),
+                                          _ldb(w_scale, 4), _ptr(H), seg.c, pool.c, _ptr(Y),
+                                          _ld(Y), st))
+
+
+def lora_base_gemm_mxfp4(Xq: torch.Tensor, x_scale: torch.Tensor, Wq: torch.Tensor,
+                         w_scale: torch.Tensor, Y: torch.Tensor, stream=None) -> None:
+    """Y = dq(Xq) dq(Wq)^T, both operands MXFP4 (lora_mxfp4_quantize); Y bf16."""
+    if Y.dtype != torch.bfloat16:
+        raise ValueError("Y must be bf16")
+    n, d_out, d_in = Xq.shape[0], Wq.shape[0], Xq.shape[1] * 2
+    _check_mxfp4(Xq, x_scale, n, d_in, "Xq, x_scale")
+    _check_mxfp4(Wq, w_scale, d_out, d_in, "Wq, w_scale")
+    if tuple(Y.shape) != (n, d_out):
+        raise ValueError("shapes: Xq [n, d_in / 2], Wq [d_out, d_in / 2], Y [n, d_out]")
+    st = _launch_stream(stream, Xq, x_scale, Wq, w_scale, Y)
+    _check(lib().lora_base_gemm_mxfp4(_ptr(Xq), _ldb(Xq, 16), _ptr(x_scale), _ldb(x_scale, 4),
+                                      _ptr(Wq), _ldb(Wq, 16), _ptr(w_scale), _ldb(w_scale, 4),
+                                      _ptr(Y), _ld(Y), n, d_in, d_out, st))
+
+
+# ---------------------------------------------------------------------------
+# expert routing
+# ---------------------------------------------------------------------------
+class Experts:
+    """Device arrays of a batch's routing (lora_experts_sort): n_tokens tokens
+    of top_k choices among n_experts experts."""
+
+    def __init__(self, n_tokens: int, top_k: int, n_experts: int, device):
+        ws = lib().lora_experts_workspace(n_tokens, top_k, n_experts)
+        if ws < 0:
+            raise ValueError(f"n_tokens >= 0, top_k in 1..{MAX_TOP_K}, n_experts in "
+                             f"1..{MAX_EXPERTS}, n_tokens * top_k <= {MAX_CHOICES}")
+        i32 = dict(dtype=torch.int32, device=device)
+        self.n_tokens, self.top_k, self.n_experts = n_tokens, top_k, n_experts
+        self.expert_offsets = torch.empty(n_experts + 1, **i32)
+        self.sorted_choice = torch.empty(n_tokens * top_k, **i32)
+        self.choice_position = torch.empty((n_tokens, top_k), **i32)
+        self.status = torch.empty(1, **i32)
+        self.workspace = torch.empty(ws // 4, **i32)
+        self._c = LoraExpertsC(n_tokens, top_k, n_experts, self.expert_offsets.data_ptr(),
+                               self.sorted_choice.data_ptr(), self.choice_position.data_ptr(),
+                               self.status.data_ptr(),
+                               self.workspace.data_ptr() if ws else None)
+
+    @property
+    def c(self):
+        return ctypes.byref(self._c)
+
+
+def lora_experts_sort(expert_ids: torch.Tensor, ex: Experts, stream=None) -> None:
+    """Choices by expert from the router's ids (int32 [n_tokens, top_k], -1 =
+    dropped)."""
+    if expert_ids.dtype != torch.int32 or not expert_ids.is_contiguous() \
+            or tuple(expert_ids.shape) != (ex.n_tokens, ex.top_k):
+        raise ValueError("expert_ids: contiguous int32 [n_tokens, top_k]")
+    st = _launch_stream(stream, expert_ids, ex.expert_offsets)
+    _check(lib().lora_experts_sort(_ptr(expert_ids), ex.c, st))
+
+
+def _expert_rows(ex: Experts, tokens: torch.Tensor, rows: Optional[torch.Tensor]) -> int:
+    d = tokens.shape[1] if tokens.dim() == 2 else -1
+    if tuple(tokens.shape) != (ex.n_tokens, d) or (
+            rows is not None and tuple(rows.shape) != (ex.n_tokens * ex.top_k, d)):
+        raise ValueError("token rows [n_tokens, d] and sorted rows [n_tokens * top_k, d]")
+    if rows is not None and rows.dtype != tokens.dtype:
+        raise ValueError("token rows and sorted rows must share a dtype")
+    return d
+
+
+def _expert_weights(ex: Experts, w: Optional[torch.Tensor], what: str) -> None:
+    if w is not None and (w.dtype != torch.float32 or not w.is_contiguous()
+                          or tuple(w.shape) != (ex.n_tokens, ex.top_k)):
+        raise ValueError(f"{what}: contiguous float32 [n_tokens, top_k]")
+
+
+def lora_experts_gather(X: torch.Tensor, ex: Experts, Xs: torch.Tensor, stream=None) -> None:
+    """Token rows into sorted order: Xs[p] = X[sorted_choice[p] // top_k].  Its
+    gradient is lora_experts_combine(dXs, None, ex, dX)."""
+    d = _expert_rows(ex, X, Xs)
+    st = _launch_stream(stream, X, Xs, ex.expert_offsets)
+    _check(lib().lora_experts_gather(_ptr(X), _ld(X), ex.c, d, _dtype_code(X.dtype), _ptr(Xs),
+                                     _ld(Xs), st))
+
+
+def lora_experts_combine(Ys: torch.Tensor, weights: Optional[torch.Tensor], ex: Experts,
+                         Y: torch.Tensor, stream=None) -> None:
+    """Sorted rows back to their tokens, Y[i] = sum_j weights[i, j] Ys[position
+    of (i, j)]; weights None: ones."""
+    d = _expert_rows(ex, Y, Ys)
+    _expert_weights(ex, weights, "weights")
+    st = _launch_stream(stream, Ys, weights, Y, ex.expert_offsets)
+    _check(lib().lora_experts_combine(_ptr(Ys), _ld(Ys), _ptr(weights), ex.c, d,
+                                      _dtype_code(Y.dtype), _ptr(Y), _ld(Y), st))
+
+
+def lora_experts_combine_backward(dY: torch.Tensor, Ys: Optional[torch.Tensor],
+                                  weights: Optional[torch.Tensor], ex: Experts,
+                                  dYs: Optional[torch.Tensor], d_weights: Optional[torch.Tensor],
+                                  stream=None) -> None:
+    """Gradients of lora_experts_combine: dYs[p] = weights[i, j] dY[i] and
+    d_weights[i, j] = <dY[i], Ys[p]>.  None leaves dYs or d_weights out."""
+    d = _expert_rows(ex, dY, Ys)
+    _expert_rows(ex, dY, dYs)
+    _expert_weights(ex, weights, "weights")
+    _expert_weights(ex, d_weights, "d_weights")
+    st = _launch_stream(stream, dY, Ys, weights, dYs, d_weights, ex.expert_offsets)
+    _check(lib().lora_experts_combine_backward(
+        _ptr(dY), _ld(dY), _ptr(Ys), 0 if Ys is None else _ld(Ys), _ptr(weights), ex.c, d,
+        _dtype_code(dY.dtype), _ptr(dYs), 0 if dYs is None else _ld(dYs), _ptr(d_weights),
+        st))
+
+
+def lora_experts_gemm_mxfp4w(X: torch.Tensor, ex: Experts, Wq: torch.Tensor,
+                             w_scale: torch.Tensor, Y: torch.Tensor, gathered: bool = True,
+                             stream=None) -> None:
+    """The experts' products Y[p] = X[row of p] dq(Wq[e])^T over every expert's
+    sorted rows, with MXFP4 weights Wq [n_experts, d_out, d_in / 2] and w_scale
+    [n_experts, d_out, d_in / 32].  gathered: X holds token rows, read through
+    sorted_choice; otherwise X is in sorted order already."""
+    if X.dtype != torch.bfloat16 or Y.dtype != torch.bfloat16:
+        raise ValueError("X and Y must be bf16")
+    if Wq.dim() != 3 or w_scale.dim() != 3 or Wq.shape[0] != ex.n_experts:
+        raise ValueError("Wq [n_experts, d_out, d_in / 2], w_scale [n_experts, d_out, d_in / 32]")
+    E, d_out, d_in = Wq.shape[0], Wq.shape[1], Wq.shape[2] * 2
+    rows = ex.n_tokens if gathered else ex.n_tokens * ex.top_k
+    if tuple(X.shape) != (rows, d_in) or tuple(Y.shape) != (ex.n_tokens * ex.top_k, d_out):
+        raise ValueError("shapes: X [rows, d_in], Y [n_tokens * top_k, d_out]")
+    for t in (Wq, w_scale):
+        if E > 1 and d_out > 1 and t.stride(0) != d_out * t.stride(1):
+            raise ValueError("the experts' weights must follow each other row by row")
+    _check_mxfp4(Wq[0], w_scale[0], d_out, d_in, "Wq[e], w_scale[e]")
+    st = _launch_stream(stream, X, Wq, w_scale, Y, ex.expert_offsets)
+    _check(lib().lora_experts_gemm_mxfp4w(_ptr(X), _ld(X), 1 if gathered else 0, ex.c, _ptr(Wq),
+                                          _ldb(Wq[0], 16), _ptr(w_scale), _ldb(w_scale[0], 4),
+                                          _ptr(Y), _ld(Y), d_in, d_out, st))

@@ -421,6 +421,225 @@ lora_status lora_layer_fused_fp8w(const int32_t *row_slot, const void *X, int64_
   return layer_call(row_slot, X, ldx, Wq, ldw, w_scale, pool, seg, H, Y, ldy, sync, stream);
 }
 
+namespace {
+
+// MXFP4 matrix of rows of d values: codes and E8M0 scales.
+lora_status check_mxfp4(const void *q, int64_t ldq, const void *s, int64_t lds, int32_t d,
+                        int32_t rows) {
+  if (rows == 0) return LORA_OK;
+  if (!q || !s) return LORA_ERR_NULL;
+  if (ldq < d / 2 || ldq > LORA_MAX_LD || lds < d / 32 || lds > LORA_MAX_LD) return LORA_ERR_SHAPE;
+  if (ldq % 16 || lds % 4 || !aligned16(q) || !aligned16(s)) return LORA_ERR_ALIGN;
+  return LORA_OK;
+}
+
+lora_status check_mx_convert(const void *X, int64_t ldx, int32_t n_rows, int32_t d, int32_t dtype,
+                             const void *q, int64_t ldq, const void *s, int64_t lds) {
+  if (!valid_dtype(dtype)) return LORA_ERR_DTYPE;
+  if (n_rows < 0 || d <= 0 || d > LORA_MAX_LD) return LORA_ERR_SHAPE;
+  if (d % 32) return LORA_ERR_ALIGN;
+  const lora_status st = check_matrix(X, ldx, d, n_rows);
+  return st != LORA_OK ? st : check_mxfp4(q, ldq, s, lds, d, n_rows);
+}
+
+lora_status check_product_shape(int32_t n_rows, int32_t d_in, int32_t d_out) {
+  if (n_rows < 0 || d_in <= 0 || d_out <= 0 || d_in > LORA_MAX_LD) return LORA_ERR_SHAPE;
+  return d_in % 32 || d_out % 8 ? LORA_ERR_ALIGN : LORA_OK;
+}
+
+lora_status check_experts(const lora_experts *ex) {
+  if (!ex) return LORA_ERR_NULL;
+  const int64_t ws = lora_experts_workspace(ex->n_tokens, ex->top_k, ex->n_experts);
+  if (ws < 0) return LORA_ERR_SHAPE;
+  if (!ex->expert_offsets || !ex->status) return LORA_ERR_NULL;
+  if (ex->n_tokens > 0 && (!ex->sorted_choice || !ex->choice_position)) return LORA_ERR_NULL;
+  return LORA_OK;
+}
+
+lora_status check_expert_rows(const lora_experts *ex, int32_t d, int32_t dtype) {
+  const lora_status st = check_experts(ex);
+  if (st != LORA_OK) return st;
+  if (!valid_dtype(dtype)) return LORA_ERR_DTYPE;
+  if (d <= 0 || d > LORA_MAX_LD) return LORA_ERR_SHAPE;
+  return d % 8 ? LORA_ERR_ALIGN : LORA_OK;
+}
+
+}  // namespace
+
+lora_status lora_mxfp4_quantize(const void *X, int64_t ldx, int32_t n_rows, int32_t d,
+                                int32_t dtype, void *Xq, int64_t ldq, void *x_scale, int64_t lds,
+                                void *stream) {
+  const lora_status st = check_mx_convert(X, ldx, n_rows, d, dtype, Xq, ldq, x_scale, lds);
+  if (st != LORA_OK || n_rows == 0) return st;
+  return hip_status(lora::launch_mx_quantize(X, ldx, n_rows, d, dtype, Xq, ldq, x_scale, lds,
+                                             static_cast<hipStream_t>(stream)));
+}
+
+lora_status lora_mxfp4_dequantize(const void *Xq, int64_t ldq, const void *x_scale, int64_t lds,
+                                  int32_t n_rows, int32_t d, int32_t dtype, void *X, int64_t ldx,
+                                  void *stream) {
+  const lora_status st = check_mx_convert(X, ldx, n_rows, d, dtype, Xq, ldq, x_scale, lds);
+  if (st != LORA_OK || n_rows == 0) return st;
+  return hip_status(lora::launch_mx_dequantize(Xq, ldq, x_scale, lds, n_rows, d, dtype, X, ldx,
+                                               static_cast<hipStream_t>(stream)));
+}
+
+lora_status lora_base_gemm_mxfp4w(const void *X, int64_t ldx, const void *Wq, int64_t ldw,
+                                  const void *w_scale, int64_t ldws, void *Y, int64_t ldy,
+                                  int32_t n_rows, int32_t d_in, int32_t d_out, void *stream) {
+  lora_status st = check_product_shape(n_rows, d_in, d_out);
+  if (st != LORA_OK) return st;
+  st = check_mxfp4(Wq, ldw, w_scale, ldws, d_in, d_out);
+  if (st != LORA_OK) return st;
+  st = check_matrix(X, ldx, d_in, n_rows);
+  if (st != LORA_OK) return st;
+  st = check_matrix(Y, ldy, d_out, n_rows);
+  if (st != LORA_OK) return st;
+  if (n_rows == 0) return LORA_OK;
+  const lora::MxScales mx{nullptr, 0, static_cast<const unsigned char *>(w_scale), ldws};
+  return hip_status(lora::launch_gemm_mx(X, ldx, Wq, ldw, mx, Y, ldy, n_rows, d_in, d_out, nullptr,
+                                         nullptr, nullptr, static_cast<hipStream_t>(stream)));
+}
+
+lora_status lora_linear_fused_mxfp4w(const void *X, int64_t ldx, const void *Wq, int64_t ldw,
+                                     const void *w_scale, int64_t ldws, const float *H,
+                                     const lora_segments *seg, const lora_pool *pool, void *Y,
+                                     int64_t ldy, void *stream) {
+  lora_status st = check_pool(pool);
+  if (st != LORA_OK) return st;
+  if (pool->dtype != LORA_BF16) return LORA_ERR_DTYPE;
+  st = check_segments(seg, pool);
+  if (st != LORA_OK) return st;
+  const int32_t n = seg->n_rows;
+  st = check_product_shape(n, pool->d_in, pool->d_out);
+  if (st != LORA_OK) return st;
+  st = check_mxfp4(Wq, ldw, w_scale, ldws, pool->d_in, pool->d_out);
+  if (st != LORA_OK) return st;
+  st = check_matrix(X, ldx, pool->d_in, n);
+  if (st != LORA_OK) return st;
+  st = check_matrix(Y, ldy, pool->d_out, n);
+  if (st != LORA_OK) return st;
+  if (n == 0) return LORA_OK;
+  if (!H) return LORA_ERR_NULL;
+  if (!aligned16(H)) return LORA_ERR_ALIGN;
+  const lora::SegView sv = seg_view(seg);
+  const lora::PoolView pv = pool_view(pool);
+  const lora::MxScales mx{nullptr, 0, static_cast<const unsigned char *>(w_scale), ldws};
+  return hip_status(lora::launch_gemm_mx(X, ldx, Wq, ldw, mx, Y, ldy, n, pool->d_in, pool->d_out, H,
+                                         &sv, &pv, static_cast<hipStream_t>(stream)));
+}
+
+lora_status lora_base_gemm_mxfp4(const void *Xq, int64_t ldx, const void *x_scale, int64_t ldxs,
+                                 const void *Wq, int64_t ldw, const void *w_scale, int64_t ldws,
+                                 void *Y, int64_t ldy, int32_t n_rows, int32_t d_in,
+                                 int32_t d_out, void *stream) {
+  lora_status st = check_product_shape(n_rows, d_in, d_out);
+  if (st != LORA_OK) return st;
+  st = check_mxfp4(Wq, ldw, w_scale, ldws, d_in, d_out);
+  if (st != LORA_OK) return st;
+  st = check_mxfp4(Xq, ldx, x_scale, ldxs, d_in, n_rows);
+  if (st != LORA_OK) return st;
+  st = check_matrix(Y, ldy, d_out, n_rows);
+  if (st != LORA_OK) return st;
+  if (n_rows == 0) return LORA_OK;
+  const lora::MxScales mx{static_cast<const unsigned char *>(x_scale), ldxs,
+                          static_cast<const unsigned char *>(w_scale), ldws};
+  return hip_status(lora::launch_gemm_mx(Xq, ldx, Wq, ldw, mx, Y, ldy, n_rows, d_in, d_out, nullptr,
+                                         nullptr, nullptr, static_cast<hipStream_t>(stream)));
+}
+
+int64_t lora_experts_workspace(int32_t n_tokens, int32_t top_k, int32_t n_experts) {
+  if (n_tokens < 0 || top_k < 1 || top_k > LORA_MAX_TOP_K || n_experts < 1 ||
+      n_experts > LORA_MAX_EXPERTS || (int64_t)n_tokens * top_k > LORA_MAX_CHOICES)
+    return -1;
+  const int32_t n = n_tokens * top_k;
+  if (n <= lora::kExpertOneGroupChoices) return 0;
+  return (int64_t)lora::expert_blocks(n) * (n_experts + 1) * 4;
+}
+
+lora_status lora_experts_sort(const int32_t *expert_ids, const lora_experts *ex, void *stream) {
+  const lora_status st = check_experts(ex);
+  if (st != LORA_OK) return st;
+  if (ex->n_tokens > 0 && !expert_ids) return LORA_ERR_NULL;
+  if (lora_experts_workspace(ex->n_tokens, ex->top_k, ex->n_experts) > 0 && !ex->workspace)
+    return LORA_ERR_NULL;
+  return hip_status(lora::launch_experts_sort(
+      expert_ids, ex->n_tokens * ex->top_k, ex->n_experts, ex->expert_offsets, ex->sorted_choice,
+      ex->choice_position, ex->status, ex->workspace, static_cast<hipStream_t>(stream)));
+}
+
+lora_status lora_experts_gather(const void *X, int64_t ldx, const lora_experts *ex, int32_t d,
+                                int32_t dtype, void *Xs, int64_t ldxs, void *stream) {
+  lora_status st = check_expert_rows(ex, d, dtype);
+  if (st != LORA_OK) return st;
+  st = check_matrix(X, ldx, d, ex->n_tokens);
+  if (st != LORA_OK) return st;
+  st = check_matrix(Xs, ldxs, d, ex->n_tokens);
+  if (st != LORA_OK || ex->n_tokens == 0) return st;
+  return hip_status(lora::launch_experts_gather(X, ldx, ex->choice_position, ex->n_tokens,
+                                                ex->top_k, d, dtype, Xs, ldxs,
+                                                static_cast<hipStream_t>(stream)));
+}
+
+lora_status lora_experts_combine(const void *Ys, int64_t ldys, const float *weights,
+                                 const lora_experts *ex, int32_t d, int32_t dtype, void *Y,
+                                 int64_t ldy, void *stream) {
+  lora_status st = check_expert_rows(ex, d, dtype);
+  if (st != LORA_OK) return st;
+  st = check_matrix(Ys, ldys, d, ex->n_tokens);
+  if (st != LORA_OK) return st;
+  st = check_matrix(Y, ldy, d, ex->n_tokens);
+  if (st != LORA_OK || ex->n_tokens == 0) return st;
+  return hip_status(lora::launch_experts_combine(Ys, ldys, weights, ex->choice_position,
+                                                 ex->n_tokens, ex->top_k, d, dtype, Y, ldy,
+                                                 static_cast<hipStream_t>(stream)));
+}
+
+lora_status lora_experts_combine_backward(const void *dY, int64_t lddy, const void *Ys,
+                                          int64_t ldys, const float *weights,
+                                          const lora_experts *ex, int32_t d, int32_t dtype,
+                                          void *dYs, int64_t lddys, float *d_weights,
+                                          void *stream) {
+  lora_status st = check_expert_rows(ex, d, dtype);
+  if (st != LORA_OK) return st;
+  st = check_matrix(dY, lddy, d, ex->n_tokens);
+  if (st != LORA_OK) return st;
+  if (ex->n_tokens > 0 && !dYs && !d_weights) return LORA_ERR_NULL;
+  if (dYs) st = check_matrix(dYs, lddys, d, ex->n_tokens);
+  if (st != LORA_OK) return st;
+  if (d_weights) st = check_matrix(Ys, ldys, d, ex->n_tokens);
+  if (st != LORA_OK || ex->n_tokens == 0) return st;
+  return hip_status(lora::launch_experts_combine_backward(
+      dY, lddy, Ys, ldys, weights, ex->choice_position, ex->n_tokens, ex->top_k, d, dtype, dYs,
+      lddys, d_weights, static_cast<hipStream_t>(stream)));
+}
+
+lora_status lora_experts_gemm_mxfp4w(const void *X, int64_t ldx, int32_t gathered,
+                                     const lora_experts *ex, const void *Wq, int64_t ldw,
+                                     const void *w_scale, int64_t ldws, void *Y, int64_t ldy,
+                                     int32_t d_in, int32_t d_out, void *stream) {
+  lora_status st = check_experts(ex);
+  if (st != LORA_OK) return st;
+  st = check_product_shape(ex->n_tokens, d_in, d_out);
+  if (st != LORA_OK) return st;
+  st = check_mxfp4(Wq, ldw, w_scale, ldws, d_in, d_out);
+  if (st != LORA_OK) return st;
+  st = check_matrix(X, ldx, d_in, ex->n_tokens);
+  if (st != LORA_OK) return st;
+  st = check_matrix(Y, ldy, d_out, ex->n_tokens);
+  if (st != LORA_OK || ex->n_tokens == 0) return st;
+  const lora::MxScales mx{nullptr, 0, static_cast<const unsigned char *>(w_scale), ldws};
+  const lora::ExpertView ev{ex->n_tokens * ex->top_k,
+                            ex->top_k,
+                            ex->n_experts,
+                            ex->expert_offsets,
+                            gathered ? ex->sorted_choice : nullptr,
+                            (int64_t)d_out * ldw,
+                            (int64_t)d_out * ldws};
+  return hip_status(lora::launch_experts_gemm_mx(X, ldx, ev, Wq, ldw, mx, Y, ldy, d_in, d_out,
+                                                 static_cast<hipStream_t>(stream)));
+}
+
 lora_status lora_linear_fused_static(const int32_t *row_slot, const void *X, int64_t ldx,
                                      const void *W, int64_t ldw, const lora_pool *pool,
                                      int32_t n_rows, void *Y, int64_t ldy, void *stream) {

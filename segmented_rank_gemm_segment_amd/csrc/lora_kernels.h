@@ -48,6 +48,25 @@ __host__ __device__ inline int proj_of(const ProjView &pv, int col) {
   return q;
 }
 
+// E8M0 block scales of MXFP4 operands, one byte per 32 codes: rows of ldx and
+// ldw bytes (multiples of 4).  x: scales of X when it holds codes too.
+struct MxScales {
+  const unsigned char *x;
+  int64_t ldx;
+  const unsigned char *w;
+  int64_t ldw;
+};
+
+// The experts' product: sorted rows [off[e], off[e + 1]) are expert e's, whose
+// codes and scales start e strides (bytes) after the first expert's.  Sorted
+// row p is X row sorted_choice[p] / top_k, or X row p where that is null.
+struct ExpertView {
+  int n_choices, top_k, n_experts;
+  const int32_t *off;
+  const int32_t *sorted_choice;
+  int64_t w_stride, s_stride;
+};
+
 struct BuildArgs {
   const int32_t *row_slot;
   int n, n_slots, r_max;
@@ -104,6 +123,43 @@ hipError_t launch_gemm(const void *X, int64_t ldx, const void *W, int64_t ldw, v
                        int64_t ldy, int M, int K, int N, int dtype, const float *H,
                        const SegView *seg, const PoolView *pool, hipStream_t stream,
                        const float *wscale = nullptr);
+
+// The same with an MXFP4 weight (codes W, ldw bytes a row) and bf16 X
+// (mx.x null), or with both operands MXFP4 codes (ldx bytes a row).
+hipError_t launch_gemm_mx(const void *X, int64_t ldx, const void *W, int64_t ldw,
+                          const MxScales &mx, void *Y, int64_t ldy, int M, int K, int N,
+                          const float *H, const SegView *seg, const PoolView *pool,
+                          hipStream_t stream);
+
+// Y[p] = X[row of p] W_e^T for every sorted row p of every expert e.
+hipError_t launch_experts_gemm_mx(const void *X, int64_t ldx, const ExpertView &ex, const void *W,
+                                  int64_t ldw, const MxScales &mx, void *Y, int64_t ldy, int K,
+                                  int N, hipStream_t stream);
+
+// MXFP4 codes and scales (ldq and lds bytes a row) of rows of d values, and back.
+hipError_t launch_mx_quantize(const void *X, int64_t ldx, int n, int d, int dtype, void *q,
+                              int64_t ldq, void *s, int64_t lds, hipStream_t stream);
+hipError_t launch_mx_dequantize(const void *q, int64_t ldq, const void *s, int64_t lds, int n,
+                                int d, int dtype, void *X, int64_t ldx, hipStream_t stream);
+
+// Choices sorted by expert.  Batches past one workgroup's count them per block
+// of kExpertBlockChoices: counts holds expert_blocks(n) (n_experts + 1) words.
+constexpr int kExpertOneGroupChoices = 8192, kExpertBlockChoices = 4096;
+inline int expert_blocks(int n_choices) {
+  return (int)(((int64_t)n_choices + kExpertBlockChoices - 1) / kExpertBlockChoices);
+}
+hipError_t launch_experts_sort(const int32_t *ids, int n_choices, int n_experts, int32_t *offsets,
+                               int32_t *sorted, int32_t *position, int32_t *status,
+                               int32_t *counts, hipStream_t stream);
+hipError_t launch_experts_gather(const void *X, int64_t ldx, const int32_t *position, int n, int k,
+                                 int d, int dtype, void *Xs, int64_t lds, hipStream_t stream);
+hipError_t launch_experts_combine(const void *Ys, int64_t lds, const float *w,
+                                  const int32_t *position, int n, int k, int d, int dtype, void *Y,
+                                  int64_t ldy, hipStream_t stream);
+hipError_t launch_experts_combine_backward(const void *dY, int64_t ldy, const void *Ys, int64_t lds,
+                                           const float *w, const int32_t *position, int n, int k,
+                                           int d, int dtype, void *dYs, int64_t ldds, float *dw,
+                                           hipStream_t stream);
 
 // Inputs and outputs of the one-launch layer beyond the product's own
 // (layer.cuh): the per-row slot ids and the pool's shrink operands, H, the
