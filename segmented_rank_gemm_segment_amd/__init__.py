@@ -222,7 +222,7 @@ def _dtype_code(t: torch.dtype) -> int:
 
 
 def _ptr(t: Optional[torch.Tensor]):
-    return None if t is None or t.numel() == 0 else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr() or None     # (0 for an empty tensor)
 
 
 def _stream(stream=None):
@@ -231,11 +231,12 @@ def _stream(stream=None):
 
 
 def _ld(t: torch.Tensor) -> int:
-    if t.dim() == 2 and t.numel() == 0:
+    s = t.stride()
+    if len(s) == 2 and t.numel() == 0:
         return max(int(t.shape[1]), 8)
-    if t.dim() != 2 or t.stride(1) != 1:
+    if len(s) != 2 or s[1] != 1:
         raise ValueError("expected a row-major 2-D tensor")
-    return t.stride(0)
+    return s[0]
 
 
 # ---------------------------------------------------------------------------
@@ -665,12 +666,17 @@ def lora_linear_fused_static(row_slot: torch.Tensor, X: torch.Tensor, W: torch.T
 # ---------------------------------------------------------------------------
 def _launch_stream(stream, *tensors):
     """The call's stream, after checking that every tensor is on its device (a
-    kernel would fault on another's memory)."""
-    s = torch.cuda.current_stream() if stream is None else stream
+    kernel would fault on another's memory).  By raw handle: a Stream object
+    costs more than the rest of a decode-sized call."""
+    if stream is None:
+        dev = torch.cuda.current_device()
+        handle = torch._C._cuda_getCurrentRawStream(dev)
+    else:
+        dev, handle = stream.device.index, stream.cuda_stream
     for t in tensors:
-        if t is not None and t.device != s.device:
-            raise ValueError(f"tensor on {t.device}, the call's stream is on {s.device}")
-    return ctypes.c_void_p(s.cuda_stream)
+        if t is not None and (not t.is_cuda or t.get_device() != dev):
+            raise ValueError(f"tensor on {t.device}, the call's stream is on cuda:{dev}")
+    return handle
 
 
 def mxfp4_empty(n_rows: int, d: int, device="cuda"):
@@ -683,40 +689,41 @@ def mxfp4_empty(n_rows: int, d: int, device="cuda"):
             torch.empty((n_rows, (d // 32 + 3) // 4 * 4), **u8)[:, :d // 32])
 
 
-def _check_mxfp4(q: torch.Tensor, scale: torch.Tensor, rows: int, d: int, what: str) -> None:
-    if q.dtype != torch.uint8 or scale.dtype != torch.uint8:
+def _mxfp4(q: torch.Tensor, scale: torch.Tensor, rows: int, d: int, what: str, *batch: int):
+    """(codes, bytes a row, scales, bytes a row) of an MXFP4 matrix, checked; with
+    `batch`, of that many after each other.  A single row may have any stride,
+    and needs no more than its width."""
+    if q.dtype is not torch.uint8 or scale.dtype is not torch.uint8:
         raise ValueError(f"{what}: uint8 E2M1 codes and E8M0 scales")
-    if d % 32 or tuple(q.shape) != (rows, d // 2) or tuple(scale.shape) != (rows, d // 32):
+    hb, g = d // 2, d // 32
+    if d % 32 or q.shape != (*batch, rows, hb) or scale.shape != (*batch, rows, g):
         raise ValueError(f"{what}: codes [{rows}, d / 2] and scales [{rows}, d / 32], d % 32 == 0")
-
-
-def _ldb(t: torch.Tensor, unit: int) -> int:
-    """Bytes a row of a uint8 matrix; a single row (or none) may have any
-    stride, and needs no more than its width."""
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError("expected a row-major 2-D tensor")
-    return t.stride(0) if t.shape[0] > 1 else (t.shape[1] + unit - 1) // unit * unit
+    (*qe, ldq, one), (*se, lds, s_one) = q.stride(), scale.stride()
+    if one != 1 or (s_one != 1 and g > 1):
+        raise ValueError(f"{what}: expected row-major tensors")
+    if batch and batch[0] > 1 and (qe[0] != rows * ldq or se[0] != rows * lds):
+        raise ValueError(f"{what}: the matrices must follow each other row by row")
+    if rows <= 1 and not batch:
+        ldq, lds = hb, (g + 3) // 4 * 4
+    return q.data_ptr() or None, ldq, scale.data_ptr() or None, lds
 
 
 def lora_mxfp4_quantize(X: torch.Tensor, Xq: torch.Tensor, x_scale: torch.Tensor,
                         stream=None) -> None:
     """Rows of X (bf16 or float32) to MXFP4 codes and scales (``mxfp4_empty``)."""
     n, d = X.shape
-    _check_mxfp4(Xq, x_scale, n, d, "Xq, x_scale")
+    q = _mxfp4(Xq, x_scale, n, d, "Xq, x_scale")
     st = _launch_stream(stream, X, Xq, x_scale)
-    _check(lib().lora_mxfp4_quantize(_ptr(X), _ld(X), n, d, _dtype_code(X.dtype), _ptr(Xq),
-                                     _ldb(Xq, 16), _ptr(x_scale), _ldb(x_scale, 4),
-                                     st))
+    _check(lib().lora_mxfp4_quantize(_ptr(X), _ld(X), n, d, _dtype_code(X.dtype), *q, st))
 
 
 def lora_mxfp4_dequantize(Xq: torch.Tensor, x_scale: torch.Tensor, X: torch.Tensor,
                           stream=None) -> None:
     """The values of MXFP4 codes and scales, into X (bf16 or float32)."""
     n, d = X.shape
-    _check_mxfp4(Xq, x_scale, n, d, "Xq, x_scale")
+    q = _mxfp4(Xq, x_scale, n, d, "Xq, x_scale")
     st = _launch_stream(stream, Xq, x_scale, X)
-    _check(lib().lora_mxfp4_dequantize(_ptr(Xq), _ldb(Xq, 16), _ptr(x_scale), _ldb(x_scale, 4), n,
-                                       d, _dtype_code(X.dtype), _ptr(X), _ld(X), st))
+    _check(lib().lora_mxfp4_dequantize(*q, n, d, _dtype_code(X.dtype), _ptr(X), _ld(X), st))
 
 
 def lora_base_gemm_mxfp4w(X: torch.Tensor, Wq: torch.Tensor, w_scale: torch.Tensor,
@@ -726,13 +733,11 @@ def lora_base_gemm_mxfp4w(X: torch.Tensor, Wq: torch.Tensor, w_scale: torch.Tens
         raise ValueError("X and Y must be bf16")
     n, d_in = X.shape
     d_out = Wq.shape[0]
-    _check_mxfp4(Wq, w_scale, d_out, d_in, "Wq, w_scale")
+    w = _mxfp4(Wq, w_scale, d_out, d_in, "Wq, w_scale")
     if tuple(Y.shape) != (n, d_out):
         raise ValueError("shapes: X [n, d_in], Wq [d_out, d_in / 2], Y [n, d_out]")
     st = _launch_stream(stream, X, Wq, w_scale, Y)
-    _check(lib().lora_base_gemm_mxfp4w(_ptr(X), _ld(X), _ptr(Wq), _ldb(Wq, 16), _ptr(w_scale),
-                                       _ldb(w_scale, 4), _ptr(Y), _ld(Y), n, d_in, d_out,
-                                       st))
+    _check(lib().lora_base_gemm_mxfp4w(_ptr(X), _ld(X), *w, _ptr(Y), _ld(Y), n, d_in, d_out, st))
 
 
 def lora_linear_fused_mxfp4w(X: torch.Tensor, Wq: torch.Tensor, w_scale: torch.Tensor,
@@ -741,14 +746,13 @@ def lora_linear_fused_mxfp4w(X: torch.Tensor, Wq: torch.Tensor, w_scale: torch.T
     """lora_linear_fused with an MXFP4 base weight (Wq, w_scale)."""
     if not (X.dtype == Y.dtype == pool.dtype == torch.bfloat16):
         raise ValueError("X and Y must be bf16, as the pool")
-    _check_mxfp4(Wq, w_scale, pool.d_out, pool.d_in, "Wq, w_scale")
+    w = _mxfp4(Wq, w_scale, pool.d_out, pool.d_in, "Wq, w_scale")
     if tuple(X.shape) != (seg.n_rows, pool.d_in) or tuple(Y.shape) != (seg.n_rows, pool.d_out):
         raise ValueError("shapes: X [n, d_in], Wq [d_out, d_in / 2], Y [n, d_out]")
     if H.dtype != torch.float32 or tuple(H.shape) != (seg.n_rows, pool.r_max) or not H.is_contiguous():
         raise ValueError("H: contiguous float32 [n_rows, r_max]")
     st = _launch_stream(stream, X, Wq, w_scale, H, Y)
-    _check(lib().lora_linear_fused_mxfp4w(_ptr(X), _ld(X), _ptr(Wq), _ldb(Wq, 16), _ptr(w_scale),
-                                          _ldb(w_scale, 4), _ptr(H), seg.c, pool.c, _ptr(Y),
+    _check(lib().lora_linear_fused_mxfp4w(_ptr(X), _ld(X), *w, _ptr(H), seg.c, pool.c, _ptr(Y),
                                           _ld(Y), st))
 
 
@@ -758,14 +762,12 @@ def lora_base_gemm_mxfp4(Xq: torch.Tensor, x_scale: torch.Tensor, Wq: torch.Tens
     if Y.dtype != torch.bfloat16:
         raise ValueError("Y must be bf16")
     n, d_out, d_in = Xq.shape[0], Wq.shape[0], Xq.shape[1] * 2
-    _check_mxfp4(Xq, x_scale, n, d_in, "Xq, x_scale")
-    _check_mxfp4(Wq, w_scale, d_out, d_in, "Wq, w_scale")
+    x = _mxfp4(Xq, x_scale, n, d_in, "Xq, x_scale")
+    w = _mxfp4(Wq, w_scale, d_out, d_in, "Wq, w_scale")
     if tuple(Y.shape) != (n, d_out):
         raise ValueError("shapes: Xq [n, d_in / 2], Wq [d_out, d_in / 2], Y [n, d_out]")
     st = _launch_stream(stream, Xq, x_scale, Wq, w_scale, Y)
-    _check(lib().lora_base_gemm_mxfp4(_ptr(Xq), _ldb(Xq, 16), _ptr(x_scale), _ldb(x_scale, 4),
-                                      _ptr(Wq), _ldb(Wq, 16), _ptr(w_scale), _ldb(w_scale, 4),
-                                      _ptr(Y), _ld(Y), n, d_in, d_out, st))
+    _check(lib().lora_base_gemm_mxfp4(*x, *w, _ptr(Y), _ld(Y), n, d_in, d_out, st))
 
 
 # ---------------------------------------------------------------------------
@@ -875,11 +877,7 @@ def lora_experts_gemm_mxfp4w(X: torch.Tensor, ex: Experts, Wq: torch.Tensor,
     rows = ex.n_tokens if gathered else ex.n_tokens * ex.top_k
     if tuple(X.shape) != (rows, d_in) or tuple(Y.shape) != (ex.n_tokens * ex.top_k, d_out):
         raise ValueError("shapes: X [rows, d_in], Y [n_tokens * top_k, d_out]")
-    for t in (Wq, w_scale):
-        if E > 1 and d_out > 1 and t.stride(0) != d_out * t.stride(1):
-            raise ValueError("the experts' weights must follow each other row by row")
-    _check_mxfp4(Wq[0], w_scale[0], d_out, d_in, "Wq[e], w_scale[e]")
+    w = _mxfp4(Wq, w_scale, d_out, d_in, "Wq, w_scale", E)
     st = _launch_stream(stream, X, Wq, w_scale, Y, ex.expert_offsets)
-    _check(lib().lora_experts_gemm_mxfp4w(_ptr(X), _ld(X), 1 if gathered else 0, ex.c, _ptr(Wq),
-                                          _ldb(Wq[0], 16), _ptr(w_scale), _ldb(w_scale[0], 4),
-                                          _ptr(Y), _ld(Y), d_in, d_out, st))
+    _check(lib().lora_experts_gemm_mxfp4w(_ptr(X), _ld(X), 1 if gathered else 0, ex.c, *w, _ptr(Y),
+                                          _ld(Y), d_in, d_out, st))

@@ -20,7 +20,8 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "liblora.so")
 
-SOURCES = ["build_segments.hip", "shrink_expand.hip", "gemm.hip", "gemm_mx.hip", "pack_slot.hip", "dora.hip",
+SOURCES = ["build_segments.hip", "shrink_expand.hip", "gemm.hip", "gemm_mx.hip", "mx_product.hip",
+           "pack_slot.hip", "dora.hip",
            "static_scratch.hip", "mxfp4.hip", "experts.hip", "lora_api.cpp"]
 ARCH = os.environ.get("LORA_OFFLOAD_ARCH", "gfx950")
 

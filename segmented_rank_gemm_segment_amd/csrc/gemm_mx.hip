@@ -34,6 +34,8 @@ hipError_t launch_gemm_mx(const void *X, int64_t ldx, const void *W, int64_t ldw
                           const float *H, const SegView *seg, const PoolView *pool,
                           hipStream_t stream) {
   const bool lora = seg != nullptr;
+  if (mx.x && M > LORA_GEMM_SMALL_M && !mid_tiles(M, N))
+    return launch_mx_product(X, ldx, W, ldw, mx, Y, ldy, M, K, N, stream);
   if (mx.x) {
     // both operands in units of four codes
     GemmArgs g = gemm_args(X, ldx / 2, W, ldw / 2, Y, ldy, M, K / 4, N, nullptr, nullptr, nullptr);

@@ -34,6 +34,10 @@ __device__ __forceinline__ void dma16_s(uint32_t m0, uint32_t off, const void *b
                : "memory", "m0");
 }
 
+__device__ __forceinline__ void dma4_s(uint32_t m0, uint32_t off, const void *base) {
+  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dword %1, %2" ::"s"(m0), "v"(off), "s"(base)
+               : "memory", "m0");
+}
 // One dword per lane: 64 lanes x 4 bytes into 256 bytes of LDS.
 __device__ __forceinline__ void dma4(uint32_t m0, const void *src) {
   asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dword %1, off" ::"s"(m0), "v"(src)

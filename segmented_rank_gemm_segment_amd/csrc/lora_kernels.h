@@ -131,6 +131,11 @@ hipError_t launch_gemm_mx(const void *X, int64_t ldx, const void *W, int64_t ldw
                           const float *H, const SegView *seg, const PoolView *pool,
                           hipStream_t stream);
 
+// Both operands MXFP4, large batches.
+hipError_t launch_mx_product(const void *X, int64_t ldx, const void *W, int64_t ldw,
+                             const MxScales &mx, void *Y, int64_t ldy, int M, int K, int N,
+                             hipStream_t stream);
+
 // Y[p] = X[row of p] W_e^T for every sorted row p of every expert e.
 hipError_t launch_experts_gemm_mx(const void *X, int64_t ldx, const ExpertView &ex, const void *W,
                                   int64_t ldw, const MxScales &mx, void *Y, int64_t ldy, int K,

@@ -1,0 +1,340 @@
+// Y = dq(Xq) dq(Wq)^T, both operands MXFP4, large batches: codes and scales go
+// to v_mfma_scale_f32_32x32x64_f8f6f4 as they are.
+//
+// At 8.6 PFLOP/s (the rate of a loop of these MFMAs on registers alone) a
+// 256 x 256 tile takes 1.2 thousand cycles for 128 codes of K and needs 34 KB of
+// operands for them, so the kernel lives from keeping the loads ahead:
+// * a ring of four buffers of 128 codes of K (64-byte rows, 16-byte chunks
+//   XOR-swizzled so 16 lanes' reads hit 16 bank groups), filled by direct
+//   global -> LDS loads up to four stages ahead; scales go into a ring of their
+//   own, four words a row at once where alignment allows (a word a row costs as
+//   many cache lookups as 64 bytes of codes: 671 us against 601);
+// * every wave issues the same number of loads per stage and loads complete in
+//   order, so "stage kt + 1 has landed" is vmcnt at most the loads of the stages
+//   behind it; one barrier per stage publishes it and frees a buffer;
+// * workgroups are persistent, one per CU, and the ring runs on from one tile
+//   into the next: the next tile's first stages are on their way while this
+//   tile's last products and its stores run.
+// W is the MFMA's row operand and X its column operand, so a lane ends up with
+// one row of Y and runs of columns; two lanes swap halves (v_permlane32_swap)
+// and each stores 16 bytes, without LDS, which the ring keeps.
+// 16943 x 4096 x 14336: 601 us, 3.3 PFLOP/s; the matrix pipe is 40% busy.  The
+// loads alone take 305 us (64-byte row pieces use half of each 128-byte line),
+// the products alone 283.
+#include "lds_dma.cuh"
+#include "lora_device.cuh"
+#include "lora_kernels.h"
+
+namespace lora {
+namespace {
+
+struct MxGemmArgs {
+  const unsigned char *X, *SX, *W, *SW;   // codes and scales
+  int64_t ldx, ldsx, ldw, ldsw;           // bytes a row
+  bf16_t *Y;
+  int64_t ldy;
+  int M, K, N;
+};
+
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+
+constexpr int kProductCUs = 256;
+constexpr int kProductGroup = 8;   // M-tiles per group of the tile order
+
+// SEL: the scale words' byte of this product's block (lds_dma.cuh's fragment
+// layout: lane l holds row l % 32, codes [32 (l / 32), +32) of 64).
+template <int SEL>
+__device__ __forceinline__ f32x16 mfma_mx4(u32x4 a, u32x4 b, f32x16 c, uint32_t sa, uint32_t sb) {
+  const i32x8 av = {(int)a[0], (int)a[1], (int)a[2], (int)a[3], 0, 0, 0, 0};
+  const i32x8 bv = {(int)b[0], (int)b[1], (int)b[2], (int)b[3], 0, 0, 0, 0};
+  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(av, bv, c, 4, 4, SEL, (int)sa, SEL,
+                                                         (int)sb);
+}
+
+// Tile t of the order: groups of kProductGroup M-tiles, each sweeping N.
+__device__ __forceinline__ void tile_at(int t, int tiles_m, int tiles_n, int &mi, int &ni) {
+  const int grp = t / (kProductGroup * tiles_n), first = grp * kProductGroup;
+  const int cnt = min(kProductGroup, tiles_m - first);
+  const int in = t - grp * kProductGroup * tiles_n;
+  mi = first + in % cnt;
+  ni = in / cnt;
+}
+
+// WIDE: a load of the scales takes four words a row and serves four stages.
+template <int BM, int BN, int WM, int WN, bool WIDE>
+__global__ __launch_bounds__(WM *WN *kWave) void mx_product_kernel(MxGemmArgs g) {
+  constexpr int NW = WM * WN, TM = BM / WM, TN = BN / WN, FM = TM / 32, FN = TN / 32;
+  constexpr int R = BM + BN;
+  constexpr int STAGES = 4, STAGE = R * 64;
+  constexpr int CI = R / 16 / NW, SI = R / 64 / NW;   // a wave's loads of codes and of scales
+  // scales: loaded every SPER stages into one of SBUFS buffers, SROW bytes a row
+  constexpr int SPER = WIDE ? 4 : 1, SROW = 4 * SPER, SBUFS = WIDE ? 2 : STAGES, SSTAGE = R * SROW;
+  constexpr int PER = CI + (WIDE ? 0 : SI);         // loads a stage has at least
+  static_assert(R % (64 * NW) == 0 && BM % (64 * SI) == 0 && BM % (16 * CI) == 0, "load split");
+  static_assert(STAGES * STAGE + SBUFS * SSTAGE <= 160 * 1024, "LDS");
+  static_assert((STAGES - 1) * PER <= 63, "vmcnt");
+  __shared__ __align__(16) unsigned char smem[STAGES * STAGE + SBUFS * SSTAGE];
+
+  const int tid = threadIdx.x, l = tid & (kWave - 1);
+  const int wid = __builtin_amdgcn_readfirstlane(tid / kWave);
+  const int wm = wid / WN, wn = wid % WN;
+  const int tiles_m = (g.M + BM - 1) / BM, tiles_n = (g.N + BN - 1) / BN;
+  const int tiles = tiles_m * tiles_n;
+  const int KT = (g.K + 127) / 128;
+  const bool ktail = g.K % 128 != 0;
+
+  // XCD x (workgroups x, x + 8, ...) owns the x-th eighth of the tile order and
+  // its workgroups take that in turn.
+  const int per = (tiles + 7) / 8, xcd = blockIdx.x & 7, stride = gridDim.x / 8;
+  const int t_end = min(tiles, (xcd + 1) * per);
+  int t_issue = xcd * per + blockIdx.x / 8;
+  if (t_issue >= t_end) return;
+
+  // Loads of this wave: rows [16 CI wid, 16 CI (wid + 1)) of the stage's X and W
+  // rows, so all of one operand (and the scales of rows [64 SI wid, ...)).
+  const uint32_t sbase = lds_offset(smem);
+  const bool isx = wid * CI * 16 < BM, isxs = wid * SI * 64 < BM;
+  const unsigned char *const op = isx ? g.X : g.W, *const sop = isxs ? g.SX : g.SW;
+  const int64_t ldo = isx ? g.ldx : g.ldw, ldso = isxs ? g.ldsx : g.ldsw;
+  const int row0 = wid * CI * 16 - (isx ? 0 : BM), srow0 = wid * SI * 64 - (isxs ? 0 : BM);
+  const unsigned char *base = nullptr, *bases = nullptr;
+  uint32_t off[CI], soff[SI];
+  auto chunk = [&](int i) { return (l & 3) ^ ((((wid * CI + i) * 16 + l / 4) >> 2) & 3); };
+  auto aim = [&](int t) __attribute__((always_inline)) {
+    int mi, ni;
+    tile_at(t, tiles_m, tiles_n, mi, ni);
+    const int first = isx ? mi * BM : ni * BN, last = (isx ? g.M : g.N) - 1;
+    base = op + (int64_t)first * ldo;
+#pragma unroll
+    for (int i = 0; i < CI; ++i)
+      off[i] = (uint32_t)((min(first + row0 + i * 16 + l / 4, last) - first) * (int)ldo) + chunk(i) * 16;
+    const int sfirst = isxs ? mi * BM : ni * BN, slast = (isxs ? g.M : g.N) - 1;
+    bases = sop + (int64_t)sfirst * ldso;
+#pragma unroll
+    for (int i = 0; i < SI; ++i)
+      soff[i] = (uint32_t)((min(sfirst + srow0 + i * 64 + l, slast) - sfirst) * (int)ldso);
+  };
+  // The next stage to issue: stage k_issue of tile t_issue, its scales into
+  // buffer s_issue where a load of them is due.
+  int k_issue = 0, s_issue = 0;
+  auto issue_codes = [&](int i, int buf) __attribute__((always_inline)) {
+    // a chunk past K reads the stage's first chunk (in bounds: it starts
+    // before K) and is zeroed before use
+    uint32_t o = off[i];
+    if (ktail && k_issue == KT - 1 && k_issue * 128 + chunk(i) * 32 >= g.K) o -= chunk(i) * 16;
+    dma16_s(__builtin_amdgcn_readfirstlane(sbase + buf * STAGE + (wid * CI + i) * 1024), o,
+            base + (int64_t)k_issue * 64);
+  };
+  auto issue_scales = [&]() __attribute__((always_inline)) {
+    if (k_issue % SPER) return;
+#pragma unroll
+    for (int i = 0; i < SI; ++i) {
+      const uint32_t dst = __builtin_amdgcn_readfirstlane(sbase + STAGES * STAGE + s_issue * SSTAGE +
+                                                          (wid * SI + i) * 64 * SROW);
+      if constexpr (WIDE)
+        dma16_s(dst, soff[i], bases + (int64_t)k_issue * 4);
+      else
+        dma4_s(dst, soff[i], bases + (int64_t)k_issue * 4);
+    }
+    s_issue = s_issue + 1 == SBUFS ? 0 : s_issue + 1;
+  };
+  auto advance = [&]() __attribute__((always_inline)) {
+    if (++k_issue == KT) {
+      k_issue = 0;
+      t_issue += stride;
+      if (t_issue < t_end) aim(t_issue);
+    }
+  };
+  // the stage in buf reaches past K: its chunks there to zero, their scales to
+  // 1 (a NaN would spoil them; WIDE rows have no tail)
+  auto zero_tail = [&](int buf) {
+    unsigned char *st = smem + buf * STAGE;
+#pragma unroll
+    for (int i = 0; i < CI; ++i)
+      if ((KT - 1) * 128 + chunk(i) * 32 >= g.K)
+        *reinterpret_cast<u32x4 *>(st + (wid * CI + i) * 1024 + l * 16) = u32x4{0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < SI; ++i) {
+      uint32_t *p = reinterpret_cast<uint32_t *>(smem + STAGES * STAGE + buf * SSTAGE +
+                                                 (wid * SI + i) * 256 + l * 4);
+      const uint32_t keep = ~0u >> (32 - 8 * (g.K / 32 - (KT - 1) * 4));   // 1..3 blocks
+      *p = (*p & keep) | (0x7f7f7f7fu & ~keep);
+    }
+  };
+
+  int t = t_issue;
+  aim(t);
+  int ahead = 0;                                    // stages issued and not yet waited for
+#pragma unroll
+  for (int s = 0; s < STAGES; ++s)
+    if (t_issue < t_end) {
+      issue_scales();
+#pragma unroll
+      for (int i = 0; i < CI; ++i) issue_codes(i, s);
+      advance();
+      ++ahead;
+    }
+
+  // Wait until the oldest of the `ahead` stages in flight has landed: loads
+  // complete in order, so at most the later stages' are left.  (Those may have
+  // a load of scales beside PER, and stores may be behind them: then this waits
+  // for a little more.)
+  auto wait_oldest = [&]() __attribute__((always_inline)) {
+    if (ahead >= STAGES)
+      vm_wait<(STAGES - 1) * PER>();
+    else if (ahead == STAGES - 1)
+      vm_wait<(STAGES - 2) * PER>();
+    else
+      vm_wait<0>();
+    --ahead;
+  };
+
+  // fragment offsets in a stage
+  const int arow = (BM + wn * TN + (l & 31)) * 64, brow = (wm * TM + (l & 31)) * 64;
+  int co[2];
+#pragma unroll
+  for (int s = 0; s < 2; ++s) co[s] = ((2 * s + (l >> 5)) ^ ((l >> 2) & 3)) * 16;
+  const int asc = STAGES * STAGE + (BM + wn * TN + (l & 31)) * SROW;
+  const int bsc = STAGES * STAGE + (wm * TM + (l & 31)) * SROW;
+  const int sh = (l >> 5) * 8;
+
+  f32x16 acc[FN][FM];
+  u32x4 a[2][FN], b[2][FM];
+  uint32_t sa[FN], sb[FM];
+  auto zero_acc = [&]() __attribute__((always_inline)) {
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int v = 0; v < 16; ++v) acc[j][i][v] = 0.f;
+  };
+  auto read = [&](int to, const unsigned char *st, int s) __attribute__((always_inline)) {
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+      a[to][j] = *reinterpret_cast<const u32x4 *>(st + arow + j * 32 * 64 + co[s]);
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+      b[to][i] = *reinterpret_cast<const u32x4 *>(st + brow + i * 32 * 64 + co[s]);
+  };
+  // the next stage's scale words, in order
+  int s_read = 0, w_read = 0;
+  auto read_scales = [&]() __attribute__((always_inline)) {
+    const unsigned char *st = smem + s_read * SSTAGE + w_read * 4;
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+      sa[j] = *reinterpret_cast<const uint32_t *>(st + asc + j * 32 * SROW) >> sh;
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+      sb[i] = *reinterpret_cast<const uint32_t *>(st + bsc + i * 32 * SROW) >> sh;
+    if (++w_read == SPER) {
+      w_read = 0;
+      s_read = s_read + 1 == SBUFS ? 0 : s_read + 1;
+    }
+  };
+
+  int buf = 0, kt = 0;
+  wait_oldest();
+  if (ktail && KT == 1) zero_tail(0);
+  lgkm_barrier();
+  read_scales();
+  read(0, smem, 0);
+  zero_acc();
+  while (true) {
+    const unsigned char *st = smem + buf * STAGE;
+    read(1, st, 1);
+#pragma unroll
+    for (int q = 0; q < FN * FM; ++q) {
+      acc[q / FM][q % FM] = mfma_mx4<0>(a[0][q / FM], b[0][q % FM], acc[q / FM][q % FM], sa[q / FM], sb[q % FM]);
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      if (q < FN + FM) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+    }
+    const int nbuf = buf + 1 == STAGES ? 0 : buf + 1;
+    const bool last = kt + 1 == KT;
+    const bool more = !last || t + stride < t_end;
+    if (more) {
+      wait_oldest();
+      if (ktail && (last ? KT == 1 : kt + 2 == KT)) zero_tail(nbuf);
+      lgkm_barrier();                               // stage kt + 1 is there, stage kt has been read
+    }
+    // The second half's products take their scales first: the words of stage
+    // kt + 1 (after the last stage: of a settled buffer, unused) replace them.
+    uint32_t na[FN], nb[FM];
+#pragma unroll
+    for (int j = 0; j < FN; ++j) na[j] = sa[j];
+#pragma unroll
+    for (int i = 0; i < FM; ++i) nb[i] = sb[i];
+    read_scales();
+    read(0, smem + nbuf * STAGE, 0);
+    auto second = [&](int q) __attribute__((always_inline)) {
+      acc[q / FM][q % FM] = mfma_mx4<2>(a[1][q / FM], b[1][q % FM], acc[q / FM][q % FM], na[q / FM], nb[q % FM]);
+    };
+    // with the refill of stage kt's buffer, a load between products
+    if (more && t_issue < t_end) {
+      issue_scales();
+      __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+      for (int q = 0; q < FN * FM || q < CI; ++q) {
+        if (q < CI) issue_codes(q, buf);
+        if (q < FN * FM) second(q);
+        __builtin_amdgcn_sched_barrier(0);          // in this order
+      }
+      __builtin_amdgcn_s_setprio(0);
+      advance();
+      ++ahead;
+    } else {
+#pragma unroll
+      for (int q = 0; q < FN * FM; ++q) second(q);
+    }
+    buf = nbuf;
+    if (!last) {
+      ++kt;
+      continue;
+    }
+    // the tile's rows: lane l has row wm TM + 32 i + l % 32 and, of each 32
+    // columns, [8 v + 4 (l / 32), +4) in accumulator entries [4 v, 4 v + 4)
+    int mi, ni;
+    tile_at(t, tiles_m, tiles_n, mi, ni);
+    const int n0 = ni * BN + wn * TN + (l >> 5) * 8;
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+      const int row = mi * BM + wm * TM + i * 32 + (l & 31);
+      bf16_t *y = g.Y + (int64_t)row * g.ldy;
+#pragma unroll
+      for (int j = 0; j < FN; ++j)
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          const f32x16 c = acc[j][i];
+          uint32_t lo0 = pack_bf16x2(c[8 * p], c[8 * p + 1]), lo1 = pack_bf16x2(c[8 * p + 2], c[8 * p + 3]);
+          uint32_t hi0 = pack_bf16x2(c[8 * p + 4], c[8 * p + 5]), hi1 = pack_bf16x2(c[8 * p + 6], c[8 * p + 7]);
+          // lower lanes' second quad against upper lanes' first: 8 columns each
+          const auto s0 = __builtin_amdgcn_permlane32_swap(lo0, hi0, false, false);
+          const auto s1 = __builtin_amdgcn_permlane32_swap(lo1, hi1, false, false);
+          const int col = n0 + j * 32 + p * 16;
+          if (row < g.M && col < g.N)               // N % 8 == 0: all 8 columns or none
+            stg16(y + col, make_uint4(s0[0], s1[0], s0[1], s1[1]));
+        }
+    }
+    if (!more) break;
+    t += stride;
+    kt = 0;
+    zero_acc();
+  }
+}
+
+}  // namespace
+
+hipError_t launch_mx_product(const void *X, int64_t ldx, const void *W, int64_t ldw,
+                             const MxScales &mx, void *Y, int64_t ldy, int M, int K, int N,
+                             hipStream_t stream) {
+  const MxGemmArgs g{(const unsigned char *)X, mx.x, (const unsigned char *)W, mx.w,
+                     ldx, mx.ldx, ldw, mx.ldw, (bf16_t *)Y, ldy, M, K, N};
+  // four scale words at a time where every row's are whole and aligned to that
+  if (K % 512 == 0 && mx.ldx % 16 == 0 && mx.ldw % 16 == 0)
+    hipLaunchKernelGGL((mx_product_kernel<256, 256, 4, 2, true>), dim3(kProductCUs), dim3(512), 0, stream, g);
+  else
+    hipLaunchKernelGGL((mx_product_kernel<256, 256, 4, 2, false>), dim3(kProductCUs), dim3(512), 0, stream, g);
+  return hipGetLastError();
+}
+
+}  // namespace lora

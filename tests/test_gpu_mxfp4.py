@@ -109,7 +109,7 @@ def test_dequantize_every_code_and_scale(dtype):
     with np.errstate(over="ignore"):
         want = oracle.decode_mxfp4(codes, scales)
         # rows of values past the type's range: the type's largest is below 2^128
-        want = np.where(np.abs(want) >= 2.0 ** 128, np.sign(want) * np.inf, want)
+        want[np.abs(want) >= 2.0 ** 128] *= np.inf
     assert np.array_equal(out.double().cpu().numpy(), want, equal_nan=True)
 
 
@@ -163,6 +163,31 @@ def test_both_operands_product(n, d_in, d_out):
     Y64 = X64 @ W64.T
     check_close(out[:n, :d_out], Y64, product_tol(X64, W64, Y64), f"both {n, d_in, d_out}")
     assert bool((out[n] == 7.0).all()) and bool((out[:, d_out:] == 7.0).all())
+
+
+@pytest.mark.parametrize("n,d_in,d_out", [
+    (2100, 512, 8200), (2100, 1536, 8200), (2100, 96, 8200), (2100, 640, 8200), (4200, 1024, 4104),
+    (8200, 512, 256), (700, 2560, 136), (60, 1024, 72)])
+@pytest.mark.parametrize("pad", [0, 12])
+def test_both_operands_many_tiles(n, d_in, d_out, pad):
+    """More output tiles than compute units, scale rows with and without 16-byte
+    alignment, and K of one to many stages; every element."""
+    xc, xs = wl.make_mxfp4(n + 1, n, d_in, 124, 130)
+    wc, wsc = wl.make_mxfp4(d_out, d_out, d_in)
+    dev = []
+    for c, s in ((xc, xs), (wc, wsc)):
+        q = torch.from_numpy(c).to(DEV)
+        sp = torch.full((len(s), (s.shape[1] + 15) // 16 * 16 + pad), 255, dtype=torch.uint8, device=DEV)
+        sp[:, :s.shape[1]] = torch.from_numpy(s).to(DEV)
+        dev += [q, sp[:, :s.shape[1]]]
+    out = torch.full((n + 1, d_out + 8), 7.0, dtype=torch.bfloat16, device=DEV)
+    srg.lora_base_gemm_mxfp4(*dev, out[:n, :d_out])
+    assert bool((out[n] == 7.0).all()) and bool((out[:, d_out:] == 7.0).all())
+    X64 = torch.from_numpy(oracle.decode_mxfp4(xc, xs)).to(DEV)
+    W64 = torch.from_numpy(oracle.decode_mxfp4(wc, wsc)).to(DEV)
+    Y64 = X64 @ W64.t()
+    tol = 2.0 ** -8 * Y64.abs() + d_in * U * (X64.abs() @ W64.abs().t())
+    assert bool(((out[:n, :d_out].double() - Y64).abs() <= tol).all())
 
 
 LORA_CASES = [
