@@ -21,8 +21,8 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "liblora.so")
 
 SOURCES = ["build_segments.hip", "shrink_expand.hip", "gemm.hip", "gemm_mx.hip", "mx_product.hip",
-           "pack_slot.hip", "dora.hip",
-           "static_scratch.hip", "mxfp4.hip", "experts.hip", "lora_api.cpp"]
+           "pack_slot.hip", "dora.hip", "static_scratch.hip", "mxfp4.hip", "experts.hip",
+           "lora_api.cpp"]
 ARCH = os.environ.get("LORA_OFFLOAD_ARCH", "gfx950")
 
 COMMON = ["-O3", "-std=c++17", "-fPIC", "-Wall", "-Wno-unused-function", "-Wno-inline-asm",

@@ -1,7 +1,7 @@
 // Launches of the products with MXFP4 operands (the MFMA tiles of
 // gemm_tile.cuh): an MXFP4 weight under bf16 activations, with or without the
 // LoRA term, both operands MXFP4, and the experts' product.
-#include "gemm_tile.cuh"
+#include "mx_stream.cuh"
 
 namespace lora {
 namespace {
@@ -49,6 +49,7 @@ hipError_t launch_gemm_mx(const void *X, int64_t ldx, const void *W, int64_t ldw
   }
   GemmArgs g = gemm_args(X, ldx, W, ldw * 2, Y, ldy, M, K, N, H, seg, pool);
   g.mx = mx;
+  if (M <= kStreamRows) return launch_mx_stream(g, lora, stream);
   return launch_rows_split(g, lora, [&](const GemmArgs &a) {
     if (a.M <= LORA_GEMM_SMALL_M) return launch_tile<LORA_GEMM_SMALL, kMxW>(a, lora, stream);
     if (mid_tiles(a.M, N)) return launch_tile<LORA_GEMM_MID, kMxW>(a, lora, stream);
@@ -68,7 +69,7 @@ hipError_t launch_experts_gemm_mx(const void *X, int64_t ldx, const ExpertView &
     const int64_t t = (int64_t)ex.n_choices / bm + ex.n_experts;
     return (int)(t < ex.n_choices ? t : ex.n_choices);
   };
-  if (ex.n_choices / ex.n_experts <= 64) return launch_experts<LORA_GEMM_SMALL>(g, tiles(64), stream);
+  if (ex.n_choices / ex.n_experts <= 32) return launch_experts_stream(g, tiles(16), stream);
   return launch_experts<LORA_GEMM_MID>(g, tiles(128), stream);
 }
 
