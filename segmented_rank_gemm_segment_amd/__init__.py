@@ -213,12 +213,14 @@ def _check(code: int) -> None:
         raise LoraError(code, lib().lora_status_str(code).decode())
 
 
+_DTYPE_CODES = {torch.bfloat16: LORA_BF16, torch.float32: LORA_F32}
+
+
 def _dtype_code(t: torch.dtype) -> int:
-    if t == torch.bfloat16:
-        return LORA_BF16
-    if t == torch.float32:
-        return LORA_F32
-    raise ValueError(f"unsupported dtype {t}")
+    code = _DTYPE_CODES.get(t)
+    if code is None:
+        raise ValueError(f"unsupported dtype {t}")
+    return code
 
 
 def _ptr(t: Optional[torch.Tensor]):
@@ -734,7 +736,7 @@ def lora_base_gemm_mxfp4w(X: torch.Tensor, Wq: torch.Tensor, w_scale: torch.Tens
     n, d_in = X.shape
     d_out = Wq.shape[0]
     w = _mxfp4(Wq, w_scale, d_out, d_in, "Wq, w_scale")
-    if tuple(Y.shape) != (n, d_out):
+    if Y.shape != (n, d_out):
         raise ValueError("shapes: X [n, d_in], Wq [d_out, d_in / 2], Y [n, d_out]")
     st = _launch_stream(stream, X, Wq, w_scale, Y)
     _check(lib().lora_base_gemm_mxfp4w(_ptr(X), _ld(X), *w, _ptr(Y), _ld(Y), n, d_in, d_out, st))
@@ -793,35 +795,32 @@ class Experts:
                                self.sorted_choice.data_ptr(), self.choice_position.data_ptr(),
                                self.status.data_ptr(),
                                self.workspace.data_ptr() if ws else None)
-
-    @property
-    def c(self):
-        return ctypes.byref(self._c)
+        self.c = ctypes.byref(self._c)
 
 
 def lora_experts_sort(expert_ids: torch.Tensor, ex: Experts, stream=None) -> None:
     """Choices by expert from the router's ids (int32 [n_tokens, top_k], -1 =
     dropped)."""
-    if expert_ids.dtype != torch.int32 or not expert_ids.is_contiguous() \
-            or tuple(expert_ids.shape) != (ex.n_tokens, ex.top_k):
+    if expert_ids.dtype is not torch.int32 or not expert_ids.is_contiguous() \
+            or expert_ids.shape != (ex.n_tokens, ex.top_k):
         raise ValueError("expert_ids: contiguous int32 [n_tokens, top_k]")
     st = _launch_stream(stream, expert_ids, ex.expert_offsets)
     _check(lib().lora_experts_sort(_ptr(expert_ids), ex.c, st))
 
 
 def _expert_rows(ex: Experts, tokens: torch.Tensor, rows: Optional[torch.Tensor]) -> int:
-    d = tokens.shape[1] if tokens.dim() == 2 else -1
-    if tuple(tokens.shape) != (ex.n_tokens, d) or (
-            rows is not None and tuple(rows.shape) != (ex.n_tokens * ex.top_k, d)):
+    d = tokens.shape[-1]
+    if tokens.shape != (ex.n_tokens, d) or (
+            rows is not None and rows.shape != (ex.n_tokens * ex.top_k, d)):
         raise ValueError("token rows [n_tokens, d] and sorted rows [n_tokens * top_k, d]")
-    if rows is not None and rows.dtype != tokens.dtype:
+    if rows is not None and rows.dtype is not tokens.dtype:
         raise ValueError("token rows and sorted rows must share a dtype")
     return d
 
 
 def _expert_weights(ex: Experts, w: Optional[torch.Tensor], what: str) -> None:
-    if w is not None and (w.dtype != torch.float32 or not w.is_contiguous()
-                          or tuple(w.shape) != (ex.n_tokens, ex.top_k)):
+    if w is not None and (w.dtype is not torch.float32 or not w.is_contiguous()
+                          or w.shape != (ex.n_tokens, ex.top_k)):
         raise ValueError(f"{what}: contiguous float32 [n_tokens, top_k]")
 
 

@@ -11,7 +11,7 @@
 // Rows move in token order (gather, combine and its backward alike): a token's
 // row is read once and its top_k sorted rows are written or read beside it, so
 // each array passes HBM once.  All three are bound by HBM: 16 bytes per lane,
-// a wave per token, or four for batches of few tokens.
+// four waves per token.
 #include "lora_device.cuh"
 #include "lora_kernels.h"
 
@@ -23,6 +23,8 @@ constexpr int kMaxE = LORA_MAX_EXPERTS;
 static_assert(kMaxE <= kSortThreads, "one expert per thread in the scans");
 constexpr int kOneGroupSteps = kExpertOneGroupChoices / kSortThreads;
 constexpr int kBlockChoices = kExpertBlockChoices, kBlockSteps = kBlockChoices / kSortThreads;
+
+constexpr int kScanBlocks = 64;
 
 struct SortArgs {
   const int32_t *ids;
@@ -185,15 +187,40 @@ __global__ __launch_bounds__(kSortThreads) void sort_scan_kernel(SortArgs a, int
   if (threadIdx.x == 0) a.offsets[a.E] = total;
 }
 
+// The block's choices to their places.  SCAN: the counts are still per block;
+// every workgroup sums them itself, and the first writes the experts' rows.
+template <bool SCAN>
 __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortArgs a) {
   __shared__ SortLds L;
   int key[kBlockSteps], rank[kBlockSteps];
   const int base = blockIdx.x * kBlockChoices;
+  const int e = threadIdx.x;
+  int before = 0, all = 0, bad = 0;
+  if constexpr (SCAN) {
+    for (int b = 0; b < (int)gridDim.x; ++b) {
+      const int32_t *c = a.counts + b * (a.E + 1);
+      const int v = e < a.E ? c[e] : 0;
+      before += b < (int)blockIdx.x ? v : 0;
+      all += v;
+      bad += c[a.E];
+    }
+  }
   rank_choices<kBlockSteps>(a, base, L, key, rank);
   wave_bases(a.E, L);
-  if ((int)threadIdx.x < a.E)
-    L.off[threadIdx.x] = a.offsets[threadIdx.x] +
-                         a.counts[(int64_t)blockIdx.x * (a.E + 1) + threadIdx.x];
+  if constexpr (SCAN) {
+    int total;
+    const int at = block_scan(all, L.scan, total);
+    if (e < a.E) L.off[e] = at + before;
+    if (blockIdx.x == 0) {
+      if (e < a.E) a.offsets[e] = at;
+      if (e == 0) {
+        a.offsets[a.E] = total;
+        *a.status = bad;
+      }
+    }
+  } else if (e < a.E) {
+    L.off[e] = a.offsets[e] + a.counts[(int64_t)blockIdx.x * (a.E + 1) + e];
+  }
   __syncthreads();
   place<kBlockSteps>(a, base, L, key, rank);
 }
@@ -245,7 +272,7 @@ __global__ __launch_bounds__(kRowWaves *kWave) void gather_kernel(RowArgs a) {
 
 template <typename T, int WPT>
 __global__ __launch_bounds__(kRowWaves *kWave) void combine_kernel(RowArgs a) {
-  constexpr int V = Elem<T>::kVec;
+  constexpr int V = Elem<T>::kVec, JB = 8;
   int64_t i;
   int part, pos;
   if (!wave_token<WPT>(a, i, part, pos)) return;
@@ -253,14 +280,23 @@ __global__ __launch_bounds__(kRowWaves *kWave) void combine_kernel(RowArgs a) {
   T *y = static_cast<T *>(a.out) + i * a.ldo;
   for (int c = (part * kWave + lane_id()) * V; c < a.d; c += WPT * kWave * V) {
     float o[V] = {};
-    for (int j = 0; j < a.k; ++j) {
-      const int p = __builtin_amdgcn_readlane(pos, j);
-      if (p < 0) continue;
-      const float w = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(wl), j));
-      float v[V];
-      Elem<T>::unpack(ldg16(static_cast<const T *>(a.in) + (int64_t)p * a.ldi + c), v);
+    for (int j0 = 0; j0 < a.k; j0 += JB) {
+      uint4 raw[JB];                    // all of the block's loads before the first use
 #pragma unroll
-      for (int e = 0; e < V; ++e) o[e] = fmaf(w, v[e], o[e]);
+      for (int q = 0; q < JB; ++q) {
+        const int p = j0 + q < a.k ? __builtin_amdgcn_readlane(pos, j0 + q) : -1;
+        if (p >= 0) raw[q] = ldg16(static_cast<const T *>(a.in) + (int64_t)p * a.ldi + c);
+      }
+#pragma unroll
+      for (int q = 0; q < JB; ++q) {
+        const int p = j0 + q < a.k ? __builtin_amdgcn_readlane(pos, j0 + q) : -1;
+        if (p < 0) continue;
+        const float w = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(wl), j0 + q));
+        float v[V];
+        Elem<T>::unpack(raw[q], v);
+#pragma unroll
+        for (int e = 0; e < V; ++e) o[e] = fmaf(w, v[e], o[e]);
+      }
     }
     stg16(y + c, Elem<T>::pack(o));
   }
@@ -280,14 +316,21 @@ __global__ __launch_bounds__(kRowWaves *kWave) void combine_backward_kernel(RowA
     float dot[JB] = {};
     for (int c = (part * kWave + lane_id()) * V; c < a.d; c += WPT * kWave * V) {
       float g[V];
-      Elem<T>::unpack(ldg16(dy + c), g);
+      const uint4 graw = ldg16(dy + c);
+      uint4 raw[JB];                    // all of the block's loads before the first use
+#pragma unroll
+      for (int q = 0; q < JB; ++q) {
+        const int p = j0 + q < a.k ? __builtin_amdgcn_readlane(pos, j0 + q) : -1;
+        if (p >= 0 && a.dw) raw[q] = ldg16(static_cast<const T *>(a.in2) + (int64_t)p * a.ldi2 + c);
+      }
+      Elem<T>::unpack(graw, g);
 #pragma unroll
       for (int q = 0; q < JB; ++q) {
         const int p = j0 + q < a.k ? __builtin_amdgcn_readlane(pos, j0 + q) : -1;
         if (p < 0) continue;
         if (a.dw) {
           float v[V];
-          Elem<T>::unpack(ldg16(static_cast<const T *>(a.in2) + (int64_t)p * a.ldi2 + c), v);
+          Elem<T>::unpack(raw[q], v);
 #pragma unroll
           for (int e = 0; e < V; ++e) dot[q] = fmaf(g[e], v[e], dot[q]);
         }
@@ -323,18 +366,21 @@ __global__ __launch_bounds__(kRowWaves *kWave) void combine_backward_kernel(RowA
   }
 }
 
-// Batches of fewer tokens than this give each four waves, so that a decode
-// batch still fills the CUs.
-constexpr int kWideTokens = 4096;
+// A token's row takes four waves, or one where that holds it in one step
+// (16384 tokens x 4 of 8 KB: combine in 141 us with four waves, 157 with one).
+template <typename T>
+bool one_wave(int d) {
+  return d <= kWave * Elem<T>::kVec;
+}
 
-template <template <typename, int> class Launch, typename... A>
-void by_type(int dtype, int n, A... args) {
+template <template <typename, int> class Launch>
+void by_type(int dtype, const RowArgs &a, hipStream_t s) {
   if (dtype == LORA_BF16) {
-    if (n < kWideTokens) Launch<bf16_t, 4>::go(args...);
-    else Launch<bf16_t, 1>::go(args...);
+    if (one_wave<bf16_t>(a.d)) Launch<bf16_t, 1>::go(a, s);
+    else Launch<bf16_t, 4>::go(a, s);
   } else {
-    if (n < kWideTokens) Launch<float, 4>::go(args...);
-    else Launch<float, 1>::go(args...);
+    if (one_wave<float>(a.d)) Launch<float, 1>::go(a, s);
+    else Launch<float, 4>::go(a, s);
   }
 }
 template <int WPT>
@@ -342,17 +388,17 @@ dim3 row_grid(int n) {
   return dim3((unsigned)(((int64_t)n * WPT + kRowWaves - 1) / kRowWaves));
 }
 template <typename T, int WPT> struct Gather {
-  static void go(RowArgs a, hipStream_t s) {
+  static void go(const RowArgs &a, hipStream_t s) {
     hipLaunchKernelGGL((gather_kernel<T, WPT>), row_grid<WPT>(a.n), dim3(kRowWaves * kWave), 0, s, a);
   }
 };
 template <typename T, int WPT> struct Combine {
-  static void go(RowArgs a, hipStream_t s) {
+  static void go(const RowArgs &a, hipStream_t s) {
     hipLaunchKernelGGL((combine_kernel<T, WPT>), row_grid<WPT>(a.n), dim3(kRowWaves * kWave), 0, s, a);
   }
 };
 template <typename T, int WPT> struct CombineBackward {
-  static void go(RowArgs a, hipStream_t s) {
+  static void go(const RowArgs &a, hipStream_t s) {
     hipLaunchKernelGGL((combine_backward_kernel<T, WPT>), row_grid<WPT>(a.n),
                        dim3(kRowWaves * kWave), 0, s, a);
   }
@@ -372,15 +418,21 @@ hipError_t launch_experts_sort(const int32_t *ids, int n_choices, int n_experts,
   } else {
     const int blocks = expert_blocks(n_choices);
     hipLaunchKernelGGL(sort_count_kernel, dim3(blocks), block, 0, stream, a);
-    hipLaunchKernelGGL(sort_scan_kernel, dim3(1), block, 0, stream, a, blocks);
-    hipLaunchKernelGGL(sort_place_kernel, dim3(blocks), block, 0, stream, a);
+    // one launch less while every workgroup can read all blocks' counts
+    // (65536 choices, 64 experts: 17 us against 19 and a launch)
+    if (blocks <= kScanBlocks) {
+      hipLaunchKernelGGL(sort_place_kernel<true>, dim3(blocks), block, 0, stream, a);
+    } else {
+      hipLaunchKernelGGL(sort_scan_kernel, dim3(1), block, 0, stream, a, blocks);
+      hipLaunchKernelGGL(sort_place_kernel<false>, dim3(blocks), block, 0, stream, a);
+    }
   }
   return hipGetLastError();
 }
 
 hipError_t launch_experts_gather(const void *X, int64_t ldx, const int32_t *position, int n, int k,
                                  int d, int dtype, void *Xs, int64_t lds, hipStream_t stream) {
-  by_type<Gather>(dtype, n, RowArgs{n, k, d, position, X, ldx, nullptr, 0, nullptr, Xs, lds, nullptr},
+  by_type<Gather>(dtype, RowArgs{n, k, d, position, X, ldx, nullptr, 0, nullptr, Xs, lds, nullptr},
                   stream);
   return hipGetLastError();
 }
@@ -388,7 +440,7 @@ hipError_t launch_experts_gather(const void *X, int64_t ldx, const int32_t *posi
 hipError_t launch_experts_combine(const void *Ys, int64_t lds, const float *w,
                                   const int32_t *position, int n, int k, int d, int dtype, void *Y,
                                   int64_t ldy, hipStream_t stream) {
-  by_type<Combine>(dtype, n, RowArgs{n, k, d, position, Ys, lds, nullptr, 0, w, Y, ldy, nullptr},
+  by_type<Combine>(dtype, RowArgs{n, k, d, position, Ys, lds, nullptr, 0, w, Y, ldy, nullptr},
                    stream);
   return hipGetLastError();
 }
@@ -397,7 +449,7 @@ hipError_t launch_experts_combine_backward(const void *dY, int64_t ldy, const vo
                                            const float *w, const int32_t *position, int n, int k,
                                            int d, int dtype, void *dYs, int64_t ldds, float *dw,
                                            hipStream_t stream) {
-  by_type<CombineBackward>(dtype, n, RowArgs{n, k, d, position, dY, ldy, Ys, lds, w, dYs, ldds, dw},
+  by_type<CombineBackward>(dtype, RowArgs{n, k, d, position, dY, ldy, Ys, lds, w, dYs, ldds, dw},
                            stream);
   return hipGetLastError();
 }

@@ -70,6 +70,7 @@ hipError_t launch_experts_gemm_mx(const void *X, int64_t ldx, const ExpertView &
     return (int)(t < ex.n_choices ? t : ex.n_choices);
   };
   if (ex.n_choices / ex.n_experts <= 32) return launch_experts_stream(g, tiles(16), stream);
+  if (ex.n_choices / ex.n_experts >= 512) return launch_experts<LORA_GEMM_LARGE>(g, tiles(256), stream);
   return launch_experts<LORA_GEMM_MID>(g, tiles(128), stream);
 }
 

@@ -62,6 +62,7 @@ SORTS = [
     (64, 8, 128, "skewed"), (63, 2, 1024, "uniform"), (512, 2, 1, "one"), (513, 2, 1000, "bad"),
     (1000, 8, 64, "skewed"), (1024, 8, 1024, "bad"), (1025, 8, 33, "uniform"), (3000, 3, 17, "none"),
     (20000, 4, 256, "skewed"), (16384, 8, 1024, "bad"), (50000, 1, 2, "one"),
+    (262145, 1, 7, "skewed"), (270000, 1, 1024, "bad"),
 ]
 
 
