@@ -6,21 +6,24 @@
 // operands for them, so the kernel lives from keeping the loads ahead:
 // * a ring of four buffers of 128 codes of K (64-byte rows, 16-byte chunks
 //   XOR-swizzled so 16 lanes' reads hit 16 bank groups), filled by direct
-//   global -> LDS loads up to four stages ahead; scales go into a ring of their
-//   own, four words a row at once where alignment allows (a word a row costs as
-//   many cache lookups as 64 bytes of codes: 671 us against 601);
+//   global -> LDS loads three stages ahead; scales go into a ring of their own,
+//   four words a row at once where alignment allows (a word a row costs as many
+//   cache lookups as 64 bytes of codes: 671 us against 601);
 // * every wave issues the same number of loads per stage and loads complete in
-//   order, so "stage kt + 1 has landed" is vmcnt at most the loads of the stages
-//   behind it; one barrier per stage publishes it and frees a buffer;
+//   order, so "stage kt + 1 has landed" is vmcnt at most the loads issued after
+//   its; one barrier per stage publishes it and frees a buffer;
+// * a load between every few products: issued together behind the barrier they
+//   filled the load queue and held up the products (601 us against 541);
 // * workgroups are persistent, one per CU, and the ring runs on from one tile
 //   into the next: the next tile's first stages are on their way while this
 //   tile's last products and its stores run.
 // W is the MFMA's row operand and X its column operand, so a lane ends up with
 // one row of Y and runs of columns; two lanes swap halves (v_permlane32_swap)
 // and each stores 16 bytes, without LDS, which the ring keeps.
-// 16943 x 4096 x 14336: 601 us, 3.3 PFLOP/s; the matrix pipe is 40% busy.  The
-// loads alone take 305 us (64-byte row pieces use half of each 128-byte line),
-// the products alone 283.
+// 16943 x 4096 x 14336: 541 us, 3.7 PFLOP/s; 8192^3: 273 us, 4.0 PFLOP/s.  The
+// matrix pipe is 48% busy, at 1.84 GHz: the clock falls as it gets busier (1.97
+// GHz at 40%).  The loads alone take 305 us (64-byte row pieces use half of each
+// 128-byte line), the products alone 283, the stores 100.
 #include "lds_dma.cuh"
 #include "lora_device.cuh"
 #include "lora_kernels.h"
@@ -72,7 +75,7 @@ __global__ __launch_bounds__(WM *WN *kWave) void mx_product_kernel(MxGemmArgs g)
   constexpr int PER = CI + (WIDE ? 0 : SI);         // loads a stage has at least
   static_assert(R % (64 * NW) == 0 && BM % (64 * SI) == 0 && BM % (16 * CI) == 0, "load split");
   static_assert(STAGES * STAGE + SBUFS * SSTAGE <= 160 * 1024, "LDS");
-  static_assert((STAGES - 1) * PER <= 63, "vmcnt");
+  static_assert((STAGES - 1) * PER <= 63 && CI <= 4, "vmcnt, places for the loads");
   __shared__ __align__(16) unsigned char smem[STAGES * STAGE + SBUFS * SSTAGE];
 
   const int tid = threadIdx.x, l = tid & (kWave - 1);
@@ -141,8 +144,8 @@ __global__ __launch_bounds__(WM *WN *kWave) void mx_product_kernel(MxGemmArgs g)
   auto advance = [&]() __attribute__((always_inline)) {
     if (++k_issue == KT) {
       k_issue = 0;
-      t_issue += stride;
-      if (t_issue < t_end) aim(t_issue);
+      // past the last tile the ring goes round on that one, unread
+      if (t_issue + stride < t_end) aim(t_issue += stride);
     }
   };
   // the stage in buf reaches past K: its chunks there to zero, their scales to
@@ -164,30 +167,13 @@ __global__ __launch_bounds__(WM *WN *kWave) void mx_product_kernel(MxGemmArgs g)
 
   int t = t_issue;
   aim(t);
-  int ahead = 0;                                    // stages issued and not yet waited for
 #pragma unroll
-  for (int s = 0; s < STAGES; ++s)
-    if (t_issue < t_end) {
-      issue_scales();
+  for (int s = 0; s < STAGES - 1; ++s) {
+    issue_scales();
 #pragma unroll
-      for (int i = 0; i < CI; ++i) issue_codes(i, s);
-      advance();
-      ++ahead;
-    }
-
-  // Wait until the oldest of the `ahead` stages in flight has landed: loads
-  // complete in order, so at most the later stages' are left.  (Those may have
-  // a load of scales beside PER, and stores may be behind them: then this waits
-  // for a little more.)
-  auto wait_oldest = [&]() __attribute__((always_inline)) {
-    if (ahead >= STAGES)
-      vm_wait<(STAGES - 1) * PER>();
-    else if (ahead == STAGES - 1)
-      vm_wait<(STAGES - 2) * PER>();
-    else
-      vm_wait<0>();
-    --ahead;
-  };
+    for (int i = 0; i < CI; ++i) issue_codes(i, s);
+    advance();
+  }
 
   // fragment offsets in a stage
   const int arow = (BM + wn * TN + (l & 31)) * 64, brow = (wm * TM + (l & 31)) * 64;
@@ -200,7 +186,7 @@ __global__ __launch_bounds__(WM *WN *kWave) void mx_product_kernel(MxGemmArgs g)
 
   f32x16 acc[FN][FM];
   u32x4 a[2][FN], b[2][FM];
-  uint32_t sa[FN], sb[FM];
+  uint32_t sa[FN], sb[FM], ra[FN], rb[FM];          // the stage's scales, the next one's words
   auto zero_acc = [&]() __attribute__((always_inline)) {
 #pragma unroll
     for (int j = 0; j < FN; ++j)
@@ -209,13 +195,19 @@ __global__ __launch_bounds__(WM *WN *kWave) void mx_product_kernel(MxGemmArgs g)
 #pragma unroll
         for (int v = 0; v < 16; ++v) acc[j][i][v] = 0.f;
   };
-  auto read = [&](int to, const unsigned char *st, int s) __attribute__((always_inline)) {
+  // the products so far, here and not where their sums are next looked at
+  auto pin = [&]() __attribute__((always_inline)) {
 #pragma unroll
     for (int j = 0; j < FN; ++j)
-      a[to][j] = *reinterpret_cast<const u32x4 *>(st + arow + j * 32 * 64 + co[s]);
 #pragma unroll
-    for (int i = 0; i < FM; ++i)
-      b[to][i] = *reinterpret_cast<const u32x4 *>(st + brow + i * 32 * 64 + co[s]);
+      for (int i = 0; i < FM; ++i) asm volatile("" : "+v"(acc[j][i]));
+  };
+  // fragment q of half step s of the stage at st
+  auto read1 = [&](int q, const unsigned char *st, int s) __attribute__((always_inline)) {
+    if (q < FN)
+      a[s][q] = *reinterpret_cast<const u32x4 *>(st + arow + q * 32 * 64 + co[s]);
+    else
+      b[s][q - FN] = *reinterpret_cast<const u32x4 *>(st + brow + (q - FN) * 32 * 64 + co[s]);
   };
   // the next stage's scale words, in order
   int s_read = 0, w_read = 0;
@@ -223,69 +215,65 @@ __global__ __launch_bounds__(WM *WN *kWave) void mx_product_kernel(MxGemmArgs g)
     const unsigned char *st = smem + s_read * SSTAGE + w_read * 4;
 #pragma unroll
     for (int j = 0; j < FN; ++j)
-      sa[j] = *reinterpret_cast<const uint32_t *>(st + asc + j * 32 * SROW) >> sh;
+      ra[j] = *reinterpret_cast<const uint32_t *>(st + asc + j * 32 * SROW);
 #pragma unroll
     for (int i = 0; i < FM; ++i)
-      sb[i] = *reinterpret_cast<const uint32_t *>(st + bsc + i * 32 * SROW) >> sh;
-    if (++w_read == SPER) {
-      w_read = 0;
-      s_read = s_read + 1 == SBUFS ? 0 : s_read + 1;
-    }
+      rb[i] = *reinterpret_cast<const uint32_t *>(st + bsc + i * 32 * SROW);
+    const bool next = ++w_read == SPER;
+    w_read = next ? 0 : w_read;
+    s_read = next ? (s_read + 1 == SBUFS ? 0 : s_read + 1) : s_read;
   };
 
   int buf = 0, kt = 0;
-  wait_oldest();
+  vm_wait<(STAGES - 2) * PER>();
   if (ktail && KT == 1) zero_tail(0);
   lgkm_barrier();
   read_scales();
-  read(0, smem, 0);
+#pragma unroll
+  for (int q = 0; q < FN + FM; ++q) read1(q, smem, 0);
   zero_acc();
+  // A stage in two half steps of 64 codes.  While the first is multiplied, the
+  // second's fragments are read; then stage kt + 1 has landed for everyone and
+  // its first fragments are read while the second half step is multiplied.  The
+  // loads of stage kt + 3, into the buffer of stage kt - 1, are spread over the
+  // products, as a wave that finds the load queue full stalls.  Nothing branches
+  // among the products and their sums are pinned after each half step: the
+  // compiler would otherwise move them all behind the last branch.
+  constexpr int EARLY = (CI + 1) / 2;               // loads of the first half step
   while (true) {
     const unsigned char *st = smem + buf * STAGE;
-    read(1, st, 1);
+    const int nbuf = buf + 1 == STAGES ? 0 : buf + 1, obuf = buf == 0 ? STAGES - 1 : buf - 1;
+    issue_scales();
+    // byte 2 s of a shifted word: half step s's block of this half of the wave
+#pragma unroll
+    for (int j = 0; j < FN; ++j) sa[j] = ra[j] >> sh;
+#pragma unroll
+    for (int i = 0; i < FM; ++i) sb[i] = rb[i] >> sh;
 #pragma unroll
     for (int q = 0; q < FN * FM; ++q) {
       acc[q / FM][q % FM] = mfma_mx4<0>(a[0][q / FM], b[0][q % FM], acc[q / FM][q % FM], sa[q / FM], sb[q % FM]);
-      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-      if (q < FN + FM) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+      if (q < FN + FM) read1(q, st, 1);
+      if (q % 3 == 2 && q / 3 < EARLY) issue_codes(q / 3, obuf);
+      __builtin_amdgcn_sched_barrier(0);
     }
-    const int nbuf = buf + 1 == STAGES ? 0 : buf + 1;
+    pin();
+    // loads complete in order: at most those of stage kt + 2 and the first of
+    // kt + 3 are left (a load of scales among them, or stores behind them, only
+    // make this wait for a little more)
+    vm_wait<PER + EARLY>();
     const bool last = kt + 1 == KT;
-    const bool more = !last || t + stride < t_end;
-    if (more) {
-      wait_oldest();
-      if (ktail && (last ? KT == 1 : kt + 2 == KT)) zero_tail(nbuf);
-      lgkm_barrier();                               // stage kt + 1 is there, stage kt has been read
+    if (!WIDE && ktail && (last ? KT == 1 : kt + 2 == KT)) zero_tail(nbuf);
+    lgkm_barrier();                                 // stage kt + 1 is there, stage kt has been read
+    read_scales();                                  // (after the last stage: of a settled buffer)
+#pragma unroll
+    for (int q = 0; q < FN * FM; ++q) {
+      acc[q / FM][q % FM] = mfma_mx4<2>(a[1][q / FM], b[1][q % FM], acc[q / FM][q % FM], sa[q / FM], sb[q % FM]);
+      if (q < FN + FM) read1(q, smem + nbuf * STAGE, 0);
+      if (q % 3 == 2 && q / 3 < CI - EARLY) issue_codes(EARLY + q / 3, obuf);
+      __builtin_amdgcn_sched_barrier(0);
     }
-    // The second half's products take their scales first: the words of stage
-    // kt + 1 (after the last stage: of a settled buffer, unused) replace them.
-    uint32_t na[FN], nb[FM];
-#pragma unroll
-    for (int j = 0; j < FN; ++j) na[j] = sa[j];
-#pragma unroll
-    for (int i = 0; i < FM; ++i) nb[i] = sb[i];
-    read_scales();
-    read(0, smem + nbuf * STAGE, 0);
-    auto second = [&](int q) __attribute__((always_inline)) {
-      acc[q / FM][q % FM] = mfma_mx4<2>(a[1][q / FM], b[1][q % FM], acc[q / FM][q % FM], na[q / FM], nb[q % FM]);
-    };
-    // with the refill of stage kt's buffer, a load between products
-    if (more && t_issue < t_end) {
-      issue_scales();
-      __builtin_amdgcn_s_setprio(1);
-#pragma unroll
-      for (int q = 0; q < FN * FM || q < CI; ++q) {
-        if (q < CI) issue_codes(q, buf);
-        if (q < FN * FM) second(q);
-        __builtin_amdgcn_sched_barrier(0);          // in this order
-      }
-      __builtin_amdgcn_s_setprio(0);
-      advance();
-      ++ahead;
-    } else {
-#pragma unroll
-      for (int q = 0; q < FN * FM; ++q) second(q);
-    }
+    pin();
+    advance();
     buf = nbuf;
     if (!last) {
       ++kt;
@@ -315,11 +303,12 @@ __global__ __launch_bounds__(WM *WN *kWave) void mx_product_kernel(MxGemmArgs g)
             stg16(y + col, make_uint4(s0[0], s1[0], s0[1], s1[1]));
         }
     }
-    if (!more) break;
     t += stride;
+    if (t >= t_end) break;
     kt = 0;
     zero_acc();
   }
+  vm_wait<0>();                                     // no load outlives the workgroup's LDS
 }
 
 }  // namespace
