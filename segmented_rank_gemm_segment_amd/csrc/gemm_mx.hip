@@ -2,6 +2,7 @@
 // gemm_tile.cuh): an MXFP4 weight under bf16 activations, with or without the
 // LoRA term, both operands MXFP4, and the experts' product.
 #include "mx_stream.cuh"
+#include "mx_weight.cuh"
 
 namespace lora {
 namespace {
@@ -50,6 +51,7 @@ hipError_t launch_gemm_mx(const void *X, int64_t ldx, const void *W, int64_t ldw
   GemmArgs g = gemm_args(X, ldx, W, ldw * 2, Y, ldy, M, K, N, H, seg, pool);
   g.mx = mx;
   if (M <= kStreamRows) return launch_mx_stream(g, lora, stream);
+  if (M > LORA_GEMM_SMALL_M && !mid_tiles(M, N) && !lora) return launch_mx_weight(g, stream);
   return launch_rows_split(g, lora, [&](const GemmArgs &a) {
     if (a.M <= LORA_GEMM_SMALL_M) return launch_tile<LORA_GEMM_SMALL, kMxW>(a, lora, stream);
     if (mid_tiles(a.M, N)) return launch_tile<LORA_GEMM_MID, kMxW>(a, lora, stream);
@@ -70,7 +72,7 @@ hipError_t launch_experts_gemm_mx(const void *X, int64_t ldx, const ExpertView &
     return (int)(t < ex.n_choices ? t : ex.n_choices);
   };
   if (ex.n_choices / ex.n_experts <= 32) return launch_experts_stream(g, tiles(16), stream);
-  if (ex.n_choices / ex.n_experts >= 512) return launch_experts<LORA_GEMM_LARGE>(g, tiles(256), stream);
+  if (ex.n_choices / ex.n_experts >= 512) return launch_mx_weight(g, stream);
   return launch_experts<LORA_GEMM_MID>(g, tiles(128), stream);
 }
 

@@ -15,7 +15,7 @@ import oracle
 import segmented_rank_gemm_segment_amd as srg
 import workloads as wl
 from gpu_harness import DEV, say
-from test_gpu_mxfp4 import U, bf16_device, check_close, mx_device, product_tol
+from test_gpu_mxfp4 import U, bf16_device, check_close, mx_device, packed, product_tol
 
 pytestmark = pytest.mark.gpu
 
@@ -226,6 +226,32 @@ def test_experts_product(n, k, E, d_in, d_out, kind, gathered):
         d = np.abs(Y[off[e]:off[e + 1], :d_out].double().cpu().numpy() - Y64)
         assert np.all(d <= product_tol(Xe, W64, Y64)), e
     assert bool((Y[kept:] == 7.0).all()) and bool((Y[:, d_out:] == 7.0).all())
+
+
+@pytest.mark.parametrize("n,k,E,d_in,d_out,kind", [
+    (3000, 2, 5, 512, 520, "uniform"), (5000, 4, 9, 1024, 1096, "skewed"), (4100, 2, 3, 1536, 264, "bad"),
+    (6000, 3, 12, 128, 2056, "skewed"), (2048, 1, 2, 608, 72, "one")])
+def test_experts_product_of_long_segments(n, k, E, d_in, d_out, kind):
+    """Segments of many tiles, aligned scale rows; every element."""
+    ids = make_ids(n + d_in, n, k, E, kind)
+    ref = oracle.expert_routing(ids, E)
+    order, off = ref["sorted_choice"], ref["expert_offsets"]
+    ex = sorted_batch(ids, E)
+    codes, scales = wl.make_mxfp4(E + d_out, E * d_out, d_in)
+    Wq, ws = packed(codes, scales)
+    Wq = Wq.view(E, d_out, d_in // 2)
+    ws = ws.as_strided((E, d_out, d_in // 32), (d_out * ws.stride(0), ws.stride(0), 1))
+    X = torch.randn(n, d_in, device=DEV, generator=torch.Generator(DEV).manual_seed(n)).bfloat16()
+    Y = torch.full((n * k, d_out), 7.0, dtype=torch.bfloat16, device=DEV)
+    srg.lora_experts_gemm_mxfp4w(X, ex, Wq, ws, Y)
+    for e in range(E):
+        W64 = torch.from_numpy(oracle.decode_mxfp4(codes[e * d_out:(e + 1) * d_out],
+                                                   scales[e * d_out:(e + 1) * d_out])).to(DEV)
+        X64 = X.double()[torch.from_numpy(order[off[e]:off[e + 1]] // k).long().to(DEV)]
+        Y64 = X64 @ W64.t()
+        tol = 2.0 ** -8 * Y64.abs() + d_in * U * (X64.abs() @ W64.abs().t())
+        assert bool(((Y[off[e]:off[e + 1]].double() - Y64).abs() <= tol).all()), e
+    assert bool((Y[len(order):] == 7.0).all())
 
 
 def test_layer_run_in_a_graph():

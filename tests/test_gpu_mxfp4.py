@@ -190,6 +190,34 @@ def test_both_operands_many_tiles(n, d_in, d_out, pad):
     assert bool(((out[:n, :d_out].double() - Y64).abs() <= tol).all())
 
 
+def packed(codes, scales, pad=0):
+    """On the device, scale rows a multiple of 16 bytes apart plus pad; what
+    pads them (NaN scales) must never be used."""
+    q = torch.from_numpy(codes).to(DEV)
+    s = torch.full((len(scales), (scales.shape[1] + 15) // 16 * 16 + pad), 255, dtype=torch.uint8,
+                   device=DEV)
+    s[:, :scales.shape[1]] = torch.from_numpy(scales).to(DEV)
+    return q, s[:, :scales.shape[1]]
+
+
+@pytest.mark.parametrize("n,d_in,d_out", [
+    (2100, 512, 8200), (2100, 1536, 8200), (2100, 32, 8200), (2100, 64, 8200), (2100, 96, 8200),
+    (2100, 128, 8200), (2100, 608, 8200), (2100, 704, 8200), (4200, 1024, 4104), (8200, 640, 2056)])
+@pytest.mark.parametrize("pad", [0, 12])
+def test_weight_many_tiles(n, d_in, d_out, pad):
+    """More output tiles than compute units, scale rows with and without 16-byte
+    alignment, K of one stage to many with every tail; every element."""
+    codes, scales = wl.make_mxfp4(d_out, d_out, d_in)
+    X = torch.randn(n, d_in, device=DEV, generator=torch.Generator(DEV).manual_seed(n)).bfloat16()
+    out = torch.full((n + 1, d_out + 8), 7.0, dtype=torch.bfloat16, device=DEV)
+    srg.lora_base_gemm_mxfp4w(X, *packed(codes, scales, pad), out[:n, :d_out])
+    assert bool((out[n] == 7.0).all()) and bool((out[:, d_out:] == 7.0).all())
+    X64, W64 = X.double(), torch.from_numpy(oracle.decode_mxfp4(codes, scales)).to(DEV)
+    Y64 = X64 @ W64.t()
+    tol = 2.0 ** -8 * Y64.abs() + d_in * U * (X64.abs() @ W64.abs().t())
+    assert bool(((out[:n, :d_out].double() - Y64).abs() <= tol).all())
+
+
 LORA_CASES = [
     # seed, n, d_in, d_out, n_slots, r_max, p_base, runs
     (601, 1, 64, 72, 3, 8, 0.0, False),
