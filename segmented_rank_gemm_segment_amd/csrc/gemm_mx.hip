@@ -51,13 +51,15 @@ hipError_t launch_gemm_mx(const void *X, int64_t ldx, const void *W, int64_t ldw
   GemmArgs g = gemm_args(X, ldx, W, ldw * 2, Y, ldy, M, K, N, H, seg, pool);
   g.mx = mx;
   if (M <= kStreamRows) return launch_mx_stream(g, lora, stream);
-  if (M > LORA_GEMM_SMALL_M && !mid_tiles(M, N) && !lora) return launch_mx_weight(g, stream);
-  return launch_rows_split(g, lora, [&](const GemmArgs &a) {
-    if (a.M <= LORA_GEMM_SMALL_M) return launch_tile<LORA_GEMM_SMALL, kMxW>(a, lora, stream);
-    if (mid_tiles(a.M, N)) return launch_tile<LORA_GEMM_MID, kMxW>(a, lora, stream);
-    if (large192_tiles(a.M, N)) return launch_tile<LORA_GEMM_LARGE192, kMxW>(a, lora, stream);
-    return launch_tile<LORA_GEMM_LARGE, kMxW>(a, lora, stream);
-  });
+  if (M <= LORA_GEMM_SMALL_M) return launch_tile<LORA_GEMM_SMALL, kMxW>(g, lora, stream);
+  if (mid_tiles(M, N)) return launch_tile<LORA_GEMM_MID, kMxW>(g, lora, stream);
+  if (!lora) return launch_mx_weight<false>(g, stream);
+  // With adapters the shared tiles, whose LoRA term goes through LDS: read from
+  // memory into each wave's fragments instead it cost 11 us a tile, and the two
+  // were level (16943 x 4096 x 14336, 8 slots: 1.69 ms).  Both add up K in the same
+  // order, so base-only rows keep the base product's bits.
+  if (large192_tiles(M, N)) return launch_tile<LORA_GEMM_LARGE192, kMxW>(g, lora, stream);
+  return launch_tile<LORA_GEMM_LARGE, kMxW>(g, lora, stream);
 }
 
 hipError_t launch_experts_gemm_mx(const void *X, int64_t ldx, const ExpertView &ex, const void *W,
@@ -72,7 +74,7 @@ hipError_t launch_experts_gemm_mx(const void *X, int64_t ldx, const ExpertView &
     return (int)(t < ex.n_choices ? t : ex.n_choices);
   };
   if (ex.n_choices / ex.n_experts <= 32) return launch_experts_stream(g, tiles(16), stream);
-  if (ex.n_choices / ex.n_experts >= 512) return launch_mx_weight(g, stream);
+  if (ex.n_choices / ex.n_experts >= 512) return launch_mx_weight<true>(g, stream);
   return launch_experts<LORA_GEMM_MID>(g, tiles(128), stream);
 }
 

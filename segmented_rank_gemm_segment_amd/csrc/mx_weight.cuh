@@ -31,7 +31,7 @@ __device__ __forceinline__ void tile_at(int t, int tiles_m, int tiles_n, int &mi
 // multiple of 128.
 template <bool GROUPED, bool WIDE, bool TAIL>
 __global__ __launch_bounds__(512) void mx_weight_kernel(GemmArgs g) {
-  constexpr int BM = 256, BN = 256, WN = 4, TM = 128, TN = 64, FM = 4, FN = 2, NW = 8;
+  constexpr int BM = 256, BN = 256, WN = 4, TM = 128, TN = 64, FM = 4, FN = 2;
   constexpr int XST = BM * 128, XN = 3;             // X: bytes of a stage, stages
   constexpr int WST = BN * 64, WNB = 2;             // W: bytes of 128 of K, pieces
   constexpr int SROW = WIDE ? 16 : 4, SST = BN * SROW, SNB = 2;
@@ -92,8 +92,10 @@ __global__ __launch_bounds__(512) void mx_weight_kernel(GemmArgs g) {
   // piece, one per stage, 16 rows of 64 bytes each.  Scales: 64 rows, waves w and
   // w + 4 the same (so that all waves issue as many).
   const uint32_t sbase = lds_offset(smem);
-  const unsigned char *xrow[4], *wbase = nullptr, *sbase_g = nullptr;
-  uint32_t woff[2], soff;
+  // Rows as 32-bit offsets from the tile's first (leading dimensions are below
+  // 2^22 elements); the experts' X rows lie anywhere and take an address each.
+  const unsigned char *xrow[GROUPED ? 4 : 1], *xbase = nullptr, *wbase = nullptr, *sbase_g = nullptr;
+  uint32_t xoff[4], woff[2], soff;
   auto xchunk = [&](int i) { return (l & 7) ^ ((((wid * 4 + i) * 8 + l / 8) >> 1) & 7); };
   auto wchunk = [&](int i) { return (l & 3) ^ ((((wid * 2 + i) * 16 + l / 4) >> 2) & 3); };
   auto aim = [&](int tile) __attribute__((always_inline)) {
@@ -103,9 +105,14 @@ __global__ __launch_bounds__(512) void mx_weight_kernel(GemmArgs g) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int p = min(m0 + (wid * 4 + i) * 8 + l / 8, m1 - 1);
-      const int row = GROUPED && g.ex.sorted_choice ? g.ex.sorted_choice[p] / g.ex.top_k : p;
-      xrow[i] = reinterpret_cast<const unsigned char *>(g.X + (int64_t)row * g.ldx) + xchunk(i) * 16;
+      if constexpr (GROUPED) {
+        const int row = g.ex.sorted_choice ? g.ex.sorted_choice[p] / g.ex.top_k : p;
+        xrow[i] = reinterpret_cast<const unsigned char *>(g.X + (int64_t)row * g.ldx) + xchunk(i) * 16;
+      } else {
+        xoff[i] = (uint32_t)(p - m0) * (uint32_t)(g.ldx * 2) + xchunk(i) * 16;
+      }
     }
+    if constexpr (!GROUPED) xbase = reinterpret_cast<const unsigned char *>(g.X + (int64_t)m0 * g.ldx);
     const int n0 = ni * BN;
     const int64_t ldw = g.ldw / 2;                  // bytes
     wbase = reinterpret_cast<const unsigned char *>(g.W) + (GROUPED ? e * g.ex.w_stride : 0) + n0 * ldw;
@@ -123,8 +130,11 @@ __global__ __launch_bounds__(512) void mx_weight_kernel(GemmArgs g) {
     // a chunk past K reads the stage's first chunk and is zeroed before use
     const int c = xchunk(i);
     const int back = TAIL && k_issue * 64 + c * 8 >= K ? c * 16 : 0;
-    dma16(__builtin_amdgcn_readfirstlane(sbase + xb * XST + (wid * 4 + i) * 1024),
-          xrow[i] + (int64_t)k_issue * 128 - back);
+    const uint32_t dst = __builtin_amdgcn_readfirstlane(sbase + xb * XST + (wid * 4 + i) * 1024);
+    if constexpr (GROUPED)
+      dma16(dst, xrow[i] + (int64_t)k_issue * 128 - back);
+    else
+      dma16_s(dst, xoff[i] - back, xbase + (int64_t)k_issue * 128);
   };
   auto issue_w = [&](int i) __attribute__((always_inline)) {
     const int c = wchunk(i), p = k_issue / 2;
@@ -340,22 +350,15 @@ __global__ __launch_bounds__(512) void mx_weight_kernel(GemmArgs g) {
   vm_wait<0>();                                     // no load outlives the workgroup's LDS
 }
 
-inline hipError_t launch_mx_weight(const GemmArgs &g, hipStream_t stream) {
+template <bool GROUPED>
+hipError_t launch_mx_weight(const GemmArgs &g, hipStream_t stream) {
   const dim3 grid(kCUs), block(512);
-  const bool wide = g.K % 512 == 0 && g.mx.ldw % 16 == 0, tail = g.K % 128 != 0;
-  const bool grouped = g.ex.n_experts > 0;
-#define LORA_MX_WEIGHT(G, W, T)                                                         \
-  hipLaunchKernelGGL((mx_weight_kernel<G, W, T>), grid, block, 0, stream, g)
-  if (grouped) {
-    if (wide) LORA_MX_WEIGHT(true, true, false);
-    else if (tail) LORA_MX_WEIGHT(true, false, true);
-    else LORA_MX_WEIGHT(true, false, false);
-  } else {
-    if (wide) LORA_MX_WEIGHT(false, true, false);
-    else if (tail) LORA_MX_WEIGHT(false, false, true);
-    else LORA_MX_WEIGHT(false, false, false);
-  }
-#undef LORA_MX_WEIGHT
+  if (g.K % 512 == 0 && g.mx.ldw % 16 == 0)
+    hipLaunchKernelGGL((mx_weight_kernel<GROUPED, true, false>), grid, block, 0, stream, g);
+  else if (g.K % 128 == 0)
+    hipLaunchKernelGGL((mx_weight_kernel<GROUPED, false, false>), grid, block, 0, stream, g);
+  else
+    hipLaunchKernelGGL((mx_weight_kernel<GROUPED, false, true>), grid, block, 0, stream, g);
   return hipGetLastError();
 }
 

@@ -398,3 +398,50 @@ def test_quantize_then_product_on_another_stream_and_in_a_graph():
         side.synchronize()
         assert torch.equal(Y, y2) and torch.equal(Yw, yw2) and torch.equal(Xq, q2)
         assert float(Y.abs().max()) > 0
+
+
+@pytest.mark.parametrize("n,d_in,d_out,n_slots,r_max", [
+    (2100, 512, 8200, 7, 64), (2100, 96, 8200, 16, 16), (2100, 640, 8200, 5, 8), (2304, 128, 8192, 17, 32),
+    (2040, 1024, 8200, 3, 32), (3100, 96, 5120, 9, 64)])
+@pytest.mark.parametrize("runs", [True, False])
+def test_fused_lora_many_tiles(n, d_in, d_out, n_slots, r_max, runs):
+    """The large batches' LoRA term, requests of many rows and rows of their own
+    adapter each, more tiles than compute units; every element, and the
+    base-only rows bit for bit the base product's."""
+    w = wl.make_random(640 + n_slots, n, d_in, d_out, n_slots, r_max, p_base=0.1, dtype="bf16", runs=runs)
+    w.slot_rank[1] = 0
+    if r_max > 8:
+        w.slot_rank[2] = 5                               # a rank that is no multiple of 8
+    codes, scales = wl.make_mxfp4(641, d_out, d_in)
+    Wq, ws = packed(codes, scales)
+    d = wl.device_tensors(w, DEV)
+    pool = srg.Pool(d["A"], d["Bt"], d["slot_rank"], w.slot_alpha)
+    seg = srg.Segments(w.n, w.n_slots, DEV)
+    H = torch.full((n, r_max), float("nan"), device=DEV)
+    srg.lora_build_shrink(d["row_slot"], d["X"], pool, seg, H)
+    Yf = torch.full((n + 1, d_out + 8), 7.0, dtype=torch.bfloat16, device=DEV)
+    srg.lora_linear_fused_mxfp4w(d["X"], Wq, ws, H, seg, pool, Yf[:n, :d_out])
+    assert bool((Yf[n] == 7.0).all()) and bool((Yf[:, d_out:] == 7.0).all())
+    Yb = torch.empty((n, d_out), dtype=torch.bfloat16, device=DEV)
+    srg.lora_base_gemm_mxfp4w(d["X"], Wq, ws, Yb)
+    X64, W64 = d["X"].double(), torch.from_numpy(oracle.decode_mxfp4(codes, scales)).to(DEV)
+    sums = X64.abs() @ W64.abs().t()
+    Y64 = X64 @ W64.t()
+    tol = torch.zeros_like(Y64)
+    slot = torch.from_numpy(w.row_slot).to(DEV)
+    base = slot < 0
+    for a in range(n_slots):
+        r, rows = int(w.slot_rank[a]), (slot == a).nonzero().squeeze(1)
+        if r == 0:
+            base |= slot == a
+            continue
+        s = float(w.slot_alpha[a]) / r
+        A, B = d["A"][a, :r].double(), d["Bt"][a, :r].double()
+        h, h_abs = X64[rows] @ A.t(), X64[rows].abs() @ A.abs().t()
+        Y64[rows] += s * (h @ B)
+        # H's sum, its split and the term's own sum, as in lora_tol
+        tol[rows] += s * ((h_abs * (d_in + r + 2) * U + h.abs() * 2.0 ** -16) @ B.abs())
+        tol[rows] += (2 * r + 2) * U * (sums[rows] + s * (h_abs @ B.abs()))
+    tol += 2.0 ** -8 * Y64.abs() + d_in * U * sums
+    assert bool(((Yf[:n, :d_out].double() - Y64).abs() <= tol).all())
+    assert torch.equal(Yf[:n, :d_out][base], Yb[base])
