@@ -1,6 +1,7 @@
 // Launches of the products with MXFP4 operands (the MFMA tiles of
 // gemm_tile.cuh): an MXFP4 weight under bf16 activations, with or without the
 // LoRA term, both operands MXFP4, and the experts' product.
+#include "mx_mid.cuh"
 #include "mx_stream.cuh"
 #include "mx_weight.cuh"
 
@@ -37,6 +38,11 @@ hipError_t launch_gemm_mx(const void *X, int64_t ldx, const void *W, int64_t ldw
   const bool lora = seg != nullptr;
   if (mx.x && M > LORA_GEMM_SMALL_M && !mid_tiles(M, N))
     return launch_mx_product(X, ldx, W, ldw, mx, Y, ldy, M, K, N, stream);
+  if (mx.x && M <= LORA_GEMM_SMALL_M) {
+    GemmArgs g = gemm_args(X, ldx, W, ldw * 2, Y, ldy, M, K, N, nullptr, nullptr, nullptr);
+    g.mx = mx;
+    return launch_mx_mid<true>(g, false, stream);
+  }
   if (mx.x) {
     // both operands in units of four codes
     GemmArgs g = gemm_args(X, ldx / 2, W, ldw / 2, Y, ldy, M, K / 4, N, nullptr, nullptr, nullptr);
@@ -51,7 +57,7 @@ hipError_t launch_gemm_mx(const void *X, int64_t ldx, const void *W, int64_t ldw
   GemmArgs g = gemm_args(X, ldx, W, ldw * 2, Y, ldy, M, K, N, H, seg, pool);
   g.mx = mx;
   if (M <= kStreamRows) return launch_mx_stream(g, lora, stream);
-  if (M <= LORA_GEMM_SMALL_M) return launch_tile<LORA_GEMM_SMALL, kMxW>(g, lora, stream);
+  if (M <= LORA_GEMM_SMALL_M) return launch_mx_mid<false>(g, lora, stream);
   if (mid_tiles(M, N)) return launch_tile<LORA_GEMM_MID, kMxW>(g, lora, stream);
   if (!lora) return launch_mx_weight<false>(g, stream);
   // With adapters the shared tiles, whose LoRA term goes through LDS: read from
