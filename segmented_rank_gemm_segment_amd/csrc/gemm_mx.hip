@@ -1,6 +1,9 @@
-// Launches of the products with MXFP4 operands (the MFMA tiles of
-// gemm_tile.cuh): an MXFP4 weight under bf16 activations, with or without the
-// LoRA term, both operands MXFP4, and the experts' product.
+// Launches of the products with MXFP4 operands: an MXFP4 weight under bf16
+// activations, with or without the LoRA term, both operands MXFP4, and the
+// experts' product.  Which kernel a batch takes is a matter of how many tiles of
+// each size it makes for the CUs.
+#include <cmath>
+
 #include "mx_mid.cuh"
 #include "mx_stream.cuh"
 #include "mx_weight.cuh"
@@ -16,17 +19,17 @@ hipError_t launch_codes(const GemmArgs &g, hipStream_t stream) {
   return hipGetLastError();
 }
 
-template <int BM, int BN, int WM, int WN, int BK, int STAGES, int KG>
-hipError_t launch_experts(const GemmArgs &g, int tiles_m, hipStream_t stream) {
-  const int tn = (g.N + BN - 1) / BN;
-  // the workgroups find the number of tiles themselves: room for any up to tiles_m
-  const int split = tiles_m < kHeavyMaxTilesM ? tiles_m : kHeavyMaxTilesM;
-  int grid = (tiles_m * tn + 7) / 8 * 8;
-  if (8 * ((tn + 7) / 8) * split > grid) grid = 8 * ((tn + 7) / 8) * split;
-  hipLaunchKernelGGL(
-      (gemm_bf16_kernel<BM, BN, WM, WN, BK, STAGES, KG, 0, false, kMxW, false, true>), dim3(grid),
-      dim3(WM * WN * KG * kWave), 0, stream, g);
-  return hipGetLastError();
+// Cost of a batch in tiles of 64, 128 and 256 rows and columns: rounds over the
+// CUs (64: several workgroups follow each other on a CU, so parts of a round)
+// times a round's time, given in microseconds at K 4096.
+struct TileCost {
+  double t64, t128, t256;
+};
+TileCost tile_cost(int M, int N, double us64, double us128, double us256) {
+  auto tiles = [&](int b) { return (double)(((int64_t)M + b - 1) / b) * (((int64_t)N + b - 1) / b); };
+  const double n64 = tiles(64) / kCUs;
+  return TileCost{(n64 < 1 ? 1 : n64) * us64, ceil(tiles(128) / kCUs) * us128,
+                  ceil(tiles(256) / kCUs) * us256};
 }
 
 }  // namespace
@@ -36,36 +39,37 @@ hipError_t launch_gemm_mx(const void *X, int64_t ldx, const void *W, int64_t ldw
                           const float *H, const SegView *seg, const PoolView *pool,
                           hipStream_t stream) {
   const bool lora = seg != nullptr;
-  if (mx.x && M > LORA_GEMM_SMALL_M && !mid_tiles(M, N))
-    return launch_mx_product(X, ldx, W, ldw, mx, Y, ldy, M, K, N, stream);
-  if (mx.x && M <= LORA_GEMM_SMALL_M) {
-    GemmArgs g = gemm_args(X, ldx, W, ldw * 2, Y, ldy, M, K, N, nullptr, nullptr, nullptr);
-    g.mx = mx;
-    return launch_mx_mid<true>(g, false, stream);
-  }
   if (mx.x) {
-    // both operands in units of four codes
+    const TileCost c = tile_cost(M, N, 6.6, 19.6, 27.5);
+    if (c.t64 <= c.t128 && c.t64 <= c.t256) {
+      GemmArgs g = gemm_args(X, ldx, W, ldw * 2, Y, ldy, M, K, N, nullptr, nullptr, nullptr);
+      g.mx = mx;
+      return launch_mx_mid<true>(g, false, stream);
+    }
+    if (c.t256 <= c.t128) return launch_mx_product(X, ldx, W, ldw, mx, Y, ldy, M, K, N, stream);
+    // in units of four codes
     GemmArgs g = gemm_args(X, ldx / 2, W, ldw / 2, Y, ldy, M, K / 4, N, nullptr, nullptr, nullptr);
     g.mx = mx;
-    return launch_rows_split(g, false, [&](const GemmArgs &a) {
-      if (a.M <= LORA_GEMM_SMALL_M) return launch_codes<LORA_GEMM_SMALL>(a, stream);
-      if (mid_tiles(a.M, N)) return launch_codes<LORA_GEMM_MID>(a, stream);
-      if (large192_tiles(a.M, N)) return launch_codes<LORA_GEMM_LARGE192>(a, stream);
-      return launch_codes<LORA_GEMM_LARGE>(a, stream);
-    });
+    return launch_codes<LORA_GEMM_MID>(g, stream);
   }
   GemmArgs g = gemm_args(X, ldx, W, ldw * 2, Y, ldy, M, K, N, H, seg, pool);
   g.mx = mx;
   if (M <= kStreamRows) return launch_mx_stream(g, lora, stream);
-  if (M <= LORA_GEMM_SMALL_M) return launch_mx_mid<false>(g, lora, stream);
-  if (mid_tiles(M, N)) return launch_tile<LORA_GEMM_MID, kMxW>(g, lora, stream);
-  if (!lora) return launch_mx_weight<false>(g, stream);
+  // Base-only rows of a batch with adapters have the base product's bits, so both
+  // go by the same rule as far as the order of adding up K goes: the 64-tiles', or
+  // that of all others.
+  const TileCost c = tile_cost(M, N, 15, 50, 86);
+  if (c.t64 <= c.t128 && c.t64 <= c.t256) return launch_mx_mid<false>(g, lora, stream);
+  if (!lora)
+    return c.t256 <= c.t128 ? launch_mx_weight<false>(g, stream)
+                            : launch_tile<LORA_GEMM_MID, kMxW>(g, false, stream);
   // With adapters the shared tiles, whose LoRA term goes through LDS: read from
-  // memory into each wave's fragments instead it cost 11 us a tile, and the two
-  // were level (16943 x 4096 x 14336, 8 slots: 1.69 ms).  Both add up K in the same
-  // order, so base-only rows keep the base product's bits.
-  if (large192_tiles(M, N)) return launch_tile<LORA_GEMM_LARGE192, kMxW>(g, lora, stream);
-  return launch_tile<LORA_GEMM_LARGE, kMxW>(g, lora, stream);
+  // memory into each wave's fragments instead, at the end of the persistent
+  // kernel's tiles, it cost 11 us a tile, and the two were level (16943 x 4096 x
+  // 14336, 8 slots: 1.69 ms).
+  if (c.t128 <= c.t256 * (109. / 86)) return launch_tile<LORA_GEMM_MID, kMxW>(g, true, stream);
+  if (large192_tiles(M, N)) return launch_tile<LORA_GEMM_LARGE192, kMxW>(g, true, stream);
+  return launch_tile<LORA_GEMM_LARGE, kMxW>(g, true, stream);
 }
 
 hipError_t launch_experts_gemm_mx(const void *X, int64_t ldx, const ExpertView &ex, const void *W,
@@ -79,9 +83,14 @@ hipError_t launch_experts_gemm_mx(const void *X, int64_t ldx, const ExpertView &
     const int64_t t = (int64_t)ex.n_choices / bm + ex.n_experts;
     return (int)(t < ex.n_choices ? t : ex.n_choices);
   };
-  if (ex.n_choices / ex.n_experts <= 32) return launch_experts_stream(g, tiles(16), stream);
-  if (ex.n_choices / ex.n_experts >= 512) return launch_mx_weight<true>(g, stream);
-  return launch_experts<LORA_GEMM_MID>(g, tiles(128), stream);
+  // by the mean rows of an expert (64 experts of 2048 -> 1536, in us: 8 rows 38
+  // streamed against 64 on the 64-tiles, 24 rows 69 against 82, 16 experts of 4096
+  // -> 4096 86 against 61; 64 rows 110 on those against 100 on the 256-tiles, and 92
+  // against 104)
+  const int rows = ex.n_choices / ex.n_experts;
+  if (rows <= 16) return launch_experts_stream(g, tiles(16), stream);
+  if (rows < 64) return launch_experts_mid(g, tiles(64), stream);
+  return launch_mx_weight<true>(g, stream);
 }
 
 }  // namespace lora

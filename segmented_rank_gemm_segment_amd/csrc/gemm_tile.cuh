@@ -506,20 +506,16 @@ __device__ __forceinline__ void expert_of_tile(const ExpertView &ex, const Exper
 //     are, 64 codes per sub-step.
 // MX scales travel with the stage, SCW words of 4 blocks per row behind the B
 // rows.
-// GROUPED (kMxW, LORA 0): the experts' product.  An M-tile is up to BM
-// consecutive sorted rows of one expert, its X rows are found through
-// sorted_choice and its W is the expert's own.
 // LORA: 0 = plain product; 1 = fused LoRA with B gathered from Bt; 2 = fused
 // LoRA with B read from its d_out-major copy.  DORA: rows of rank > 0 are
 // multiplied by their slot's column factors before the rounding.  LAYER
 // (small tiles): the whole layer in one launch (layer.cuh); the row
 // metadata and H come from the launch itself instead of earlier calls.
 template <int BM, int BN, int WM, int WN, int BK, int STAGES, int KG, int LORA, bool DORA,
-          int WQ, bool LAYER = false, bool GROUPED = false>
+          int WQ, bool LAYER = false>
 __global__ __launch_bounds__(WM *WN *KG *kWave) void gemm_bf16_kernel(GemmArgs g) {
   using C = TileCfg<BM, BN, WM, WN, BK, STAGES, KG, WQ>;
   constexpr bool WF8 = WQ == kFp8W, MX = WQ == kMxW || WQ == kMxXW;
-  static_assert(!GROUPED || (WQ == kMxW && LORA == 0 && !LAYER), "the experts' product");
   static_assert(!LAYER || (KG > 1 && LORA == 1 && WM * WN * KG * kWave == kLayerThreads),
                 "the one-launch layer runs on the small tiles");
   static_assert(!LAYER || C::LDS >= (4 * 4095 + 2) * 4, "the build's tables fit in the ring");
@@ -543,19 +539,13 @@ __global__ __launch_bounds__(WM *WN *KG *kWave) void gemm_bf16_kernel(GemmArgs g
   const int wid = __builtin_amdgcn_readfirstlane((tid / kWave) % C::NWG);
   const int wm = wid / WN, wn = wid % WN;
   const int kg0 = kgrp * BK;                        // the group's offset in a K step
-  const int N = g.N, K = g.K;
-  int M = g.M, tiles_m = (M + BM - 1) / BM;
-  ExpertTiles et{0, 0, 0};
-  if constexpr (GROUPED) {
-    et = expert_tiles<BM, C::T>(g.ex, reinterpret_cast<int *>(smem));
-    tiles_m = et.total;
-  }
+  const int M = g.M, N = g.N, K = g.K;
 
   // XCD-aware tile order (tile_order): consecutive workgroup ids go to
   // different XCDs (round robin over 8), and each XCD walks its share of the
   // tiles in groups of M-tiles sweeping N, so operand tiles shared by
   // neighbours stay inside one L2.
-  const int tiles_n = (N + BN - 1) / BN;
+  const int tiles_m = (M + BM - 1) / BM, tiles_n = (N + BN - 1) / BN;
   // Tiles of many LoRA runs take the row epilogue, which costs more than
   // the staged one (decode rows beside a prefill request); so that they run
   // first rather than in a last, partly filled wave, the end M-tile of the
@@ -573,22 +563,8 @@ __global__ __launch_bounds__(WM *WN *KG *kWave) void gemm_bf16_kernel(GemmArgs g
   // (a layer workgroup without a tile still has its row of the layer to do)
   if (!LAYER && !has_tile) return;
   if (LAYER && !has_tile) m_idx = n_idx = 0;
-  int m0 = m_idx * BM;
+  const int m0 = m_idx * BM;
   const int n0 = n_idx * BN;
-  // the experts' product: rows [m0, M) are the tile's expert's, W its weight
-  const unsigned char *Wt = reinterpret_cast<const unsigned char *>(g.W);
-  const unsigned char *SWt = g.mx.w;
-  if constexpr (GROUPED) {
-    int e;
-    expert_of_tile<BM, C::T>(g.ex, et, m_idx, reinterpret_cast<int *>(smem), e, m0, M);
-    Wt += (int64_t)e * g.ex.w_stride;
-    SWt += (int64_t)e * g.ex.s_stride;
-  }
-  // X row of tile row r (rows past M read the last one)
-  auto xrow = [&](int r) __attribute__((always_inline)) {
-    const int p = min(m0 + r, M - 1);
-    return GROUPED && g.ex.sorted_choice ? g.ex.sorted_choice[p] / g.ex.top_k : p;
-  };
 
   // Small tiles (two K groups) finish row by row: thread tid owns tile row
   // tid / (BN / 8) and 8 consecutive columns (see the end of the kernel);
@@ -631,13 +607,14 @@ __global__ __launch_bounds__(WM *WN *KG *kWave) void gemm_bf16_kernel(GemmArgs g
   for (int i = 0; i < C::AI; ++i) {
     const int row = (wid * C::AI + i) * C::RPI + rr;
     alc[i] = C::swz(l % C::CH, row);
-    asrc[i] = g.X + (int64_t)xrow(row) * g.ldx + alc[i] * 8;
+    asrc[i] = g.X + (int64_t)min(m0 + row, M - 1) * g.ldx + alc[i] * 8;
   }
 #pragma unroll
   for (int i = 0; i < C::BI; ++i) {
     const int row = (wid * C::BI + i) * C::RPIB + rrb;
     blc[i] = C::swzb(l % C::CHB, row);
-    bsrc[i] = Wt + wbytes((int64_t)min(n0 + row, N - 1) * g.ldw + blc[i] * C::EPCB);
+    bsrc[i] = reinterpret_cast<const unsigned char *>(g.W) +
+              wbytes((int64_t)min(n0 + row, N - 1) * g.ldw + blc[i] * C::EPCB);
   }
   // byte offset of K position k0 in a B row's chunk, or back to the row's
   // first chunk when the chunk lies past K (in bounds; zeroed before use)
@@ -665,7 +642,7 @@ __global__ __launch_bounds__(WM *WN *KG *kWave) void gemm_bf16_kernel(GemmArgs g
     const unsigned char *src =
         WQ == kMxXW && row < BM
             ? g.mx.x + (int64_t)min(m0 + row, M - 1) * g.mx.ldx
-            : SWt + (int64_t)min(n0 + row - (WQ == kMxXW ? BM : 0), N - 1) * g.mx.ldw;
+            : g.mx.w + (int64_t)min(n0 + row - (WQ == kMxXW ? BM : 0), N - 1) * g.mx.ldw;
     dma4(__builtin_amdgcn_readfirstlane(slice + C::SOFF + q * 256), src + w * 4);
   };
   // blocks past K: scale 1 (their codes are zeroed; a NaN scale would spoil them)
@@ -720,20 +697,17 @@ __global__ __launch_bounds__(WM *WN *KG *kWave) void gemm_bf16_kernel(GemmArgs g
   // scalar bases, and per lane the byte offset of its row (rows past M / N
   // clamped to the last) and chunk from them -- below 2^32 because leading
   // dimensions are below 2^22 elements and tiles have at most 256 rows.
-  // (The experts' X rows may lie anywhere: a 64-bit address each.)
-  const unsigned char *const xa =
-      reinterpret_cast<const unsigned char *>(g.X + (GROUPED ? 0 : (int64_t)m0 * g.ldx));
-  const unsigned char *const wb = Wt + wbytes((int64_t)n0 * g.ldw);
+  const unsigned char *const xa = reinterpret_cast<const unsigned char *>(g.X + (int64_t)m0 * g.ldx);
+  const unsigned char *const wb = reinterpret_cast<const unsigned char *>(g.W) +
+                                  wbytes((int64_t)n0 * g.ldw);
   uint32_t own_off[OWNED ? NIB : 1];
-  const unsigned char *own_row[OWNED && GROUPED ? AIG : 1];
   if constexpr (OWNED) {
 #pragma unroll
     for (int t = 0; t < NIB; ++t) {
       if (t < AIG) {
         const int row = t * C::RPI + rr;
-        own_off[t] = (uint32_t)(GROUPED ? 0 : (min(m0 + row, M - 1) - m0) * g.ldx * 2) +
+        own_off[t] = (uint32_t)((min(m0 + row, M - 1) - m0) * g.ldx * 2) +
                      C::swz(l % C::CH, row) * 16;
-        if constexpr (GROUPED) own_row[t] = xa + (int64_t)xrow(row) * g.ldx * 2;
       } else {
         const int row = (t - AIG) * C::RPIB + rrb;
         own_off[t] = (uint32_t)wbytes((min(n0 + row, N - 1) - n0) * g.ldw) +
@@ -750,10 +724,7 @@ __global__ __launch_bounds__(WM *WN *KG *kWave) void gemm_bf16_kernel(GemmArgs g
     if (t >= NIB) {
       if constexpr (MX) issue_scales(t - NIB, sbase + buf * C::STAGE + kgrp * C::GSTAGE, k0);
     } else if (t < AIG) {
-      if constexpr (GROUPED) {
-        const int c = C::swz(l % C::CH, t * C::RPI + rr);
-        dma16(dst, own_row[t] + (!tail || k0 + c * 8 < K ? own_off[t] + k0 * 2 : 0));
-      } else if (!tail) {
+      if (!tail) {
         dma16_s(dst, own_off[t], xa + (int64_t)k0 * 2);
       } else {
         // the base stays scalar: the K position goes into the lane offsets
@@ -1600,7 +1571,6 @@ hipError_t launch_rows_split(GemmArgs g, bool lora, Launch launch) {
   g.M = M1;
   g2.X += (int64_t)M1 * g.ldx;
   g2.Y += (int64_t)M1 * g.ldy;
-  if (g.mx.x) g2.mx.x += (int64_t)M1 * g.mx.ldx;
   if (lora) {
     g2.row_segment += M1;
     g2.H += (int64_t)M1 * g.r_max;

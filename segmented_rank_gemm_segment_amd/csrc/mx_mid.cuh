@@ -22,7 +22,7 @@
 namespace lora {
 namespace {
 
-template <bool XMX, bool LORA, bool DORA>
+template <bool XMX, bool LORA, bool DORA, bool GROUPED = false>
 __global__ __launch_bounds__(512) void mx_mid_kernel(GemmArgs g) {
   constexpr int BM = 64, BN = 64, KG = 4, NST = 3;
   constexpr int KS = XMX ? 512 : 256;               // K of a stage
@@ -40,10 +40,24 @@ __global__ __launch_bounds__(512) void mx_mid_kernel(GemmArgs g) {
   const int tid = threadIdx.x, l = tid & (kWave - 1), h = l >> 5;
   const int wid = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int kg = wid / 2, wn = wid % 2;
-  const int M = g.M, N = g.N, K = g.K;
-  int mi = 0, ni = 0;
-  if (!tile_order(blockIdx.x, (M + BM - 1) / BM, (N + BN - 1) / BN, -1, mi, ni)) return;
-  const int m0 = mi * BM, n0 = ni * BN;
+  const int N = g.N, K = g.K;
+  int M = g.M, tiles_m = (M + BM - 1) / BM, mi = 0, ni = 0;
+  ExpertTiles et{0, 0, 0};
+  if constexpr (GROUPED) {
+    et = expert_tiles<BM, 512>(g.ex, reinterpret_cast<int *>(smem));
+    tiles_m = et.total;
+  }
+  if (!tile_order(blockIdx.x, tiles_m, (N + BN - 1) / BN, -1, mi, ni)) return;
+  int m0 = mi * BM;
+  const int n0 = ni * BN;
+  // the experts' product: rows [m0, M) are the tile's expert's, W its weight
+  const unsigned char *W = reinterpret_cast<const unsigned char *>(g.W), *SW = g.mx.w;
+  if constexpr (GROUPED) {
+    int e;
+    expert_of_tile<BM, 512>(g.ex, et, mi, reinterpret_cast<int *>(smem), e, m0, M);
+    W += (int64_t)e * g.ex.w_stride;
+    SW += (int64_t)e * g.ex.s_stride;
+  }
 
   // row of this thread's outputs
   const int e_row = tid / 8, e_c8 = tid % 8 * 8;
@@ -51,23 +65,32 @@ __global__ __launch_bounds__(512) void mx_mid_kernel(GemmArgs g) {
   if constexpr (LORA) e_seg = g.row_segment[min(m0 + e_row, M - 1)];
 
   // Loads, rows past the ends clamped to the last: 32-bit offsets from the
-  // tile's first rows (leading dimensions are below 2^22 elements).
+  // tile's first rows (leading dimensions are below 2^22 elements); the experts'
+  // X rows lie anywhere and take an address each.
   const uint32_t sbase = lds_offset(smem);
   const int64_t ldxb = XMX ? g.ldx : g.ldx * 2, ldwb = g.ldw / 2;
-  const unsigned char *const xb = reinterpret_cast<const unsigned char *>(g.X) + (int64_t)m0 * ldxb;
-  const unsigned char *const wb = reinterpret_cast<const unsigned char *>(g.W) + (int64_t)n0 * ldwb;
+  const unsigned char *const xb =
+      reinterpret_cast<const unsigned char *>(g.X) + (GROUPED ? 0 : (int64_t)m0 * ldxb);
+  const unsigned char *const wb = W + (int64_t)n0 * ldwb;
   constexpr int XCH = XR / 16, WCH = WR / 16;       // 16-byte chunks per row
   // physical chunk of logical chunk c in row r: 16 rows' reads of one chunk hit 16
   // bank groups
   auto xsw = [](int c, int r) { return c ^ (r & 15); };
   auto wsw = [](int c, int r) { return WCH >= 16 ? c ^ (r & 15) : c ^ ((r >> 1) & 7); };
   uint32_t xoff[XI], woff[WI];
+  const unsigned char *xrow[GROUPED ? XI : 1];
   int xc[XI], wc[WI];                               // logical chunks
 #pragma unroll
   for (int i = 0; i < XI; ++i) {
     const int r = ((wid * XI + i) * 64 + l) / XCH;
     xc[i] = xsw(l % XCH, r);
-    xoff[i] = (uint32_t)min(r, M - 1 - m0) * (uint32_t)ldxb + xc[i] * 16;
+    if constexpr (GROUPED) {
+      const int p = min(m0 + r, M - 1);
+      xrow[i] = xb + (g.ex.sorted_choice ? g.ex.sorted_choice[p] / g.ex.top_k : p) * ldxb;
+      xoff[i] = xc[i] * 16;
+    } else {
+      xoff[i] = (uint32_t)min(r, M - 1 - m0) * (uint32_t)ldxb + xc[i] * 16;
+    }
   }
 #pragma unroll
   for (int i = 0; i < WI; ++i) {
@@ -80,7 +103,7 @@ __global__ __launch_bounds__(512) void mx_mid_kernel(GemmArgs g) {
   const int si = wid % (SR * WPR / 64), srow = (si * 64 + l) / WPR, sword = l % WPR;
   const unsigned char *const sp =
       XMX && srow < BM ? g.mx.x + (int64_t)min(m0 + srow, M - 1) * g.mx.ldx
-                       : g.mx.w + (int64_t)min(n0 + srow - (SR - BN), N - 1) * g.mx.ldw;
+                       : SW + (int64_t)min(n0 + srow - (SR - BN), N - 1) * g.mx.ldw;
   const int blocks = K / 32;
   constexpr int XE = XMX ? 32 : 8;                  // K of an X chunk
   auto issue = [&](int k, int buf) __attribute__((always_inline)) {
@@ -88,9 +111,14 @@ __global__ __launch_bounds__(512) void mx_mid_kernel(GemmArgs g) {
     const uint32_t st = sbase + buf * STAGE;
     const int k0 = k * KS;
 #pragma unroll
-    for (int i = 0; i < XI; ++i)
-      dma16_s(__builtin_amdgcn_readfirstlane(st + (wid * XI + i) * 1024),
-              xoff[i] - (k0 + xc[i] * XE >= K ? xc[i] * 16 : 0), xb + (int64_t)k * XR);
+    for (int i = 0; i < XI; ++i) {
+      const uint32_t dst = __builtin_amdgcn_readfirstlane(st + (wid * XI + i) * 1024);
+      const uint32_t off = xoff[i] - (k0 + xc[i] * XE >= K ? xc[i] * 16 : 0);
+      if constexpr (GROUPED)
+        dma16(dst, xrow[i] + (int64_t)k * XR + off);
+      else
+        dma16_s(dst, off, xb + (int64_t)k * XR);
+    }
 #pragma unroll
     for (int i = 0; i < WI; ++i)
       dma16_s(__builtin_amdgcn_readfirstlane(st + WOFF + (wid * WI + i) * 1024),
@@ -237,6 +265,19 @@ hipError_t launch_mx_mid(const GemmArgs &g, bool lora, hipStream_t stream) {
     }
   }
   hipLaunchKernelGGL((mx_mid_kernel<XMX, false, false>), grid, block, 0, stream, g);
+  return hipGetLastError();
+}
+
+// Workgroups for an experts' product of up to tiles_m M-tiles: they find the
+// number there are themselves, and either tile order of it has to fit.
+inline int expert_grid(int tiles_m, int tiles_n) {
+  const int split = tiles_m < kHeavyMaxTilesM ? tiles_m : kHeavyMaxTilesM;
+  const int a = (tiles_m * tiles_n + 7) / 8 * 8, b = 8 * ((tiles_n + 7) / 8) * split;
+  return a > b ? a : b;
+}
+inline hipError_t launch_experts_mid(const GemmArgs &g, int tiles_m, hipStream_t stream) {
+  hipLaunchKernelGGL((mx_mid_kernel<false, false, false, true>),
+                     dim3(expert_grid(tiles_m, (g.N + 63) / 64)), dim3(512), 0, stream, g);
   return hipGetLastError();
 }
 
