@@ -2,21 +2,26 @@
 // and for the experts' decode products (a few rows on each expert's weight).
 //
 // Bound by reading W (17/32 byte a weight) from HBM, so W goes from memory
-// straight to registers and each byte is read once: a workgroup takes 16 NT rows
-// of W, its KW waves every KW-th 256 codes of K, and their sums meet in LDS at
-// the end.  A wave works in half steps of 128 codes: lane l holds row l % 16 of
-// each 16-row tile and block l / 16 of the half step's four 32-code blocks (16
-// bytes, one scale); the two half steps of a row make whole 128-byte lines.  A
-// block feeds four v_mfma_f32_16x16x32_bf16 with 8 codes widened to bf16 under
-// its scale (exact); the K order inside is the same permutation for X, whose
-// rows are the MFMA's columns: 16 MT of them.  A half step's loads are issued
-// before the products of the one before it; registers for two workgroups of
-// eight waves on a CU.
+// straight to registers: a workgroup takes NT tiles of W rows, its KW waves every
+// KW-th 256 codes of K, and their sums meet in LDS at the end.  A block of 32
+// codes is a lane's 16 bytes; it feeds four v_mfma_f32_16x16x32_bf16 with 8 codes
+// each widened to bf16 under the block's scale (exact), and the K order inside
+// is the same permutation for X, whose rows are the MFMA's columns.
 //
-// 1 x 8192 -> 28672 (125 MB): 35.4 us, 3.5 TB/s; 28 us where W's rows are not a
-// power of two apart (such rows share few cache sets, so the second half of a
-// line is often fetched again).  64 x 8 choices on 128 experts of 2048 -> 1536
-// (212 MB): 58 us.  Non-temporal loads of W lose the half lines: 41 us.
+// KP 1: a tile is 16 rows of W and up to 16 MT of X; a load takes 64 bytes of each
+// W row, half of its 128-byte line, and the next load the other half.
+// KP 2: up to 8 rows of X, whose columns the MFMA has twice over.  A tile is 8
+// rows of W, a load takes their whole 128-byte lines: the MFMA's rows (and
+// columns) 0 to 7 are the tile's (and X's) rows at the first 128 codes of K, 8 to
+// 15 the same rows at the next 128; D[r][m] + D[r + 8][m + 8] is the sum, and the
+// mixed quarters go unused.
+// The next loads are issued before a load's products; registers for two
+// workgroups of eight waves on a CU.
+//
+// 1 x 8192 -> 28672 (125 MB): 28.1 us, 4.5 TB/s (KP 1: 35.4, as W's rows, a power of
+// two apart, share few cache sets and the second half of a line was often fetched
+// again); 16 rows 45 us.  Non-temporal loads of W, which lose half lines: 41 us
+// with KP 1.  64 x 8 choices on 128 experts of 2048 -> 1536 (212 MB): 58 us.
 #pragma once
 
 #include "gemm_tile.cuh"
@@ -24,16 +29,16 @@
 namespace lora {
 namespace {
 
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-
 template <int NT, int MT>
-struct StreamHalf {
+struct StreamLoad {
   u32x4 w[NT], x[MT][4];
+  uint32_t sc[NT];
 };
 
-template <int NT, int KW, int MT, bool GROUPED, bool LORA, bool DORA>
+template <int NT, int KW, int MT, int KP, bool GROUPED, bool LORA, bool DORA>
 __global__ __launch_bounds__(KW *kWave, MT == 1 ? 4 : 2) void mx_stream_kernel(GemmArgs g) {
-  constexpr int T = KW * kWave, BN = 16 * NT, BM = 16 * MT;
+  constexpr int T = KW * kWave, RW = 16 / KP, BN = RW * NT, XM = 16 / KP, BM = XM * MT;
+  static_assert(KP == 1 || (KP == 2 && MT == 1), "K parts");
   __shared__ __align__(16) float red[KW][NT][kWave * 4];
   const int tid = threadIdx.x, l = tid & (kWave - 1);
   const int wid = __builtin_amdgcn_readfirstlane(tid / kWave);
@@ -52,33 +57,41 @@ __global__ __launch_bounds__(KW *kWave, MT == 1 ? 4 : 2) void mx_stream_kernel(G
     SW += (int64_t)e * g.ex.s_stride;
   }
   const int n0 = n_idx * BN;
-  const int rows = min(m1 - m0, BM), parts = (rows + 15) / 16;
+  const int rows = min(m1 - m0, BM), parts = (rows + XM - 1) / XM;
 
-  // this lane's W rows and X row (rows past the ends read the last one)
-  const int r16 = l & 15, gq = l >> 4;
-  const unsigned char *wp[NT], *sp[NT];
+  // this lane's W rows and X rows (rows past the ends read the last one), from
+  // its block of a load's K on
+  const int rw = l & (RW - 1), kp = (l & 15) / RW, gq = l >> 4, kb = kp * 128 + gq * 32;
+  const unsigned char *const wb = W + (int64_t)n0 * (g.ldw / 2), *const sb = SW + (int64_t)n0 * g.mx.ldw;
+  uint32_t wo[NT], so[NT];
 #pragma unroll
   for (int j = 0; j < NT; ++j) {
-    const int row = min(n0 + j * 16 + r16, N - 1);
-    wp[j] = W + (int64_t)row * (g.ldw / 2) + gq * 16;
-    sp[j] = SW + (int64_t)row * g.mx.ldw;
+    const uint32_t row = min(j * RW + rw, N - 1 - n0);
+    wo[j] = row * (uint32_t)(g.ldw / 2) + kb / 2;
+    so[j] = row * (uint32_t)g.mx.ldw;
   }
   const bf16_t *xp[MT];
 #pragma unroll
   for (int i = 0; i < MT; ++i) {
-    const int p = m0 + min(i * 16 + r16, rows - 1);
+    const int p = m0 + min(i * XM + rw, rows - 1);
     const int row = GROUPED && g.ex.sorted_choice ? g.ex.sorted_choice[p] / g.ex.top_k : p;
-    xp[i] = g.X + (int64_t)row * g.ldx + gq * 32;
+    xp[i] = g.X + (int64_t)row * g.ldx + kb;
   }
   const int steps = (K + 255) / 256, last_word = (K / 32 - 1) / 4;
-  // half step b of step s: blocks past K read their row's start, their X is
-  // zeroed and their scale 1 (a NaN would spoil the zeros)
-  auto load = [&](StreamHalf<NT, MT> &t, int s, int b) __attribute__((always_inline)) {
-    const int k = s * 256 + b * 128;
-    const bool in = k + gq * 32 < K;
-    const int kx = in ? k : -gq * 32;
+  const int mine = (steps - wid + KW - 1) / KW;     // steps of this wave (negative: none)
+  const int loads = KP == 1 ? 2 * mine : mine;
+  auto k_of = [&](int p) { return KP == 1 ? ((p >> 1) * KW + wid) * 256 + (p & 1) * 128 : (p * KW + wid) * 256; };
+  // blocks past K read their row's start, their X is zeroed and their scale 1 (a
+  // NaN would spoil the zeros)
+  auto load = [&](StreamLoad<NT, MT> &t, int p) __attribute__((always_inline)) {
+    const int k = k_of(p);
+    const bool in = k + kb < K;
+    const int kx = in ? k : -kb;
 #pragma unroll
-    for (int j = 0; j < NT; ++j) t.w[j] = *reinterpret_cast<const u32x4 *>(wp[j] + kx / 2);
+    for (int j = 0; j < NT; ++j) {
+      t.w[j] = *reinterpret_cast<const u32x4 *>(wb + (wo[j] + (uint32_t)(kx / 2)));
+      t.sc[j] = *reinterpret_cast<const uint32_t *>(sb + (so[j] + 4 * (uint32_t)min(k / 128 + kp, last_word)));
+    }
 #pragma unroll
     for (int i = 0; i < MT; ++i)
 #pragma unroll
@@ -87,24 +100,16 @@ __global__ __launch_bounds__(KW *kWave, MT == 1 ? 4 : 2) void mx_stream_kernel(G
         t.x[i][kk] = in ? v : u32x4{0, 0, 0, 0};
       }
   };
-  auto load_scales = [&](u32x2 (&sc)[NT], int s) __attribute__((always_inline)) {
-#pragma unroll
-    for (int j = 0; j < NT; ++j)
-#pragma unroll
-      for (int b = 0; b < 2; ++b)
-        sc[j][b] = *reinterpret_cast<const uint32_t *>(sp[j] + min(s * 2 + b, last_word) * 4);
-  };
   f32x4 acc[NT][MT];
 #pragma unroll
   for (int j = 0; j < NT; ++j)
 #pragma unroll
     for (int i = 0; i < MT; ++i) acc[j][i] = f32x4{0.f, 0.f, 0.f, 0.f};
-  auto multiply = [&](const StreamHalf<NT, MT> &t, const u32x2 (&sc)[NT], int s, int b)
-                      __attribute__((always_inline)) {
-    const bool in = s * 256 + b * 128 + gq * 32 < K;
+  auto multiply = [&](const StreamLoad<NT, MT> &t, int p) __attribute__((always_inline)) {
+    const bool in = k_of(p) + kb < K;
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
-      const float f = in ? __uint_as_float((sc[j][b] >> (gq * 8) & 0xffu) << 23) : 1.f;
+      const float f = in ? __uint_as_float((t.sc[j] >> (gq * 8) & 0xffu) << 23) : 1.f;
 #pragma unroll
       for (int kk = 0; kk < 4; ++kk) {
         const mfma_bf16x8 w = fp4x8_to_bf16x8(t.w[j][kk], f);
@@ -115,29 +120,17 @@ __global__ __launch_bounds__(KW *kWave, MT == 1 ? 4 : 2) void mx_stream_kernel(G
     }
   };
 
-  StreamHalf<NT, MT> h0, h1;
-  u32x2 sc0[NT], sc1[NT];
-  int s = wid;
-  if (s < steps) {
-    load_scales(sc0, s);
-    load(h0, s, 0);
-  }
-  for (; s < steps; s += KW) {
-    load(h1, s, 1);
-    multiply(h0, sc0, s, 0);
-    const bool more = s + KW < steps;
-    if (more) {
-      load_scales(sc1, s + KW);
-      load(h0, s + KW, 0);
-    }
-    multiply(h1, sc0, s, 1);
-    if (more)
-#pragma unroll
-      for (int j = 0; j < NT; ++j) sc0[j] = sc1[j];
+  StreamLoad<NT, MT> a, b;
+  if (loads > 0) load(a, 0);
+  for (int p = 0; p < loads; p += 2) {
+    if (p + 1 < loads) load(b, p + 1);
+    multiply(a, p);
+    if (p + 2 < loads) load(a, p + 2);
+    if (p + 1 < loads) multiply(b, p + 1);
   }
 
-  // the waves' sums, 16 rows of X at a time: slot (j, lane) holds columns
-  // [16 j + 4 (lane / 16), +4) of row lane % 16
+  // the waves' sums, XM rows of X at a time: slot (j, lane) holds W rows
+  // [4 (lane / 16), +4) of the MFMA's 16 and its column lane % 16
 #pragma unroll
   for (int i = 0; i < MT; ++i) {
     if (i >= parts) break;
@@ -145,22 +138,25 @@ __global__ __launch_bounds__(KW *kWave, MT == 1 ? 4 : 2) void mx_stream_kernel(G
     for (int j = 0; j < NT; ++j)
       *reinterpret_cast<f32x4 *>(&red[wid][j][l * 4]) = acc[j][i];
     __syncthreads();
-    // a thread finishes 8 columns: two neighbouring slots
-    for (int q = tid; q < NT * 32; q += T) {
-      const int j = q / 32, r = q % 16, h = q / 16 % 2;
+    // a thread finishes 8 columns of one row
+    for (int q = tid; q < NT * XM * (RW / 8); q += T) {
+      const int r = q % XM, h = q / XM % (RW / 8), j = q / (XM * (RW / 8));
       float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int w = 0; w < KW; ++w) {
-        const f32x4 a = *reinterpret_cast<const f32x4 *>(&red[w][j][(r + 32 * h) * 4]);
-        const f32x4 b = *reinterpret_cast<const f32x4 *>(&red[w][j][(r + 32 * h + 16) * 4]);
+      for (int w = 0; w < KW; ++w)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          o[e] += a[e];
-          o[4 + e] += b[e];
+        for (int c = 0; c < KP; ++c) {
+          const int at = r + c * XM + 16 * (c * (4 / KP) + 2 * h);
+          const f32x4 lo = *reinterpret_cast<const f32x4 *>(&red[w][j][at * 4]);
+          const f32x4 hi = *reinterpret_cast<const f32x4 *>(&red[w][j][(at + 16) * 4]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            o[e] += lo[e];
+            o[4 + e] += hi[e];
+          }
         }
-      }
-      const int row = m0 + i * 16 + r, col = n0 + j * 16 + h * 8;
-      if (row < m1 && i * 16 + r < rows && col < N) {   // N % 8 == 0: all 8 columns or none
+      const int row = m0 + i * XM + r, col = n0 + j * RW + h * 8;
+      if (i * XM + r < rows && col < N) {           // N % 8 == 0: all 8 columns or none
         if constexpr (LORA) {
           const int sg = g.row_segment[row], rank = g.seg_rank[sg];
           if (rank > 0) lora_row8<DORA>(g, row, col, g.seg_slot[sg], rank, g.seg_scale[sg], o);
@@ -172,36 +168,41 @@ __global__ __launch_bounds__(KW *kWave, MT == 1 ? 4 : 2) void mx_stream_kernel(G
   }
 }
 
-template <int NT, int KW, int MT>
+template <int NT, int KW, int MT, int KP>
 hipError_t launch_stream(const GemmArgs &g, bool lora, hipStream_t stream) {
-  const dim3 grid((g.N + 16 * NT - 1) / (16 * NT)), block(KW * kWave);
+  constexpr int BN = 16 / KP * NT;
+  const dim3 grid((g.N + BN - 1) / BN), block(KW * kWave);
   if (lora && g.dora)
-    hipLaunchKernelGGL((mx_stream_kernel<NT, KW, MT, false, true, true>), grid, block, 0, stream, g);
+    hipLaunchKernelGGL((mx_stream_kernel<NT, KW, MT, KP, false, true, true>), grid, block, 0, stream, g);
   else if (lora)
-    hipLaunchKernelGGL((mx_stream_kernel<NT, KW, MT, false, true, false>), grid, block, 0, stream, g);
+    hipLaunchKernelGGL((mx_stream_kernel<NT, KW, MT, KP, false, true, false>), grid, block, 0, stream, g);
   else
-    hipLaunchKernelGGL((mx_stream_kernel<NT, KW, MT, false, false, false>), grid, block, 0, stream, g);
+    hipLaunchKernelGGL((mx_stream_kernel<NT, KW, MT, KP, false, false, false>), grid, block, 0, stream, g);
   return hipGetLastError();
 }
 
 // Most rows of a dense batch that the kernel takes.
 constexpr int kStreamRows = 32;
 
+// The widest workgroups that still give every CU one.
+template <int MT, int KP>
+hipError_t launch_stream_rows(const GemmArgs &g, bool lora, hipStream_t stream) {
+  constexpr int RW = 16 / KP;
+  if (g.N >= 4 * RW * kCUs) return launch_stream<4, 8, MT, KP>(g, lora, stream);
+  if (g.N >= 2 * RW * kCUs) return launch_stream<2, 8, MT, KP>(g, lora, stream);
+  return launch_stream<1, 8, MT, KP>(g, lora, stream);
+}
 inline hipError_t launch_mx_stream(const GemmArgs &g, bool lora, hipStream_t stream) {
-  // the widest workgroups that still give every CU one
-  const int nt = (g.N + 63) / 64 >= kCUs ? 4 : (g.N + 31) / 32 >= kCUs ? 2 : 1;
-  if (g.M <= 16)
-    return nt == 4   ? launch_stream<4, 8, 1>(g, lora, stream)
-           : nt == 2 ? launch_stream<2, 8, 1>(g, lora, stream)
-                     : launch_stream<1, 8, 1>(g, lora, stream);
-  return nt == 4   ? launch_stream<4, 8, 2>(g, lora, stream)
-         : nt == 2 ? launch_stream<2, 8, 2>(g, lora, stream)
-                   : launch_stream<1, 8, 2>(g, lora, stream);
+  if (g.M <= 8) return launch_stream_rows<1, 2>(g, lora, stream);
+  if (g.M <= 16) return launch_stream_rows<1, 1>(g, lora, stream);
+  return launch_stream_rows<2, 1>(g, lora, stream);
 }
 
-inline hipError_t launch_experts_stream(const GemmArgs &g, int tiles_m, hipStream_t stream) {
-  const int64_t tn = (g.N + 63) / 64;
-  hipLaunchKernelGGL((mx_stream_kernel<4, 4, 1, true, false, false>), dim3((unsigned)(tn * tiles_m)),
+template <int NT, int KP>
+hipError_t launch_experts_stream(const GemmArgs &g, int tiles_m, hipStream_t stream) {
+  constexpr int BN = 16 / KP * NT;
+  const int64_t tn = (g.N + BN - 1) / BN;
+  hipLaunchKernelGGL((mx_stream_kernel<NT, 4, 1, KP, true, false, false>), dim3((unsigned)(tn * tiles_m)),
                      dim3(4 * kWave), 0, stream, g);
   return hipGetLastError();
 }
