@@ -676,7 +676,7 @@ def _launch_stream(stream, *tensors):
     else:
         dev, handle = stream.device.index, stream.cuda_stream
     for t in tensors:
-        if t is not None and (not t.is_cuda or t.get_device() != dev):
+        if t is not None and t.get_device() != dev:        # (-1 for host memory)
             raise ValueError(f"tensor on {t.device}, the call's stream is on cuda:{dev}")
     return handle
 

@@ -447,13 +447,18 @@ __device__ __forceinline__ int heavier_end_tile(const int32_t *row_segment, int 
 // again on return.
 struct ExpertTiles {
   int first, count, total;
+  int off0, off1;    // the rows of the share's last expert
 };
 template <int BM, int T>
 __device__ __forceinline__ ExpertTiles expert_tiles(const ExpertView &ex, int *s) {
   const int E = ex.n_experts, ept = (E + T - 1) / T;
   const int e0 = threadIdx.x * ept, e1 = min(E, e0 + ept);
-  int n = 0;
-  for (int e = e0; e < e1; ++e) n += (ex.off[e + 1] - ex.off[e] + BM - 1) / BM;
+  int n = 0, off0 = 0, off1 = 0;
+  for (int e = e0; e < e1; ++e) {
+    off0 = ex.off[e];
+    off1 = ex.off[e + 1];
+    n += (off1 - off0 + BM - 1) / BM;
+  }
   int inc = n;
 #pragma unroll
   for (int o = 1; o < kWave; o <<= 1) {
@@ -468,7 +473,7 @@ __device__ __forceinline__ ExpertTiles expert_tiles(const ExpertView &ex, int *s
     total += s[w];
   }
   __syncthreads();
-  return ExpertTiles{before + inc - n, n, total};
+  return ExpertTiles{before + inc - n, n, total, off0, off1};
 }
 // M-tile m (< total): its expert and its sorted rows [p0, p1).
 template <int BM, int T>
@@ -476,15 +481,18 @@ __device__ __forceinline__ void expert_of_tile(const ExpertView &ex, const Exper
                                                int *s, int &e, int &p0, int &p1) {
   if (m >= et.first && m < et.first + et.count) {
     const int E = ex.n_experts, ept = (E + T - 1) / T;
-    int i = threadIdx.x * ept, at = m - et.first;
-    for (;; ++i) {                                  // ends: the share holds tile m
-      const int n = (ex.off[i + 1] - ex.off[i] + BM - 1) / BM;
+    int i = threadIdx.x * ept, at = m - et.first, o0 = et.off0, o1 = et.off1;
+    while (ept > 1) {                               // ends: the share holds tile m
+      o0 = ex.off[i];
+      o1 = ex.off[i + 1];
+      const int n = (o1 - o0 + BM - 1) / BM;
       if (at < n) break;
       at -= n;
+      ++i;
     }
     s[0] = i;
-    s[1] = ex.off[i] + at * BM;
-    s[2] = ex.off[i + 1];
+    s[1] = o0 + at * BM;
+    s[2] = o1;
   }
   __syncthreads();
   e = __builtin_amdgcn_readfirstlane(s[0]);

@@ -42,7 +42,7 @@ __global__ __launch_bounds__(512) void mx_mid_kernel(GemmArgs g) {
   const int kg = wid / 2, wn = wid % 2;
   const int N = g.N, K = g.K;
   int M = g.M, tiles_m = (M + BM - 1) / BM, mi = 0, ni = 0;
-  ExpertTiles et{0, 0, 0};
+  ExpertTiles et{};
   if constexpr (GROUPED) {
     et = expert_tiles<BM, 512>(g.ex, reinterpret_cast<int *>(smem));
     tiles_m = et.total;
