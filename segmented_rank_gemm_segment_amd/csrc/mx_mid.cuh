@@ -8,7 +8,9 @@
 // 256 (512 codes): every load instruction covers whole 128-byte lines, and three
 // stages fill the LDS.  Four K groups of two waves take a quarter of a stage each
 // (a wave all 64 rows and 32 columns of it), so a stage costs one barrier for
-// 512 bytes of K; their sums meet in LDS, where each thread then finishes 8
+// 512 bytes of K (stages are loaded by waves 0-3 and 4-7 in turn, so a wave waits
+// for all of its loads, one stage's, and no wait depends on the order in which
+// they complete); their sums meet in LDS, where each thread then finishes 8
 // columns of one row with its LoRA term, in fp32, and one rounding.
 //
 // 256 x 4096 x 4096: 13.9 us (16.6 on the tiles of the bf16 product), with a
@@ -27,19 +29,20 @@ __global__ __launch_bounds__(512) void mx_mid_kernel(GemmArgs g) {
   constexpr int BM = 64, BN = 64, KG = 4, NST = 3;
   constexpr int KS = XMX ? 512 : 256;               // K of a stage
   constexpr int XR = XMX ? 256 : 512, WR = KS / 2;  // bytes of an X and a W row in it
-  constexpr int XI = BM * XR / 1024 / 8, WI = BN * WR / 1024 / 8;   // loads per wave
+  constexpr int XI = BM * XR / 1024 / 4, WI = BN * WR / 1024 / 4;   // an owner's loads
   constexpr int WPR = KS / 128;                     // scale words per row
   constexpr int SR = XMX ? BM + BN : BN;            // rows with scales (X rows first)
   constexpr int WOFF = BM * XR, SOFF = WOFF + BN * WR, STAGE = SOFF + SR * WPR * 4;
-  constexpr int PER = XI + WI + 1;                  // and one of scales
+  constexpr int SL = SR * WPR / 64, SI = (SL + 3) / 4;   // scales: of a stage, of an owner
   constexpr int RS = BN + 4;
-  static_assert(SR * WPR % 64 == 0 && SR * WPR / 64 <= 8 && 8 % (SR * WPR / 64) == 0, "scale loads");
-  static_assert(NST * STAGE <= 160 * 1024 && KG * BM * RS * 4 <= NST * STAGE, "LDS");
+  static_assert(SR * WPR % 64 == 0 && (SL % 4 == 0 || 4 % SL == 0) && 64 % WPR == 0, "scale loads");
+  static_assert(NST == 3 && NST * STAGE <= 160 * 1024 && KG * BM * RS * 4 <= NST * STAGE, "LDS");
   __shared__ __align__(16) unsigned char smem[NST * STAGE];
 
   const int tid = threadIdx.x, l = tid & (kWave - 1), h = l >> 5;
   const int wid = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int kg = wid / 2, wn = wid % 2;
+  const int grp = wid / 4, w4 = wid % 4;            // owner of the stages k with k % 2 == grp
   const int N = g.N, K = g.K;
   int M = g.M, tiles_m = (M + BM - 1) / BM, mi = 0, ni = 0;
   ExpertTiles et{};
@@ -82,7 +85,7 @@ __global__ __launch_bounds__(512) void mx_mid_kernel(GemmArgs g) {
   int xc[XI], wc[WI];                               // logical chunks
 #pragma unroll
   for (int i = 0; i < XI; ++i) {
-    const int r = ((wid * XI + i) * 64 + l) / XCH;
+    const int r = ((w4 * XI + i) * 64 + l) / XCH;
     xc[i] = xsw(l % XCH, r);
     if constexpr (GROUPED) {
       const int p = min(m0 + r, M - 1);
@@ -94,16 +97,21 @@ __global__ __launch_bounds__(512) void mx_mid_kernel(GemmArgs g) {
   }
 #pragma unroll
   for (int i = 0; i < WI; ++i) {
-    const int r = ((wid * WI + i) * 64 + l) / WCH;
+    const int r = ((w4 * WI + i) * 64 + l) / WCH;
     wc[i] = wsw(l % WCH, r);
     woff[i] = (uint32_t)min(r, N - 1 - n0) * (uint32_t)ldwb + wc[i] * 16;
   }
-  // scales: words [64 si, +64) of the stage's, SR * WPR / 64 loads that several
-  // waves repeat so that all issue as many
-  const int si = wid % (SR * WPR / 64), srow = (si * 64 + l) / WPR, sword = l % WPR;
-  const unsigned char *const sp =
-      XMX && srow < BM ? g.mx.x + (int64_t)min(m0 + srow, M - 1) * g.mx.ldx
-                       : SW + (int64_t)min(n0 + srow - (SR - BN), N - 1) * g.mx.ldw;
+  // scales: load i has words [64 si(i), +64) of the stage's (where there are fewer
+  // loads than owners, several owners load the same)
+  auto si = [&](int i) { return SL < 4 ? w4 % SL : w4 * SI + i; };
+  const int sword = l % WPR;
+  const unsigned char *sp[SI];
+#pragma unroll
+  for (int i = 0; i < SI; ++i) {
+    const int srow = (si(i) * 64 + l) / WPR;
+    sp[i] = XMX && srow < BM ? g.mx.x + (int64_t)min(m0 + srow, M - 1) * g.mx.ldx
+                             : SW + (int64_t)min(n0 + srow - (SR - BN), N - 1) * g.mx.ldw;
+  }
   const int blocks = K / 32;
   constexpr int XE = XMX ? 32 : 8;                  // K of an X chunk
   auto issue = [&](int k, int buf) __attribute__((always_inline)) {
@@ -112,7 +120,7 @@ __global__ __launch_bounds__(512) void mx_mid_kernel(GemmArgs g) {
     const int k0 = k * KS;
 #pragma unroll
     for (int i = 0; i < XI; ++i) {
-      const uint32_t dst = __builtin_amdgcn_readfirstlane(st + (wid * XI + i) * 1024);
+      const uint32_t dst = __builtin_amdgcn_readfirstlane(st + (w4 * XI + i) * 1024);
       const uint32_t off = xoff[i] - (k0 + xc[i] * XE >= K ? xc[i] * 16 : 0);
       if constexpr (GROUPED)
         dma16(dst, xrow[i] + (int64_t)k * XR + off);
@@ -121,9 +129,11 @@ __global__ __launch_bounds__(512) void mx_mid_kernel(GemmArgs g) {
     }
 #pragma unroll
     for (int i = 0; i < WI; ++i)
-      dma16_s(__builtin_amdgcn_readfirstlane(st + WOFF + (wid * WI + i) * 1024),
+      dma16_s(__builtin_amdgcn_readfirstlane(st + WOFF + (w4 * WI + i) * 1024),
               woff[i] - (k0 + wc[i] * 32 >= K ? wc[i] * 16 : 0), wb + (int64_t)k * WR);
-    dma4(__builtin_amdgcn_readfirstlane(st + SOFF + si * 256), sp + min(k * WPR + sword, (blocks - 1) / 4) * 4);
+#pragma unroll
+    for (int i = 0; i < SI; ++i)
+      dma4(__builtin_amdgcn_readfirstlane(st + SOFF + si(i) * 256), sp[i] + min(k * WPR + sword, (blocks - 1) / 4) * 4);
   };
   const int KT = (K + KS - 1) / KS;
   auto zero_tail = [&](int buf) {
@@ -132,22 +142,25 @@ __global__ __launch_bounds__(512) void mx_mid_kernel(GemmArgs g) {
 #pragma unroll
     for (int i = 0; i < XI; ++i)
       if (k0 + xc[i] * XE >= K)
-        *reinterpret_cast<u32x4 *>(st + (wid * XI + i) * 1024 + l * 16) = u32x4{0, 0, 0, 0};
+        *reinterpret_cast<u32x4 *>(st + (w4 * XI + i) * 1024 + l * 16) = u32x4{0, 0, 0, 0};
 #pragma unroll
     for (int i = 0; i < WI; ++i)
       if (k0 + wc[i] * 32 >= K)
-        *reinterpret_cast<u32x4 *>(st + WOFF + (wid * WI + i) * 1024 + l * 16) = u32x4{0, 0, 0, 0};
+        *reinterpret_cast<u32x4 *>(st + WOFF + (w4 * WI + i) * 1024 + l * 16) = u32x4{0, 0, 0, 0};
     // scales of blocks past K to 1: a NaN would spoil the zeros
     const int left = blocks - 4 * ((KT - 1) * WPR + sword);
     if (left < 4) {
-      uint32_t *p = reinterpret_cast<uint32_t *>(st + SOFF + si * 256 + l * 4);
       const uint32_t keep = left <= 0 ? 0u : ~0u >> (32 - 8 * left);
-      *p = (*p & keep) | (0x7f7f7f7fu & ~keep);
+#pragma unroll
+      for (int i = 0; i < SI; ++i) {
+        uint32_t *p = reinterpret_cast<uint32_t *>(st + SOFF + si(i) * 256 + l * 4);
+        *p = (*p & keep) | (0x7f7f7f7fu & ~keep);
+      }
     }
   };
 #pragma unroll
   for (int s = 0; s < NST - 1; ++s)
-    if (s < KT) issue(s, s);
+    if (s == grp && s < KT) issue(s, s);
 
   f32x16 acc[2];
 #pragma unroll
@@ -159,14 +172,13 @@ __global__ __launch_bounds__(512) void mx_mid_kernel(GemmArgs g) {
   const int wrow = wn * 32 + (l & 31);
   int buf = 0;
   auto land = [&](int kt) __attribute__((always_inline)) {
-    // stage kt has landed (loads complete in order; the next stages' may be left)
-    if (kt + NST - 1 <= KT)
-      vm_wait<(NST - 2) * PER>();
-    else
+    const bool own = (kt & 1) == grp;
+    if (own) {                                      // stage kt has landed
       vm_wait<0>();
-    if (kt + 1 == KT && K % KS != 0) zero_tail(buf);
+      if (kt + 1 == KT && K % KS != 0) zero_tail(buf);
+    }
     lgkm_barrier();                                 // it is there, stage kt - 1 has been read
-    if (kt + NST - 1 < KT) issue(kt + NST - 1, buf == 0 ? NST - 1 : buf - 1);
+    if (own && kt + NST - 1 < KT) issue(kt + NST - 1, buf == 0 ? NST - 1 : buf - 1);
   };
   auto multiply = [&]() __attribute__((always_inline)) {
     const unsigned char *st = smem + buf * STAGE;

@@ -445,3 +445,29 @@ def test_fused_lora_many_tiles(n, d_in, d_out, n_slots, r_max, runs):
     tol += 2.0 ** -8 * Y64.abs() + d_in * U * sums
     assert bool(((Yf[:n, :d_out].double() - Y64).abs() <= tol).all())
     assert torch.equal(Yf[:n, :d_out][base], Yb[base])
+
+
+@pytest.mark.parametrize("n,d_in,d_out", [
+    (40, 256, 4104), (130, 512, 4096), (300, 1024, 4168), (500, 1536, 2056),
+    (2100, 64, 8200), (2100, 128, 8192), (2100, 192, 8200), (2300, 512, 8200)])
+@pytest.mark.parametrize("x_is_mx", [False, True])
+def test_short_k_fresh_operands_repeated(n, d_in, d_out, x_is_mx):
+    """One to a few stages of K on operands copied right before the call, three
+    times: a stage is read only after all of its loads have landed, cold ones
+    too, whatever order they land in."""
+    xc, xs = wl.make_mxfp4(n + 1, n, d_in, 124, 130)
+    wc, wsc = wl.make_mxfp4(d_out, d_out, d_in)
+    X64 = torch.from_numpy(oracle.decode_mxfp4(xc, xs)).to(DEV)
+    W64 = torch.from_numpy(oracle.decode_mxfp4(wc, wsc)).to(DEV)
+    Y64 = X64 @ W64.t()
+    tol = 2.0 ** -8 * Y64.abs() + d_in * U * (X64.abs() @ W64.abs().t())
+    Xb = X64.bfloat16().cpu()                       # exact: codes of 2 significant bits
+    for rep in range(3):
+        say("fresh", n, d_in, d_out, x_is_mx, rep)
+        W = packed(wc, wsc)
+        out = torch.full((n, d_out), 7.0, dtype=torch.bfloat16, device=DEV)
+        if x_is_mx:
+            srg.lora_base_gemm_mxfp4(*packed(xc, xs), *W, out)
+        else:
+            srg.lora_base_gemm_mxfp4w(Xb.to(DEV), *W, out)
+        assert bool(((out.double() - Y64).abs() <= tol).all()), rep
