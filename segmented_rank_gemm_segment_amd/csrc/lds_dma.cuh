@@ -34,10 +34,29 @@ __device__ __forceinline__ void dma16_s(uint32_t m0, uint32_t off, const void *b
                : "memory", "m0");
 }
 
+// The same unless `skip` (a wave's scalar) is other than 0.  The branch is inside the asm:
+// one that the compiler saw would split the block of products around it.
+__device__ __forceinline__ void dma16_s_unless(uint32_t skip, uint32_t m0, uint32_t off, const void *base) {
+  asm volatile("s_cmp_lg_u32 %0, 0\n\ts_cbranch_scc1 .Ldma16_skip_%=\n\ts_mov_b32 m0, %1\n\t"
+               "global_load_lds_dwordx4 %2, %3\n.Ldma16_skip_%=:" ::"s"(skip), "s"(m0), "v"(off), "s"(base)
+               : "memory", "m0", "scc");
+}
+
 __device__ __forceinline__ void dma4_s(uint32_t m0, uint32_t off, const void *base) {
   asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dword %1, %2" ::"s"(m0), "v"(off), "s"(base)
                : "memory", "m0");
 }
+__device__ __forceinline__ void dma4_s_unless(uint32_t skip, uint32_t m0, uint32_t off, const void *base) {
+  asm volatile("s_cmp_lg_u32 %0, 0\n\ts_cbranch_scc1 .Ldma4_skip_%=\n\ts_mov_b32 m0, %1\n\t"
+               "global_load_lds_dword %2, %3\n.Ldma4_skip_%=:" ::"s"(skip), "s"(m0), "v"(off), "s"(base)
+               : "memory", "m0", "scc");
+}
+__device__ __forceinline__ void dma16_unless(uint32_t skip, uint32_t m0, const void *src) {
+  asm volatile("s_cmp_lg_u32 %0, 0\n\ts_cbranch_scc1 .Ldma16v_skip_%=\n\ts_mov_b32 m0, %1\n\t"
+               "global_load_lds_dwordx4 %2, off\n.Ldma16v_skip_%=:" ::"s"(skip), "s"(m0), "v"(src)
+               : "memory", "m0", "scc");
+}
+
 // One dword per lane: 64 lanes x 4 bytes into 256 bytes of LDS.
 __device__ __forceinline__ void dma4(uint32_t m0, const void *src) {
   asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dword %1, off" ::"s"(m0), "v"(src)

@@ -254,6 +254,31 @@ def test_experts_product_of_long_segments(n, k, E, d_in, d_out, kind):
     assert bool((Y[len(order):] == 7.0).all())
 
 
+@pytest.mark.parametrize("n,k,E,d_in,d_out", [
+    (400, 2, 20, 256, 2056), (300, 4, 40, 512, 1032), (3000, 2, 5, 64, 2056), (3000, 2, 5, 192, 2056)])
+def test_experts_product_on_fresh_operands(n, k, E, d_in, d_out):
+    """One to a few stages of K on operands copied right before the call."""
+    ids = make_ids(n + d_in, n, k, E, "uniform")
+    ref = oracle.expert_routing(ids, E)
+    order, off = ref["sorted_choice"], ref["expert_offsets"]
+    codes, scales = wl.make_mxfp4(E + d_out, E * d_out, d_in)
+    X = torch.randn(n, d_in, generator=torch.Generator().manual_seed(n)).bfloat16()
+    W64 = torch.from_numpy(oracle.decode_mxfp4(codes, scales)).to(DEV).view(E, d_out, d_in)
+    for rep in range(3):
+        ex = sorted_batch(ids, E)
+        Wq, ws = packed(codes, scales)
+        Wq = Wq.view(E, d_out, d_in // 2)
+        ws = ws.as_strided((E, d_out, d_in // 32), (d_out * ws.stride(0), ws.stride(0), 1))
+        Xd = X.to(DEV)
+        Y = torch.full((n * k, d_out), 7.0, dtype=torch.bfloat16, device=DEV)
+        srg.lora_experts_gemm_mxfp4w(Xd, ex, Wq, ws, Y)
+        for e in range(E):
+            X64 = Xd.double()[torch.from_numpy(order[off[e]:off[e + 1]] // k).long().to(DEV)]
+            Y64 = X64 @ W64[e].t()
+            tol = 2.0 ** -8 * Y64.abs() + d_in * U * (X64.abs() @ W64[e].abs().t())
+            assert bool(((Y[off[e]:off[e + 1]].double() - Y64).abs() <= tol).all()), (rep, e)
+
+
 def test_layer_run_in_a_graph():
     """An expert layer as a model calls it (sort, two products, combine, then the
     combine's gradients), captured once and replayed on new inputs, against the
