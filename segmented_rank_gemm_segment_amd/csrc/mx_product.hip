@@ -9,10 +9,11 @@
 //   global -> LDS loads three stages ahead; scales go into a ring of their own,
 //   four words a row at once where alignment allows (a word a row costs as many
 //   cache lookups as 64 bytes of codes: 671 us against 601);
-// * every wave issues the same number of loads per stage and loads complete in
-//   order, so "stage kt + 1 has landed" is vmcnt at most the loads issued after
-//   its; one barrier per stage publishes it and frees a buffer;
-// * a load between every few products: issued together behind the barrier they
+// * waves 2 b and 2 b + 1 own buffer b and alone fill it, one with X's rows, the
+//   other with W's, so a wave never has more than one stage in flight and waits
+//   for all of its loads (vmcnt(0)): no wait depends on the order in which loads
+//   complete.  One barrier per stage publishes the next and frees a buffer;
+// * a load between every two products: issued together behind the barrier they
 //   filled the load queue and held up the products (601 us against 541);
 // * workgroups are persistent, one per CU, and the ring runs on from one tile
 //   into the next: the next tile's first stages are on their way while this
@@ -69,13 +70,11 @@ __global__ __launch_bounds__(WM *WN *kWave) void mx_product_kernel(MxGemmArgs g)
   constexpr int NW = WM * WN, TM = BM / WM, TN = BN / WN, FM = TM / 32, FN = TN / 32;
   constexpr int R = BM + BN;
   constexpr int STAGES = 4, STAGE = R * 64;
-  constexpr int CI = R / 16 / NW, SI = R / 64 / NW;   // a wave's loads of codes and of scales
+  constexpr int CI = R / 2 / 16, SI = R / 2 / 64;   // an owner's loads of codes and of scales
   // scales: loaded every SPER stages into one of SBUFS buffers, SROW bytes a row
   constexpr int SPER = WIDE ? 4 : 1, SROW = 4 * SPER, SBUFS = WIDE ? 2 : STAGES, SSTAGE = R * SROW;
-  constexpr int PER = CI + (WIDE ? 0 : SI);         // loads a stage has at least
-  static_assert(R % (64 * NW) == 0 && BM % (64 * SI) == 0 && BM % (16 * CI) == 0, "load split");
+  static_assert(BM == BN && NW == 2 * STAGES && CI == 2 * FM * FN, "owners, and a load to a product");
   static_assert(STAGES * STAGE + SBUFS * SSTAGE <= 160 * 1024, "LDS");
-  static_assert((STAGES - 1) * PER <= 63 && CI <= 4, "vmcnt, places for the loads");
   __shared__ __align__(16) unsigned char smem[STAGES * STAGE + SBUFS * SSTAGE];
 
   const int tid = threadIdx.x, l = tid & (kWave - 1);
@@ -93,73 +92,67 @@ __global__ __launch_bounds__(WM *WN *kWave) void mx_product_kernel(MxGemmArgs g)
   int t_issue = xcd * per + blockIdx.x / 8;
   if (t_issue >= t_end) return;
 
-  // Loads of this wave: rows [16 CI wid, 16 CI (wid + 1)) of the stage's X and W
-  // rows, so all of one operand (and the scales of rows [64 SI wid, ...)).
+  // This wave's loads, of the stages that land in buffer `pair`: all rows of one
+  // operand.  Load i has rows 16 i + l / 4 at physical chunk l % 4, logical chunk
+  // `chunk`; rows past the end read the last one.
   const uint32_t sbase = lds_offset(smem);
-  const bool isx = wid * CI * 16 < BM, isxs = wid * SI * 64 < BM;
-  const unsigned char *const op = isx ? g.X : g.W, *const sop = isxs ? g.SX : g.SW;
-  const int64_t ldo = isx ? g.ldx : g.ldw, ldso = isxs ? g.ldsx : g.ldsw;
-  const int row0 = wid * CI * 16 - (isx ? 0 : BM), srow0 = wid * SI * 64 - (isxs ? 0 : BM);
+  const int pair = wid / 2;
+  const bool isx = wid % 2 == 0;
+  const unsigned char *const op = isx ? g.X : g.W, *const sop = isx ? g.SX : g.SW;
+  const int64_t ldo = isx ? g.ldx : g.ldw, ldso = isx ? g.ldsx : g.ldsw;
+  const int chunk = (l & 3) ^ ((l >> 4) & 3);
   const unsigned char *base = nullptr, *bases = nullptr;
-  uint32_t off[CI], soff[SI];
-  auto chunk = [&](int i) { return (l & 3) ^ ((((wid * CI + i) * 16 + l / 4) >> 2) & 3); };
+  int last = 0;
   auto aim = [&](int t) __attribute__((always_inline)) {
     int mi, ni;
     tile_at(t, tiles_m, tiles_n, mi, ni);
-    const int first = isx ? mi * BM : ni * BN, last = (isx ? g.M : g.N) - 1;
+    const int first = isx ? mi * BM : ni * BN;
+    last = (isx ? g.M : g.N) - 1 - first;
     base = op + (int64_t)first * ldo;
-#pragma unroll
-    for (int i = 0; i < CI; ++i)
-      off[i] = (uint32_t)((min(first + row0 + i * 16 + l / 4, last) - first) * (int)ldo) + chunk(i) * 16;
-    const int sfirst = isxs ? mi * BM : ni * BN, slast = (isxs ? g.M : g.N) - 1;
-    bases = sop + (int64_t)sfirst * ldso;
-#pragma unroll
-    for (int i = 0; i < SI; ++i)
-      soff[i] = (uint32_t)((min(sfirst + srow0 + i * 64 + l, slast) - sfirst) * (int)ldso);
+    bases = sop + (int64_t)first * ldso;
   };
   // The next stage to issue: stage k_issue of tile t_issue, its scales into
   // buffer s_issue where a load of them is due.
   int k_issue = 0, s_issue = 0;
-  auto issue_codes = [&](int i, int buf) __attribute__((always_inline)) {
+  auto issue_codes = [&](uint32_t skip, int i) __attribute__((always_inline)) {
     // a chunk past K reads the stage's first chunk (in bounds: it starts
     // before K) and is zeroed before use
-    uint32_t o = off[i];
-    if (ktail && k_issue == KT - 1 && k_issue * 128 + chunk(i) * 32 >= g.K) o -= chunk(i) * 16;
-    dma16_s(__builtin_amdgcn_readfirstlane(sbase + buf * STAGE + (wid * CI + i) * 1024), o,
-            base + (int64_t)k_issue * 64);
+    const int c = ktail && k_issue == KT - 1 && k_issue * 128 + chunk * 32 >= g.K ? 0 : chunk;
+    dma16_s_unless(skip, __builtin_amdgcn_readfirstlane(sbase + pair * STAGE + ((isx ? 0 : CI) + i) * 1024),
+            (uint32_t)min(i * 16 + l / 4, last) * (uint32_t)ldo + c * 16, base + (int64_t)k_issue * 64);
   };
-  auto issue_scales = [&]() __attribute__((always_inline)) {
-    if (k_issue % SPER) return;
+  auto issue_scales = [&](uint32_t skip) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < SI; ++i) {
       const uint32_t dst = __builtin_amdgcn_readfirstlane(sbase + STAGES * STAGE + s_issue * SSTAGE +
-                                                          (wid * SI + i) * 64 * SROW);
+                                                          ((isx ? 0 : SI) + i) * 64 * SROW);
+      const uint32_t off = (uint32_t)min(i * 64 + l, last) * (uint32_t)ldso;
       if constexpr (WIDE)
-        dma16_s(dst, soff[i], bases + (int64_t)k_issue * 4);
+        dma16_s_unless(skip, dst, off, bases + (int64_t)k_issue * 4);
       else
-        dma4_s(dst, soff[i], bases + (int64_t)k_issue * 4);
+        dma4_s_unless(skip, dst, off, bases + (int64_t)k_issue * 4);
     }
-    s_issue = s_issue + 1 == SBUFS ? 0 : s_issue + 1;
   };
   auto advance = [&]() __attribute__((always_inline)) {
+    if (k_issue % SPER == 0) s_issue = s_issue + 1 == SBUFS ? 0 : s_issue + 1;
     if (++k_issue == KT) {
       k_issue = 0;
       // past the last tile the ring goes round on that one, unread
       if (t_issue + stride < t_end) aim(t_issue += stride);
     }
   };
-  // the stage in buf reaches past K: its chunks there to zero, their scales to
-  // 1 (a NaN would spoil them; WIDE rows have no tail)
+  // the owner's stage in buf reaches past K: its chunks there to zero, their
+  // scales to 1 (a NaN would spoil them; WIDE rows have no tail)
   auto zero_tail = [&](int buf) {
     unsigned char *st = smem + buf * STAGE;
 #pragma unroll
     for (int i = 0; i < CI; ++i)
-      if ((KT - 1) * 128 + chunk(i) * 32 >= g.K)
-        *reinterpret_cast<u32x4 *>(st + (wid * CI + i) * 1024 + l * 16) = u32x4{0, 0, 0, 0};
+      if ((KT - 1) * 128 + chunk * 32 >= g.K)
+        *reinterpret_cast<u32x4 *>(st + ((isx ? 0 : CI) + i) * 1024 + l * 16) = u32x4{0, 0, 0, 0};
 #pragma unroll
     for (int i = 0; i < SI; ++i) {
       uint32_t *p = reinterpret_cast<uint32_t *>(smem + STAGES * STAGE + buf * SSTAGE +
-                                                 (wid * SI + i) * 256 + l * 4);
+                                                 ((isx ? 0 : SI) + i) * 256 + l * 4);
       const uint32_t keep = ~0u >> (32 - 8 * (g.K / 32 - (KT - 1) * 4));   // 1..3 blocks
       *p = (*p & keep) | (0x7f7f7f7fu & ~keep);
     }
@@ -167,11 +160,11 @@ __global__ __launch_bounds__(WM *WN *kWave) void mx_product_kernel(MxGemmArgs g)
 
   int t = t_issue;
   aim(t);
-#pragma unroll
   for (int s = 0; s < STAGES - 1; ++s) {
-    issue_scales();
+    const uint32_t skip = __builtin_amdgcn_readfirstlane(s ^ pair);
+    issue_scales(skip | k_issue % SPER);
 #pragma unroll
-    for (int i = 0; i < CI; ++i) issue_codes(i, s);
+    for (int i = 0; i < CI; ++i) issue_codes(skip, i);
     advance();
   }
 
@@ -225,57 +218,58 @@ __global__ __launch_bounds__(WM *WN *kWave) void mx_product_kernel(MxGemmArgs g)
   };
 
   int buf = 0, kt = 0;
-  vm_wait<(STAGES - 2) * PER>();
-  if (ktail && KT == 1) zero_tail(0);
+  if (pair == 0) {
+    vm_wait<0>();
+    if (ktail && KT == 1) zero_tail(0);
+  }
   lgkm_barrier();
   read_scales();
 #pragma unroll
   for (int q = 0; q < FN + FM; ++q) read1(q, smem, 0);
   zero_acc();
   // A stage in two half steps of 64 codes.  While the first is multiplied, the
-  // second's fragments are read; then stage kt + 1 has landed for everyone and
-  // its first fragments are read while the second half step is multiplied.  The
-  // loads of stage kt + 3, into the buffer of stage kt - 1, are spread over the
+  // second's fragments are read; then stage kt + 1 has landed and its first
+  // fragments are read while the second half step is multiplied.  Stage kt + 3's
+  // owners issue its loads, into the buffer of stage kt - 1, spread over the
   // products, as a wave that finds the load queue full stalls.  Nothing branches
   // among the products and their sums are pinned after each half step: the
   // compiler would otherwise move them all behind the last branch.
-  constexpr int EARLY = (CI + 1) / 2;               // loads of the first half step
   while (true) {
     const unsigned char *st = smem + buf * STAGE;
     const int nbuf = buf + 1 == STAGES ? 0 : buf + 1, obuf = buf == 0 ? STAGES - 1 : buf - 1;
-    issue_scales();
+    const uint32_t skip = __builtin_amdgcn_readfirstlane(obuf ^ pair);
     // byte 2 s of a shifted word: half step s's block of this half of the wave
 #pragma unroll
     for (int j = 0; j < FN; ++j) sa[j] = ra[j] >> sh;
 #pragma unroll
     for (int i = 0; i < FM; ++i) sb[i] = rb[i] >> sh;
+    issue_scales(skip | k_issue % SPER);
 #pragma unroll
     for (int q = 0; q < FN * FM; ++q) {
       acc[q / FM][q % FM] = mfma_mx4<0>(a[0][q / FM], b[0][q % FM], acc[q / FM][q % FM], sa[q / FM], sb[q % FM]);
       if (q < FN + FM) read1(q, st, 1);
-      if (q % 3 == 2 && q / 3 < EARLY) issue_codes(q / 3, obuf);
+      issue_codes(skip, q);
       __builtin_amdgcn_sched_barrier(0);
     }
     pin();
-    // loads complete in order: at most those of stage kt + 2 and the first of
-    // kt + 3 are left (a load of scales among them, or stores behind them, only
-    // make this wait for a little more)
-    vm_wait<PER + EARLY>();
-    const bool last = kt + 1 == KT;
-    if (!WIDE && ktail && (last ? KT == 1 : kt + 2 == KT)) zero_tail(nbuf);
+    const bool last_stage = kt + 1 == KT;
+    if (pair == nbuf) {                             // the next stage's owners: it has landed
+      vm_wait<0>();
+      if (!WIDE && ktail && (last_stage ? KT == 1 : kt + 2 == KT)) zero_tail(nbuf);
+    }
     lgkm_barrier();                                 // stage kt + 1 is there, stage kt has been read
     read_scales();                                  // (after the last stage: of a settled buffer)
 #pragma unroll
     for (int q = 0; q < FN * FM; ++q) {
       acc[q / FM][q % FM] = mfma_mx4<2>(a[1][q / FM], b[1][q % FM], acc[q / FM][q % FM], sa[q / FM], sb[q % FM]);
       if (q < FN + FM) read1(q, smem + nbuf * STAGE, 0);
-      if (q % 3 == 2 && q / 3 < CI - EARLY) issue_codes(EARLY + q / 3, obuf);
+      issue_codes(skip, FN * FM + q);
       __builtin_amdgcn_sched_barrier(0);
     }
     pin();
     advance();
     buf = nbuf;
-    if (!last) {
+    if (!last_stage) {
       ++kt;
       continue;
     }
