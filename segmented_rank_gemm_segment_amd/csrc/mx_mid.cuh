@@ -13,10 +13,10 @@
 // they complete); their sums meet in LDS, where each thread then finishes 8
 // columns of one row with its LoRA term, in fp32, and one rounding.
 //
-// 256 x 4096 x 4096: 13.9 us (16.6 on the tiles of the bf16 product), with a
-// rank-16 adapter a row 19.5 (22.8): 30 MB of B rows from memory; loading them
+// 256 x 4096 x 4096: 12.9 us (16.6 on the tiles of the bf16 product), with a
+// rank-16 adapter a row 18.9 (22.8): 30 MB of B rows from memory; loading them
 // ahead of the last stages, or of all, measured no faster.  Both operands MXFP4:
-// 7.9 us; 333 x 8192 x 1024, 96 tiles, 10.8 us (14).
+// 7.7 us; 333 x 8192 x 1024, 96 tiles, 10.3 us (14).
 #pragma once
 
 #include "gemm_tile.cuh"

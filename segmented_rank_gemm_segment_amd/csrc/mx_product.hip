@@ -9,22 +9,26 @@
 //   global -> LDS loads three stages ahead; scales go into a ring of their own,
 //   four words a row at once where alignment allows (a word a row costs as many
 //   cache lookups as 64 bytes of codes: 671 us against 601);
-// * waves 2 b and 2 b + 1 own buffer b and alone fill it, one with X's rows, the
-//   other with W's, so a wave never has more than one stage in flight and waits
-//   for all of its loads (vmcnt(0)): no wait depends on the order in which loads
-//   complete.  One barrier per stage publishes the next and frees a buffer;
-// * a load between every two products: issued together behind the barrier they
-//   filled the load queue and held up the products (601 us against 541);
+// * waves 0-3 load the even stages and waves 4-7 the odd ones, so a wave never has
+//   more than one stage in flight and waits for all of its loads (vmcnt(0)): no
+//   wait depends on the order in which loads complete (two waves to a buffer,
+//   with 16 loads each, were 6% slower).  One barrier per stage publishes the
+//   next and frees a buffer;
+// * loads spread over the products: issued together behind the barrier they fill
+//   the load queue and hold the products up, and a stage's 8 over 8 products
+//   measured 616 us against 603 over 16.  A wave whose turn it is not branches
+//   over each inside the asm: branches that the compiler sees among the products
+//   make it spill or move them;
 // * workgroups are persistent, one per CU, and the ring runs on from one tile
 //   into the next: the next tile's first stages are on their way while this
 //   tile's last products and its stores run.
 // W is the MFMA's row operand and X its column operand, so a lane ends up with
 // one row of Y and runs of columns; two lanes swap halves (v_permlane32_swap)
 // and each stores 16 bytes, without LDS, which the ring keeps.
-// 16943 x 4096 x 14336: 541 us, 3.7 PFLOP/s; 8192^3: 273 us, 4.0 PFLOP/s.  The
-// matrix pipe is 48% busy, at 1.84 GHz: the clock falls as it gets busier (1.97
-// GHz at 40%).  The loads alone take 305 us (64-byte row pieces use half of each
-// 128-byte line), the products alone 283, the stores 100.
+// 16943 x 4096 x 14336: 603-613 us, 3.3 PFLOP/s; 8192^3: 305-312 us, 3.6 PFLOP/s.
+// The clock falls as the matrix pipe gets busier (1.97 GHz at 40%, 1.84 at 48%).
+// The loads alone take 305 us (64-byte row pieces use half of each 128-byte
+// line), the products alone 283, the stores 100.
 #include "lds_dma.cuh"
 #include "lora_device.cuh"
 #include "lora_kernels.h"
@@ -70,10 +74,11 @@ __global__ __launch_bounds__(WM *WN *kWave) void mx_product_kernel(MxGemmArgs g)
   constexpr int NW = WM * WN, TM = BM / WM, TN = BN / WN, FM = TM / 32, FN = TN / 32;
   constexpr int R = BM + BN;
   constexpr int STAGES = 4, STAGE = R * 64;
-  constexpr int CI = R / 2 / 16, SI = R / 2 / 64;   // an owner's loads of codes and of scales
+  constexpr int CI = R / 16 / 4, SI = R / 64 / 4;   // an owner's loads of codes and of scales
+  constexpr int C0 = CI / 2;   // loads of codes under a stage's second half step, the rest under a first
   // scales: loaded every SPER stages into one of SBUFS buffers, SROW bytes a row
   constexpr int SPER = WIDE ? 4 : 1, SROW = 4 * SPER, SBUFS = WIDE ? 2 : STAGES, SSTAGE = R * SROW;
-  static_assert(BM == BN && NW == 2 * STAGES && CI == 2 * FM * FN, "owners, and a load to a product");
+  static_assert(BM == BN && NW == 8 && CI == FM * FN, "owners, and loads to the products");
   static_assert(STAGES * STAGE + SBUFS * SSTAGE <= 160 * 1024, "LDS");
   __shared__ __align__(16) unsigned char smem[STAGES * STAGE + SBUFS * SSTAGE];
 
@@ -92,48 +97,54 @@ __global__ __launch_bounds__(WM *WN *kWave) void mx_product_kernel(MxGemmArgs g)
   int t_issue = xcd * per + blockIdx.x / 8;
   if (t_issue >= t_end) return;
 
-  // This wave's loads, of the stages that land in buffer `pair`: all rows of one
-  // operand.  Load i has rows 16 i + l / 4 at physical chunk l % 4, logical chunk
-  // `chunk`; rows past the end read the last one.
+  // This wave's loads, of every second stage: rows of one operand.  Load i has
+  // rows [16 (CI w4 + i), +16) of the stage's (X's first), row l / 4 at physical
+  // chunk l % 4, logical chunk `chunk`; rows past the end read the last one.
   const uint32_t sbase = lds_offset(smem);
-  const int pair = wid / 2;
-  const bool isx = wid % 2 == 0;
+  const int grp = wid / 4, w4 = wid % 4;
+  const bool isx = w4 < 2;
   const unsigned char *const op = isx ? g.X : g.W, *const sop = isx ? g.SX : g.SW;
   const int64_t ldo = isx ? g.ldx : g.ldw, ldso = isx ? g.ldsx : g.ldsw;
   const int chunk = (l & 3) ^ ((l >> 4) & 3);
   const unsigned char *base = nullptr, *bases = nullptr;
-  int last = 0;
+  uint32_t off[CI], offs[SI];
   auto aim = [&](int t) __attribute__((always_inline)) {
     int mi, ni;
     tile_at(t, tiles_m, tiles_n, mi, ni);
     const int first = isx ? mi * BM : ni * BN;
-    last = (isx ? g.M : g.N) - 1 - first;
+    const int last = (isx ? g.M : g.N) - 1 - first;
+#pragma unroll
+    for (int i = 0; i < CI; ++i)
+      off[i] = (uint32_t)min((w4 % 2 * CI + i) * 16 + l / 4, last) * (uint32_t)ldo + chunk * 16;
+#pragma unroll
+    for (int i = 0; i < SI; ++i) offs[i] = (uint32_t)min((w4 % 2 * SI + i) * 64 + l, last) * (uint32_t)ldso;
     base = op + (int64_t)first * ldo;
     bases = sop + (int64_t)first * ldso;
   };
-  // The next stage to issue: stage k_issue of tile t_issue, its scales into
-  // buffer s_issue where a load of them is due.
-  int k_issue = 0, s_issue = 0;
+  // The next stage to issue: stage k_issue of tile t_issue, into buffer b_issue,
+  // its scales into buffer s_issue where a load of them is due.
+  int k_issue = 0, b_issue = 0, s_issue = 0;
   auto issue_codes = [&](uint32_t skip, int i) __attribute__((always_inline)) {
     // a chunk past K reads the stage's first chunk (in bounds: it starts
     // before K) and is zeroed before use
-    const int c = ktail && k_issue == KT - 1 && k_issue * 128 + chunk * 32 >= g.K ? 0 : chunk;
-    dma16_s_unless(skip, __builtin_amdgcn_readfirstlane(sbase + pair * STAGE + ((isx ? 0 : CI) + i) * 1024),
-            (uint32_t)min(i * 16 + l / 4, last) * (uint32_t)ldo + c * 16, base + (int64_t)k_issue * 64);
+    const uint32_t back =
+        !WIDE && ktail && k_issue == KT - 1 && k_issue * 128 + chunk * 32 >= g.K ? chunk * 16 : 0;
+    dma16_s_unless(skip, __builtin_amdgcn_readfirstlane(sbase + b_issue * STAGE + (w4 * CI + i) * 1024),
+                   off[i] - back, base + (int64_t)k_issue * 64);
   };
   auto issue_scales = [&](uint32_t skip) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < SI; ++i) {
       const uint32_t dst = __builtin_amdgcn_readfirstlane(sbase + STAGES * STAGE + s_issue * SSTAGE +
-                                                          ((isx ? 0 : SI) + i) * 64 * SROW);
-      const uint32_t off = (uint32_t)min(i * 64 + l, last) * (uint32_t)ldso;
+                                                          (w4 * SI + i) * 64 * SROW);
       if constexpr (WIDE)
-        dma16_s_unless(skip, dst, off, bases + (int64_t)k_issue * 4);
+        dma16_s_unless(skip, dst, offs[i], bases + (int64_t)k_issue * 4);
       else
-        dma4_s_unless(skip, dst, off, bases + (int64_t)k_issue * 4);
+        dma4_s_unless(skip, dst, offs[i], bases + (int64_t)k_issue * 4);
     }
   };
   auto advance = [&]() __attribute__((always_inline)) {
+    b_issue = b_issue + 1 == STAGES ? 0 : b_issue + 1;
     if (k_issue % SPER == 0) s_issue = s_issue + 1 == SBUFS ? 0 : s_issue + 1;
     if (++k_issue == KT) {
       k_issue = 0;
@@ -148,11 +159,11 @@ __global__ __launch_bounds__(WM *WN *kWave) void mx_product_kernel(MxGemmArgs g)
 #pragma unroll
     for (int i = 0; i < CI; ++i)
       if ((KT - 1) * 128 + chunk * 32 >= g.K)
-        *reinterpret_cast<u32x4 *>(st + ((isx ? 0 : CI) + i) * 1024 + l * 16) = u32x4{0, 0, 0, 0};
+        *reinterpret_cast<u32x4 *>(st + (w4 * CI + i) * 1024 + l * 16) = u32x4{0, 0, 0, 0};
 #pragma unroll
     for (int i = 0; i < SI; ++i) {
       uint32_t *p = reinterpret_cast<uint32_t *>(smem + STAGES * STAGE + buf * SSTAGE +
-                                                 ((isx ? 0 : SI) + i) * 256 + l * 4);
+                                                 (w4 * SI + i) * 256 + l * 4);
       const uint32_t keep = ~0u >> (32 - 8 * (g.K / 32 - (KT - 1) * 4));   // 1..3 blocks
       *p = (*p & keep) | (0x7f7f7f7fu & ~keep);
     }
@@ -160,8 +171,8 @@ __global__ __launch_bounds__(WM *WN *kWave) void mx_product_kernel(MxGemmArgs g)
 
   int t = t_issue;
   aim(t);
-  for (int s = 0; s < STAGES - 1; ++s) {
-    const uint32_t skip = __builtin_amdgcn_readfirstlane(s ^ pair);
+  for (int s = 0; s < 2; ++s) {
+    const uint32_t skip = __builtin_amdgcn_readfirstlane(s ^ grp);
     issue_scales(skip | k_issue % SPER);
 #pragma unroll
     for (int i = 0; i < CI; ++i) issue_codes(skip, i);
@@ -217,11 +228,14 @@ __global__ __launch_bounds__(WM *WN *kWave) void mx_product_kernel(MxGemmArgs g)
     s_read = next ? (s_read + 1 == SBUFS ? 0 : s_read + 1) : s_read;
   };
 
-  int buf = 0, kt = 0;
-  if (pair == 0) {
+  int buf = 0, kt = 0, turn = 0;                    // turn: the owner of stage kt
+  if (grp == 0) {
     vm_wait<0>();
     if (ktail && KT == 1) zero_tail(0);
   }
+  issue_scales(grp | k_issue % SPER);               // stage 2's first loads
+#pragma unroll
+  for (int i = 0; i < C0; ++i) issue_codes(grp, i);
   lgkm_barrier();
   read_scales();
 #pragma unroll
@@ -229,46 +243,48 @@ __global__ __launch_bounds__(WM *WN *kWave) void mx_product_kernel(MxGemmArgs g)
   zero_acc();
   // A stage in two half steps of 64 codes.  While the first is multiplied, the
   // second's fragments are read; then stage kt + 1 has landed and its first
-  // fragments are read while the second half step is multiplied.  Stage kt + 3's
-  // owners issue its loads, into the buffer of stage kt - 1, spread over the
-  // products, as a wave that finds the load queue full stalls.  Nothing branches
-  // among the products and their sums are pinned after each half step: the
-  // compiler would otherwise move them all behind the last branch.
+  // fragments are read while the second half step is multiplied.  Under the first
+  // half step go the rest of stage kt + 2's loads, under the second the first of
+  // stage kt + 3's, by the waves that have just waited for stage kt + 1 (into a
+  // buffer that was last read during stage kt - 1).  The sums are pinned after
+  // each half step: the compiler would otherwise move the products behind the
+  // next branch.
   while (true) {
     const unsigned char *st = smem + buf * STAGE;
-    const int nbuf = buf + 1 == STAGES ? 0 : buf + 1, obuf = buf == 0 ? STAGES - 1 : buf - 1;
-    const uint32_t skip = __builtin_amdgcn_readfirstlane(obuf ^ pair);
+    const int nbuf = buf + 1 == STAGES ? 0 : buf + 1;
+    const uint32_t skip = __builtin_amdgcn_readfirstlane(turn ^ grp);
     // byte 2 s of a shifted word: half step s's block of this half of the wave
 #pragma unroll
     for (int j = 0; j < FN; ++j) sa[j] = ra[j] >> sh;
 #pragma unroll
     for (int i = 0; i < FM; ++i) sb[i] = rb[i] >> sh;
-    issue_scales(skip | k_issue % SPER);
 #pragma unroll
     for (int q = 0; q < FN * FM; ++q) {
       acc[q / FM][q % FM] = mfma_mx4<0>(a[0][q / FM], b[0][q % FM], acc[q / FM][q % FM], sa[q / FM], sb[q % FM]);
       if (q < FN + FM) read1(q, st, 1);
-      issue_codes(skip, q);
+      if (q % 2 == 0) issue_codes(skip, C0 + q / 2);
       __builtin_amdgcn_sched_barrier(0);
     }
     pin();
     const bool last_stage = kt + 1 == KT;
-    if (pair == nbuf) {                             // the next stage's owners: it has landed
+    advance();
+    if (skip) {                                     // the next stage's owners: it has landed
       vm_wait<0>();
       if (!WIDE && ktail && (last_stage ? KT == 1 : kt + 2 == KT)) zero_tail(nbuf);
     }
     lgkm_barrier();                                 // stage kt + 1 is there, stage kt has been read
     read_scales();                                  // (after the last stage: of a settled buffer)
+    issue_scales((skip ^ 1) | k_issue % SPER);
 #pragma unroll
     for (int q = 0; q < FN * FM; ++q) {
       acc[q / FM][q % FM] = mfma_mx4<2>(a[1][q / FM], b[1][q % FM], acc[q / FM][q % FM], sa[q / FM], sb[q % FM]);
       if (q < FN + FM) read1(q, smem + nbuf * STAGE, 0);
-      issue_codes(skip, FN * FM + q);
+      if (q % 2 == 0) issue_codes(skip ^ 1, q / 2);
       __builtin_amdgcn_sched_barrier(0);
     }
     pin();
-    advance();
     buf = nbuf;
+    turn ^= 1;
     if (!last_stage) {
       ++kt;
       continue;

@@ -14,9 +14,10 @@
 // Loads spread over the products, one barrier per stage, persistent workgroups
 // and stores from registers as in the product of two MXFP4 operands.
 //
-// 16943 x 4096 x 14336: 1517 us, 1.31 PFLOP/s; 8192^3: 796 us, 1.38 PFLOP/s (a
+// 16943 x 4096 x 14336: 1578 us, 1.26 PFLOP/s; 8192^3: 837 us, 1.31 PFLOP/s (a
 // library's bf16 product reaches 1.36 and 1.17 on the same shapes).  8190 x 8
-// choices on 64 experts of 2048 -> 1536: 392 us, 1.03 PFLOP/s.
+// choices on 64 experts of 2048 -> 1536: 435 us, 0.92 PFLOP/s.  An owner's first
+// loads right after its wait, a quarter of a stage earlier, measured 8% slower.
 #pragma once
 
 #include "gemm_tile.cuh"
