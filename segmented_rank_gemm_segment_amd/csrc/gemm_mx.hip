@@ -83,11 +83,12 @@ hipError_t launch_experts_gemm_mx(const void *X, int64_t ldx, const ExpertView &
     const int64_t t = (int64_t)ex.n_choices / bm + ex.n_experts;
     return (int)(t < ex.n_choices ? t : ex.n_choices);
   };
-  // by the mean rows of an expert (16 experts of 4096 -> 4096, in us: 2 rows 28 in
-  // tiles of 8 against 38 in tiles of 16, 4 rows 36 against 39; 64 of 2048 -> 1536: 2
-  // rows 25 against 28, 4 rows 31 against 29, 8 rows 38 streamed against 64 on the 64-tiles, 24 rows 69 against 82, 16 experts of 4096
-  // -> 4096 86 against 61; 64 rows 110 on those against 100 on the 256-tiles, and 92
-  // against 104)
+  // by the mean rows of an expert, in us.  16 experts of 4096 -> 4096: 2 rows 28 in
+  // tiles of 8 against 38 in tiles of 16, 4 rows 36 against 39, 24 rows 86 streamed
+  // against 61 on the 64-tiles.  64 experts of 2048 -> 1536: 2 rows 25 against 28, 4
+  // rows 31 against 29, 8 rows 38 streamed against 64 on the 64-tiles, 24 rows 69
+  // against 82.  64 rows: 110 on the 64-tiles against 100 on the 256-tiles, and 92
+  // against 104.
   const int rows = ex.n_choices / ex.n_experts;
   if (rows <= 2) return launch_experts_stream<4, 2>(g, tiles(8), stream);
   if (rows <= 16) return launch_experts_stream<4, 1>(g, tiles(16), stream);

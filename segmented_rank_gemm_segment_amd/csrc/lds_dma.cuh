@@ -16,50 +16,52 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 // Issued through inline asm so that the compiler does not add conservative
 // waits on them; completion is tracked by hand with s_waitcnt vmcnt(0) only
 // (a wave waits for all of its loads, never for a count of them, so no wait
-// depends on the order in which loads complete).
+// depends on the order in which loads complete).  Between the write of M0 and the
+// load that reads it the ISA asks for one wait state, which the compiler does not
+// add inside asm.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ uint32_t lds_offset(const void *p) {
   return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void *)p;
 }
 
 __device__ __forceinline__ void dma16(uint32_t m0, const void *src) {
-  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(m0), "v"(src)
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(m0), "v"(src)
                : "memory", "m0");
 }
 
 // The same with the source given as a 64-bit scalar base plus a 32-bit
 // per-lane byte offset (the instruction's saddr form).
 __device__ __forceinline__ void dma16_s(uint32_t m0, uint32_t off, const void *base) {
-  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(m0), "v"(off), "s"(base)
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(m0), "v"(off), "s"(base)
                : "memory", "m0");
 }
 
 // The same unless `skip` (a wave's scalar) is other than 0.  The branch is inside the asm:
 // one that the compiler saw would split the block of products around it.
 __device__ __forceinline__ void dma16_s_unless(uint32_t skip, uint32_t m0, uint32_t off, const void *base) {
-  asm volatile("s_cmp_lg_u32 %0, 0\n\ts_cbranch_scc1 .Ldma16_skip_%=\n\ts_mov_b32 m0, %1\n\t"
+  asm volatile("s_cmp_lg_u32 %0, 0\n\ts_cbranch_scc1 .Ldma16_skip_%=\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\t"
                "global_load_lds_dwordx4 %2, %3\n.Ldma16_skip_%=:" ::"s"(skip), "s"(m0), "v"(off), "s"(base)
                : "memory", "m0", "scc");
 }
 
 __device__ __forceinline__ void dma4_s(uint32_t m0, uint32_t off, const void *base) {
-  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dword %1, %2" ::"s"(m0), "v"(off), "s"(base)
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2" ::"s"(m0), "v"(off), "s"(base)
                : "memory", "m0");
 }
 __device__ __forceinline__ void dma4_s_unless(uint32_t skip, uint32_t m0, uint32_t off, const void *base) {
-  asm volatile("s_cmp_lg_u32 %0, 0\n\ts_cbranch_scc1 .Ldma4_skip_%=\n\ts_mov_b32 m0, %1\n\t"
+  asm volatile("s_cmp_lg_u32 %0, 0\n\ts_cbranch_scc1 .Ldma4_skip_%=\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\t"
                "global_load_lds_dword %2, %3\n.Ldma4_skip_%=:" ::"s"(skip), "s"(m0), "v"(off), "s"(base)
                : "memory", "m0", "scc");
 }
 __device__ __forceinline__ void dma16_unless(uint32_t skip, uint32_t m0, const void *src) {
-  asm volatile("s_cmp_lg_u32 %0, 0\n\ts_cbranch_scc1 .Ldma16v_skip_%=\n\ts_mov_b32 m0, %1\n\t"
+  asm volatile("s_cmp_lg_u32 %0, 0\n\ts_cbranch_scc1 .Ldma16v_skip_%=\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\t"
                "global_load_lds_dwordx4 %2, off\n.Ldma16v_skip_%=:" ::"s"(skip), "s"(m0), "v"(src)
                : "memory", "m0", "scc");
 }
 
 // One dword per lane: 64 lanes x 4 bytes into 256 bytes of LDS.
 __device__ __forceinline__ void dma4(uint32_t m0, const void *src) {
-  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dword %1, off" ::"s"(m0), "v"(src)
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(m0), "v"(src)
                : "memory", "m0");
 }
 
