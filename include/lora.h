@@ -381,6 +381,7 @@ lora_status lora_linear_fused_fp8w(const void *X, int64_t ldx, const void *Wq, i
                                    const lora_segments *seg, const lora_pool *pool, void *Y,
                                    int64_t ldy, void *stream);
 
+#define LORA_MAX_MX_ROWS (1 << 28)
 /*
  * MXFP4, the OCP microscaling 4-bit format: the quantized base weight at half
  * a byte per weight (adapter-batching page, section "Quantized Base Model 与
@@ -391,7 +392,8 @@ lora_status lora_linear_fused_fp8w(const void *X, int64_t ldx, const void *Wq, i
  *   codes  uint8 [n][ldq], ldq bytes a row: >= d / 2, a multiple of 16
  *   scales uint8 [n][lds], lds bytes a row: >= d / 32, a multiple of 4
  * both 16-byte aligned, ld at most LORA_MAX_LD.  Scale bytes of a row past
- * d / 32 are read (up to the next multiple of 4) but never used.
+ * d / 32 are read (up to the next multiple of 4) but never used.  The calls take
+ * at most LORA_MAX_MX_ROWS rows (or tokens; LORA_ERR_SHAPE).
  *
  * lora_mxfp4_quantize: per block, b = max(0, floor(log2 amax) + 125) and each
  * code is x / 2^(b - 127) rounded to nearest, ties to the even code, magnitudes
@@ -453,6 +455,8 @@ lora_status lora_base_gemm_mxfp4(const void *Xq, int64_t ldx, const void *x_scal
  *   choice_position[n_tokens * top_k]  choice -> sorted row, -1 = dropped
  *   status         [1]                 choices dropped for a bad id
  *   workspace      lora_experts_workspace() bytes (NULL allowed when that is 0)
+ * The arrays are one batch's: calls on two streams need two sets or an order
+ * between them.
  */
 #define LORA_MAX_EXPERTS 1024
 #define LORA_MAX_TOP_K 64

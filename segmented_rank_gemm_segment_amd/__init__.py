@@ -675,6 +675,8 @@ def _launch_stream(stream, *tensors):
         handle = torch._C._cuda_getCurrentRawStream(dev)
     else:
         dev, handle = stream.device.index, stream.cuda_stream
+        if dev != torch.cuda.current_device():
+            raise ValueError(f"the stream is on cuda:{dev}, the current device is another")
     for t in tensors:
         if t is not None and t.get_device() != dev:        # (-1 for host memory)
             raise ValueError(f"tensor on {t.device}, the call's stream is on cuda:{dev}")

@@ -229,7 +229,7 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortArgs a) {
 // rows
 // ---------------------------------------------------------------------------
 struct RowArgs {
-  int n, k, d;
+  int n, k, d;               // n: one past the launch's last token
   const int32_t *position;   // [n][k]
   const void *in;            // gather: X.  combine: Ys.  backward: dY
   int64_t ldi;
@@ -239,6 +239,7 @@ struct RowArgs {
   void *out;                 // gather: Xs.  combine: Y.  backward: dYs or null
   int64_t ldo;
   float *dw;                 // backward: [n][k] or null
+  int first;                 // the launch's first token
 };
 
 constexpr int kRowWaves = 4;
@@ -248,7 +249,7 @@ constexpr int kRowWaves = 4;
 template <int WPT>
 __device__ __forceinline__ bool wave_token(const RowArgs &a, int64_t &i, int &part, int &pos) {
   const int w = threadIdx.x / kWave;
-  i = (int64_t)blockIdx.x * (kRowWaves / WPT) + w / WPT;
+  i = a.first + (int64_t)blockIdx.x * (kRowWaves / WPT) + w / WPT;
   part = w % WPT;
   pos = i < a.n && lane_id() < a.k ? a.position[i * a.k + lane_id()] : -1;
   return i < a.n;
@@ -373,33 +374,40 @@ bool one_wave(int d) {
   return d <= kWave * Elem<T>::kVec;
 }
 
+// Tokens of a launch at most: a grid has less than 2^32 threads.
+constexpr int kLaunchTokens = 1 << 22;
+
 template <template <typename, int> class Launch>
-void by_type(int dtype, const RowArgs &a, hipStream_t s) {
-  if (dtype == LORA_BF16) {
-    if (one_wave<bf16_t>(a.d)) Launch<bf16_t, 1>::go(a, s);
-    else Launch<bf16_t, 4>::go(a, s);
-  } else {
-    if (one_wave<float>(a.d)) Launch<float, 1>::go(a, s);
-    else Launch<float, 4>::go(a, s);
+void by_type(int dtype, RowArgs a, hipStream_t s) {
+  const int n = a.n;
+  for (a.first = 0; a.first < n; a.first += kLaunchTokens) {
+    a.n = n - a.first < kLaunchTokens ? n : a.first + kLaunchTokens;
+    if (dtype == LORA_BF16) {
+      if (one_wave<bf16_t>(a.d)) Launch<bf16_t, 1>::go(a, s);
+      else Launch<bf16_t, 4>::go(a, s);
+    } else {
+      if (one_wave<float>(a.d)) Launch<float, 1>::go(a, s);
+      else Launch<float, 4>::go(a, s);
+    }
   }
 }
 template <int WPT>
-dim3 row_grid(int n) {
-  return dim3((unsigned)(((int64_t)n * WPT + kRowWaves - 1) / kRowWaves));
+dim3 row_grid(const RowArgs &a) {
+  return dim3((unsigned)(((int64_t)(a.n - a.first) * WPT + kRowWaves - 1) / kRowWaves));
 }
 template <typename T, int WPT> struct Gather {
   static void go(const RowArgs &a, hipStream_t s) {
-    hipLaunchKernelGGL((gather_kernel<T, WPT>), row_grid<WPT>(a.n), dim3(kRowWaves * kWave), 0, s, a);
+    hipLaunchKernelGGL((gather_kernel<T, WPT>), row_grid<WPT>(a), dim3(kRowWaves * kWave), 0, s, a);
   }
 };
 template <typename T, int WPT> struct Combine {
   static void go(const RowArgs &a, hipStream_t s) {
-    hipLaunchKernelGGL((combine_kernel<T, WPT>), row_grid<WPT>(a.n), dim3(kRowWaves * kWave), 0, s, a);
+    hipLaunchKernelGGL((combine_kernel<T, WPT>), row_grid<WPT>(a), dim3(kRowWaves * kWave), 0, s, a);
   }
 };
 template <typename T, int WPT> struct CombineBackward {
   static void go(const RowArgs &a, hipStream_t s) {
-    hipLaunchKernelGGL((combine_backward_kernel<T, WPT>), row_grid<WPT>(a.n),
+    hipLaunchKernelGGL((combine_backward_kernel<T, WPT>), row_grid<WPT>(a),
                        dim3(kRowWaves * kWave), 0, s, a);
   }
 };
@@ -432,7 +440,7 @@ hipError_t launch_experts_sort(const int32_t *ids, int n_choices, int n_experts,
 
 hipError_t launch_experts_gather(const void *X, int64_t ldx, const int32_t *position, int n, int k,
                                  int d, int dtype, void *Xs, int64_t lds, hipStream_t stream) {
-  by_type<Gather>(dtype, RowArgs{n, k, d, position, X, ldx, nullptr, 0, nullptr, Xs, lds, nullptr},
+  by_type<Gather>(dtype, RowArgs{n, k, d, position, X, ldx, nullptr, 0, nullptr, Xs, lds, nullptr, 0},
                   stream);
   return hipGetLastError();
 }
@@ -440,7 +448,7 @@ hipError_t launch_experts_gather(const void *X, int64_t ldx, const int32_t *posi
 hipError_t launch_experts_combine(const void *Ys, int64_t lds, const float *w,
                                   const int32_t *position, int n, int k, int d, int dtype, void *Y,
                                   int64_t ldy, hipStream_t stream) {
-  by_type<Combine>(dtype, RowArgs{n, k, d, position, Ys, lds, nullptr, 0, w, Y, ldy, nullptr},
+  by_type<Combine>(dtype, RowArgs{n, k, d, position, Ys, lds, nullptr, 0, w, Y, ldy, nullptr, 0},
                    stream);
   return hipGetLastError();
 }
@@ -449,7 +457,7 @@ hipError_t launch_experts_combine_backward(const void *dY, int64_t ldy, const vo
                                            const float *w, const int32_t *position, int n, int k,
                                            int d, int dtype, void *dYs, int64_t ldds, float *dw,
                                            hipStream_t stream) {
-  by_type<CombineBackward>(dtype, RowArgs{n, k, d, position, dY, ldy, Ys, lds, w, dYs, ldds, dw},
+  by_type<CombineBackward>(dtype, RowArgs{n, k, d, position, dY, ldy, Ys, lds, w, dYs, ldds, dw, 0},
                            stream);
   return hipGetLastError();
 }

@@ -436,14 +436,15 @@ lora_status check_mxfp4(const void *q, int64_t ldq, const void *s, int64_t lds, 
 lora_status check_mx_convert(const void *X, int64_t ldx, int32_t n_rows, int32_t d, int32_t dtype,
                              const void *q, int64_t ldq, const void *s, int64_t lds) {
   if (!valid_dtype(dtype)) return LORA_ERR_DTYPE;
-  if (n_rows < 0 || d <= 0 || d > LORA_MAX_LD) return LORA_ERR_SHAPE;
+  if (n_rows < 0 || n_rows > LORA_MAX_MX_ROWS || d <= 0 || d > LORA_MAX_LD) return LORA_ERR_SHAPE;
   if (d % 32) return LORA_ERR_ALIGN;
   const lora_status st = check_matrix(X, ldx, d, n_rows);
   return st != LORA_OK ? st : check_mxfp4(q, ldq, s, lds, d, n_rows);
 }
 
 lora_status check_product_shape(int32_t n_rows, int32_t d_in, int32_t d_out) {
-  if (n_rows < 0 || d_in <= 0 || d_out <= 0 || d_in > LORA_MAX_LD) return LORA_ERR_SHAPE;
+  if (n_rows < 0 || n_rows > LORA_MAX_MX_ROWS || d_in <= 0 || d_out <= 0 || d_in > LORA_MAX_LD)
+    return LORA_ERR_SHAPE;
   return d_in % 32 || d_out % 8 ? LORA_ERR_ALIGN : LORA_OK;
 }
 

@@ -175,3 +175,23 @@ def test_tensor_checks():
     with pytest.raises(ValueError):
         srg.lora_experts_gemm_mxfp4w(x.bfloat16(), ex, w3[:2], torch.zeros(3, 16, 4, dtype=torch.uint8)[:2, :, :2],
                                      torch.zeros(8, 16, dtype=torch.bfloat16))
+
+
+def test_rows_past_the_limit(L):
+    big = (1 << 28) + 1
+    assert L.lora_mxfp4_quantize(P, 64, big, 64, 1, P, 32, P, 4, None) == ESHAPE
+    assert L.lora_mxfp4_dequantize(P, 32, P, 4, big, 64, 1, P, 64, None) == ESHAPE
+    assert L.lora_base_gemm_mxfp4w(P, 64, P, 32, P, 4, P, 16, big, 64, 16, None) == ESHAPE
+    assert L.lora_base_gemm_mxfp4(P, 32, P, 4, P, 32, P, 4, P, 16, big, 64, 16, None) == ESHAPE
+    ex = srg.LoraExpertsC(big, 1, 4, P, P, P, P, P)
+    assert L.lora_experts_gemm_mxfp4w(P, 64, 1, ctypes.byref(ex), P, 32, P, 4, P, 16, 64, 16,
+                                      None) == ESHAPE
+
+
+def test_stream_of_another_device(monkeypatch):
+    class Stream:
+        device, cuda_stream = torch.device("cuda", 1), 0
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    X = torch.zeros(1, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="current device"):
+        srg.lora_mxfp4_quantize(X, *srg.mxfp4_empty(1, 64, "cpu"), stream=Stream())

@@ -279,6 +279,33 @@ def test_experts_product_on_fresh_operands(n, k, E, d_in, d_out):
             assert bool(((Y[off[e]:off[e + 1]].double() - Y64).abs() <= tol).all()), (rep, e)
 
 
+@pytest.mark.parametrize("d", [8, 520])
+def test_rows_of_more_tokens_than_one_launch(d):
+    """2^22 + 3 tokens: rows move in two launches, of one and of four waves a
+    token; every row against indexing."""
+    n, k, E = (1 << 22) + 3, 1, 3
+    g = torch.Generator(DEV).manual_seed(d)
+    ids = torch.randint(-1, E, (n, k), device=DEV, generator=g, dtype=torch.int32)
+    ex = srg.Experts(n, k, E, DEV)
+    srg.lora_experts_sort(ids, ex)
+    kept = int(ex.expert_offsets[E])
+    rows = torch.argsort(torch.where(ids < 0, E, ids).view(-1), stable=True)[:kept]
+    assert torch.equal(ex.sorted_choice[:kept].long(), rows)
+    X = torch.randint(-9, 10, (n, d), device=DEV, generator=g, dtype=torch.int8).bfloat16()
+    Xs = torch.full((n, d), 7.0, dtype=torch.bfloat16, device=DEV)
+    srg.lora_experts_gather(X, ex, Xs)
+    assert torch.equal(Xs[:kept], X[rows]) and bool((Xs[kept:] == 7.0).all())
+    w = torch.randint(1, 4, (n, k), device=DEV, generator=g).float()
+    Y = torch.full((n, d), 7.0, dtype=torch.bfloat16, device=DEV)
+    srg.lora_experts_combine(Xs, w, ex, Y)                 # small integers: exact
+    wx = torch.where(ids >= 0, w, 0.0)
+    assert torch.equal(Y, (X * wx).bfloat16())
+    dYs, dw = torch.full_like(Xs, 7.0), torch.full_like(w, 7.0)
+    srg.lora_experts_combine_backward(X, Xs, w, ex, dYs, dw)
+    assert torch.equal(dYs[:kept], (X * w).bfloat16()[rows]) and bool((dYs[kept:] == 7.0).all())
+    assert torch.equal(dw, torch.where(ids >= 0, (X * X).sum(1, keepdim=True, dtype=torch.float32), 0.0))
+
+
 def test_layer_run_in_a_graph():
     """An expert layer as a model calls it (sort, two products, combine, then the
     combine's gradients), captured once and replayed on new inputs, against the
