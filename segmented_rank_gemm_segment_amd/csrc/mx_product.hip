@@ -2,33 +2,30 @@
 // to v_mfma_scale_f32_32x32x64_f8f6f4 as they are.
 //
 // At 8.6 PFLOP/s (the rate of a loop of these MFMAs on registers alone) a
-// 256 x 256 tile takes 1.2 thousand cycles for 128 codes of K and needs 34 KB of
+// 256 x 256 tile takes 2.4 thousand cycles for 256 codes of K and needs 68 KB of
 // operands for them, so the kernel lives from keeping the loads ahead:
-// * a ring of four buffers of 128 codes of K (64-byte rows, 16-byte chunks
-//   XOR-swizzled so 16 lanes' reads hit 16 bank groups), filled by direct
-//   global -> LDS loads three stages ahead; scales go into a ring of their own,
-//   four words a row at once where alignment allows (a word a row costs as many
-//   cache lookups as 64 bytes of codes: 671 us against 601);
-// * waves 0-3 load the even stages and waves 4-7 the odd ones, so a wave never has
-//   more than one stage in flight and waits for all of its loads (vmcnt(0)): no
-//   wait depends on the order in which loads complete (two waves to a buffer,
-//   with 16 loads each, were 6% slower).  One barrier per stage publishes the
-//   next and frees a buffer;
-// * loads spread over the products: issued together behind the barrier they fill
-//   the load queue and hold the products up, and a stage's 8 over 8 products
-//   measured 616 us against 603 over 16.  A wave whose turn it is not branches
-//   over each inside the asm: branches that the compiler sees among the products
-//   make it spill or move them;
+// * two buffers of 256 codes of K, whose row pieces are whole 128-byte cache lines
+//   (64-byte pieces and four buffers: 609 us against 523), filled by direct
+//   global -> LDS loads, 16-byte chunks XOR-swizzled so 16 lanes' reads hit 16 bank
+//   groups; the scales go into buffers of their own, four words a row at once
+//   where alignment allows (with a word a row they cost as many cache lookups as
+//   the codes);
+// * a wave waits for all of its loads (vmcnt(0)) and then issues the next stage's,
+//   so it never has more than one stage in flight and no wait depends on the order
+//   in which loads complete.  One barrier per stage publishes the next stage and
+//   frees this one's buffer, three quarters into its products, so the loads have
+//   three quarters of a stage's products to land in;
+// * one load to a product: issued together behind the barrier they fill the load
+//   queue and hold the products up;
 // * workgroups are persistent, one per CU, and the ring runs on from one tile
 //   into the next: the next tile's first stages are on their way while this
 //   tile's last products and its stores run.
 // W is the MFMA's row operand and X its column operand, so a lane ends up with
 // one row of Y and runs of columns; two lanes swap halves (v_permlane32_swap)
 // and each stores 16 bytes, without LDS, which the ring keeps.
-// 16943 x 4096 x 14336: 603-613 us, 3.3 PFLOP/s; 8192^3: 305-312 us, 3.6 PFLOP/s.
-// The clock falls as the matrix pipe gets busier (1.97 GHz at 40%, 1.84 at 48%).
-// The loads alone take 305 us (64-byte row pieces use half of each 128-byte
-// line), the products alone 283, the stores 100.
+// 16943 x 4096 x 14336: 523 us, 3.8 PFLOP/s; 8192^3: 261 us, 4.2 PFLOP/s; 2048 x
+// 8192 x 8192: 70 us.  The clock falls as the matrix pipe gets busier (1.84 GHz at
+// 48%); the products alone take 283 us of the first, the stores 100.
 #include "lds_dma.cuh"
 #include "lora_device.cuh"
 #include "lora_kernels.h"
@@ -68,27 +65,27 @@ __device__ __forceinline__ void tile_at(int t, int tiles_m, int tiles_n, int &mi
   ni = in / cnt;
 }
 
-// WIDE: a load of the scales takes four words a row and serves four stages.
+// WIDE: a load of the scales takes four words a row and serves two stages.
 template <int BM, int BN, int WM, int WN, bool WIDE>
 __global__ __launch_bounds__(WM *WN *kWave) void mx_product_kernel(MxGemmArgs g) {
   constexpr int NW = WM * WN, TM = BM / WM, TN = BN / WN, FM = TM / 32, FN = TN / 32;
-  constexpr int R = BM + BN;
-  constexpr int STAGES = 4, STAGE = R * 64;
-  constexpr int CI = R / 16 / 4, SI = R / 64 / 4;   // an owner's loads of codes and of scales
-  constexpr int C0 = CI / 2;   // loads of codes under a stage's second half step, the rest under a first
-  // scales: loaded every SPER stages into one of SBUFS buffers, SROW bytes a row
-  constexpr int SPER = WIDE ? 4 : 1, SROW = 4 * SPER, SBUFS = WIDE ? 2 : STAGES, SSTAGE = R * SROW;
-  static_assert(BM == BN && NW == 8 && CI == FM * FN, "owners, and loads to the products");
-  static_assert(STAGES * STAGE + SBUFS * SSTAGE <= 160 * 1024, "LDS");
-  __shared__ __align__(16) unsigned char smem[STAGES * STAGE + SBUFS * SSTAGE];
+  constexpr int R = BM + BN, RW = R / NW, STAGE = R * 128;   // RW: rows that a wave loads
+  constexpr int CI = RW / 8;                        // its loads of codes in a stage
+  // scales: WIDE rows of four words, for two stages; otherwise one word of every
+  // row after the other
+  constexpr int SPER = WIDE ? 2 : 1, SSTAGE = WIDE ? R * 16 : R * 8;
+  constexpr int SOFF = 2 * STAGE;
+  static_assert(RW == kWave && BM % RW == 0 && CI == FM * FN, "a load to a product");
+  static_assert(SOFF + 2 * SSTAGE <= 160 * 1024, "LDS");
+  __shared__ __align__(16) unsigned char smem[SOFF + 2 * SSTAGE];
 
   const int tid = threadIdx.x, l = tid & (kWave - 1);
   const int wid = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int wm = wid / WN, wn = wid % WN;
   const int tiles_m = (g.M + BM - 1) / BM, tiles_n = (g.N + BN - 1) / BN;
   const int tiles = tiles_m * tiles_n;
-  const int KT = (g.K + 127) / 128;
-  const bool ktail = g.K % 128 != 0;
+  const int KT = (g.K + 255) / 256, last_word = (g.K / 32 - 1) / 4;
+  const bool ktail = g.K % 256 != 0;
 
   // XCD x (workgroups x, x + 8, ...) owns the x-th eighth of the tile order and
   // its workgroups take that in turn.
@@ -97,100 +94,100 @@ __global__ __launch_bounds__(WM *WN *kWave) void mx_product_kernel(MxGemmArgs g)
   int t_issue = xcd * per + blockIdx.x / 8;
   if (t_issue >= t_end) return;
 
-  // This wave's loads, of every second stage: rows of one operand.  Load i has
-  // rows [16 (CI w4 + i), +16) of the stage's (X's first), row l / 4 at physical
-  // chunk l % 4, logical chunk `chunk`; rows past the end read the last one.
+  // This wave's loads: rows [RW wid, +RW) of X's and W's.  Load i has rows 8 i + l / 8
+  // of them at physical chunk l % 8, logical chunk `chunk(i)`; rows past the end
+  // read the last one.
   const uint32_t sbase = lds_offset(smem);
-  const int grp = wid / 4, w4 = wid % 4;
-  const bool isx = w4 < 2;
+  constexpr int XW = BM / RW;                       // waves of X
+  const bool isx = wid < XW;
+  const int wrow0 = (isx ? wid : wid - XW) * RW;
   const unsigned char *const op = isx ? g.X : g.W, *const sop = isx ? g.SX : g.SW;
   const int64_t ldo = isx ? g.ldx : g.ldw, ldso = isx ? g.ldsx : g.ldsw;
-  const int chunk = (l & 3) ^ ((l >> 4) & 3);
+  auto chunk = [&](int i) { return (l & 7) ^ ((i & 1) * 4 + l / 16); };
   const unsigned char *base = nullptr, *bases = nullptr;
-  uint32_t off[CI], offs[SI];
+  uint32_t off[CI], offs;
   auto aim = [&](int t) __attribute__((always_inline)) {
     int mi, ni;
     tile_at(t, tiles_m, tiles_n, mi, ni);
     const int first = isx ? mi * BM : ni * BN;
+    base = op + (int64_t)first * ldo;
+    bases = sop + (int64_t)first * ldso;
     const int last = (isx ? g.M : g.N) - 1 - first;
 #pragma unroll
     for (int i = 0; i < CI; ++i)
-      off[i] = (uint32_t)min((w4 % 2 * CI + i) * 16 + l / 4, last) * (uint32_t)ldo + chunk * 16;
-#pragma unroll
-    for (int i = 0; i < SI; ++i) offs[i] = (uint32_t)min((w4 % 2 * SI + i) * 64 + l, last) * (uint32_t)ldso;
-    base = op + (int64_t)first * ldo;
-    bases = sop + (int64_t)first * ldso;
+      off[i] = (uint32_t)min(wrow0 + i * 8 + l / 8, last) * (uint32_t)ldo + chunk(i) * 16;
+    offs = (uint32_t)min(wrow0 + l, last) * (uint32_t)ldso;
   };
   // The next stage to issue: stage k_issue of tile t_issue, into buffer b_issue,
   // its scales into buffer s_issue where a load of them is due.
   int k_issue = 0, b_issue = 0, s_issue = 0;
-  auto issue_codes = [&](uint32_t skip, int i) __attribute__((always_inline)) {
+  auto issue_codes = [&](int i) __attribute__((always_inline)) {
     // a chunk past K reads the stage's first chunk (in bounds: it starts
     // before K) and is zeroed before use
     const uint32_t back =
-        !WIDE && ktail && k_issue == KT - 1 && k_issue * 128 + chunk * 32 >= g.K ? chunk * 16 : 0;
-    dma16_s_unless(skip, __builtin_amdgcn_readfirstlane(sbase + b_issue * STAGE + (w4 * CI + i) * 1024),
-                   off[i] - back, base + (int64_t)k_issue * 64);
+        !WIDE && ktail && k_issue == KT - 1 && k_issue * 256 + chunk(i) * 32 >= g.K ? chunk(i) * 16 : 0;
+    dma16_s(__builtin_amdgcn_readfirstlane(sbase + b_issue * STAGE + (wid * CI + i) * 1024),
+            off[i] - back, base + (int64_t)k_issue * 128);
   };
-  auto issue_scales = [&](uint32_t skip) __attribute__((always_inline)) {
+  auto issue_scales = [&]() __attribute__((always_inline)) {
+    const uint32_t dst = sbase + SOFF + s_issue * SSTAGE;
+    if constexpr (WIDE) {
+      // (a branch inside the asm: see the loop)
+      dma16_s_unless(__builtin_amdgcn_readfirstlane(k_issue % SPER),
+                     __builtin_amdgcn_readfirstlane(dst + wid * 64 * 16), offs, bases + (int64_t)k_issue * 8);
+    } else {
 #pragma unroll
-    for (int i = 0; i < SI; ++i) {
-      const uint32_t dst = __builtin_amdgcn_readfirstlane(sbase + STAGES * STAGE + s_issue * SSTAGE +
-                                                          (w4 * SI + i) * 64 * SROW);
-      if constexpr (WIDE)
-        dma16_s_unless(skip, dst, offs[i], bases + (int64_t)k_issue * 4);
-      else
-        dma4_s_unless(skip, dst, offs[i], bases + (int64_t)k_issue * 4);
+      for (int w = 0; w < 2; ++w)
+        dma4_s(__builtin_amdgcn_readfirstlane(dst + w * R * 4 + wid * 64 * 4), offs,
+               bases + (int64_t)min(k_issue * 2 + w, last_word) * 4);
     }
   };
   auto advance = [&]() __attribute__((always_inline)) {
-    b_issue = b_issue + 1 == STAGES ? 0 : b_issue + 1;
-    if (k_issue % SPER == 0) s_issue = s_issue + 1 == SBUFS ? 0 : s_issue + 1;
+    b_issue ^= 1;
+    if (k_issue % SPER == SPER - 1) s_issue ^= 1;   // (WIDE: KT is even)
     if (++k_issue == KT) {
       k_issue = 0;
       // past the last tile the ring goes round on that one, unread
       if (t_issue + stride < t_end) aim(t_issue += stride);
     }
   };
-  // the owner's stage in buf reaches past K: its chunks there to zero, their
-  // scales to 1 (a NaN would spoil them; WIDE rows have no tail)
+  // the wave's rows of the stage in buf reach past K: their chunks there to zero,
+  // their scales to 1 (a NaN would spoil them; WIDE rows have no tail)
   auto zero_tail = [&](int buf) {
-    unsigned char *st = smem + buf * STAGE;
 #pragma unroll
     for (int i = 0; i < CI; ++i)
-      if ((KT - 1) * 128 + chunk * 32 >= g.K)
-        *reinterpret_cast<u32x4 *>(st + (w4 * CI + i) * 1024 + l * 16) = u32x4{0, 0, 0, 0};
+      if ((KT - 1) * 256 + chunk(i) * 32 >= g.K)
+        *reinterpret_cast<u32x4 *>(smem + buf * STAGE + (wid * CI + i) * 1024 + l * 16) = u32x4{0, 0, 0, 0};
 #pragma unroll
-    for (int i = 0; i < SI; ++i) {
-      uint32_t *p = reinterpret_cast<uint32_t *>(smem + STAGES * STAGE + buf * SSTAGE +
-                                                 (w4 * SI + i) * 256 + l * 4);
-      const uint32_t keep = ~0u >> (32 - 8 * (g.K / 32 - (KT - 1) * 4));   // 1..3 blocks
+    for (int w = 0; w < 2; ++w) {
+      const int left = g.K / 32 - (KT - 1) * 8 - w * 4;   // blocks of the word inside K
+      if (left >= 4) continue;
+      uint32_t *p = reinterpret_cast<uint32_t *>(smem + SOFF + buf * SSTAGE + w * R * 4 + (wid * 64 + l) * 4);
+      const uint32_t keep = left <= 0 ? 0u : ~0u >> (32 - 8 * left);
       *p = (*p & keep) | (0x7f7f7f7fu & ~keep);
     }
   };
 
   int t = t_issue;
   aim(t);
-  for (int s = 0; s < 2; ++s) {
-    const uint32_t skip = __builtin_amdgcn_readfirstlane(s ^ grp);
-    issue_scales(skip | k_issue % SPER);
+  issue_scales();
 #pragma unroll
-    for (int i = 0; i < CI; ++i) issue_codes(skip, i);
-    advance();
-  }
+  for (int i = 0; i < CI; ++i) issue_codes(i);
+  advance();
 
   // fragment offsets in a stage
-  const int arow = (BM + wn * TN + (l & 31)) * 64, brow = (wm * TM + (l & 31)) * 64;
-  int co[2];
+  const int arow = (BM + wn * TN + (l & 31)) * 128, brow = (wm * TM + (l & 31)) * 128;
+  int co[4];
 #pragma unroll
-  for (int s = 0; s < 2; ++s) co[s] = ((2 * s + (l >> 5)) ^ ((l >> 2) & 3)) * 16;
-  const int asc = STAGES * STAGE + (BM + wn * TN + (l & 31)) * SROW;
-  const int bsc = STAGES * STAGE + (wm * TM + (l & 31)) * SROW;
+  for (int s = 0; s < 4; ++s) co[s] = ((2 * s + (l >> 5)) ^ ((l >> 1) & 7)) * 16;
+  const int asc = SOFF + (BM + wn * TN + (l & 31)) * (WIDE ? 16 : 4);
+  const int bsc = SOFF + (wm * TM + (l & 31)) * (WIDE ? 16 : 4);
   const int sh = (l >> 5) * 8;
 
   f32x16 acc[FN][FM];
   u32x4 a[2][FN], b[2][FM];
-  uint32_t sa[FN], sb[FM], ra[FN], rb[FM];          // the stage's scales, the next one's words
+  uint32_t sa[2][FN], sb[2][FM];                    // the stage's scale words
+  uint32_t ra[2][FN], rb[2][FM];                    // the next stage's
   auto zero_acc = [&]() __attribute__((always_inline)) {
 #pragma unroll
     for (int j = 0; j < FN; ++j)
@@ -206,85 +203,89 @@ __global__ __launch_bounds__(WM *WN *kWave) void mx_product_kernel(MxGemmArgs g)
 #pragma unroll
       for (int i = 0; i < FM; ++i) asm volatile("" : "+v"(acc[j][i]));
   };
-  // fragment q of half step s of the stage at st
+  // fragment q of quarter s of the stage at st
   auto read1 = [&](int q, const unsigned char *st, int s) __attribute__((always_inline)) {
     if (q < FN)
-      a[s][q] = *reinterpret_cast<const u32x4 *>(st + arow + q * 32 * 64 + co[s]);
+      a[s & 1][q] = *reinterpret_cast<const u32x4 *>(st + arow + q * 32 * 128 + co[s]);
     else
-      b[s][q - FN] = *reinterpret_cast<const u32x4 *>(st + brow + (q - FN) * 32 * 64 + co[s]);
+      b[s & 1][q - FN] = *reinterpret_cast<const u32x4 *>(st + brow + (q - FN) * 32 * 128 + co[s]);
   };
   // the next stage's scale words, in order
   int s_read = 0, w_read = 0;
   auto read_scales = [&]() __attribute__((always_inline)) {
-    const unsigned char *st = smem + s_read * SSTAGE + w_read * 4;
+    const unsigned char *st = smem + s_read * SSTAGE + w_read * 8;
 #pragma unroll
-    for (int j = 0; j < FN; ++j)
-      ra[j] = *reinterpret_cast<const uint32_t *>(st + asc + j * 32 * SROW);
+    for (int w = 0; w < 2; ++w) {
 #pragma unroll
-    for (int i = 0; i < FM; ++i)
-      rb[i] = *reinterpret_cast<const uint32_t *>(st + bsc + i * 32 * SROW);
-    const bool next = ++w_read == SPER;
-    w_read = next ? 0 : w_read;
-    s_read = next ? (s_read + 1 == SBUFS ? 0 : s_read + 1) : s_read;
+      for (int j = 0; j < FN; ++j)
+        ra[w][j] = *reinterpret_cast<const uint32_t *>(
+            st + asc + (WIDE ? j * 32 * 16 + w * 4 : j * 32 * 4 + w * R * 4));
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+        rb[w][i] = *reinterpret_cast<const uint32_t *>(
+            st + bsc + (WIDE ? i * 32 * 16 + w * 4 : i * 32 * 4 + w * R * 4));
+    }
+    w_read = WIDE ? w_read ^ 1 : 0;
+    s_read = w_read ? s_read : s_read ^ 1;
   };
 
-  int buf = 0, kt = 0, turn = 0;                    // turn: the owner of stage kt
-  if (grp == 0) {
-    vm_wait<0>();
-    if (ktail && KT == 1) zero_tail(0);
-  }
-  issue_scales(grp | k_issue % SPER);               // stage 2's first loads
-#pragma unroll
-  for (int i = 0; i < C0; ++i) issue_codes(grp, i);
+  int buf = 0, kt = 0;
+  vm_wait<0>();
+  if (!WIDE && ktail && KT == 1) zero_tail(0);
   lgkm_barrier();
+  issue_scales();
+#pragma unroll
+  for (int i = 0; i < CI; ++i) issue_codes(i);
+  advance();
   read_scales();
 #pragma unroll
   for (int q = 0; q < FN + FM; ++q) read1(q, smem, 0);
   zero_acc();
-  // A stage in two half steps of 64 codes.  While the first is multiplied, the
-  // second's fragments are read; then stage kt + 1 has landed and its first
-  // fragments are read while the second half step is multiplied.  Under the first
-  // half step go the rest of stage kt + 2's loads, under the second the first of
-  // stage kt + 3's, by the waves that have just waited for stage kt + 1 (into a
-  // buffer that was last read during stage kt - 1).  The sums are pinned after
-  // each half step: the compiler would otherwise move the products behind the
-  // next branch.
+  // A stage in four quarters of 64 codes; while one is multiplied, the next one's
+  // fragments are read.  Before the last quarter the next stage has landed and
+  // this one's buffer has been read: the loads of the stage after the next go into
+  // it, one to a product, with three quarters left to land in.  Nothing that the
+  // compiler sees branches among the products and the sums are pinned after each
+  // quarter: it would otherwise move the products behind the next branch.
   while (true) {
-    const unsigned char *st = smem + buf * STAGE;
-    const int nbuf = buf + 1 == STAGES ? 0 : buf + 1;
-    const uint32_t skip = __builtin_amdgcn_readfirstlane(turn ^ grp);
-    // byte 2 s of a shifted word: half step s's block of this half of the wave
+    const unsigned char *st = smem + buf * STAGE, *nst = smem + (buf ^ 1) * STAGE;
+    // byte 2 s of a shifted word: quarter s's block of this half of the wave
 #pragma unroll
-    for (int j = 0; j < FN; ++j) sa[j] = ra[j] >> sh;
+    for (int w = 0; w < 2; ++w) {
 #pragma unroll
-    for (int i = 0; i < FM; ++i) sb[i] = rb[i] >> sh;
+      for (int j = 0; j < FN; ++j) sa[w][j] = ra[w][j] >> sh;
 #pragma unroll
-    for (int q = 0; q < FN * FM; ++q) {
-      acc[q / FM][q % FM] = mfma_mx4<0>(a[0][q / FM], b[0][q % FM], acc[q / FM][q % FM], sa[q / FM], sb[q % FM]);
-      if (q < FN + FM) read1(q, st, 1);
-      if (q % 2 == 0) issue_codes(skip, C0 + q / 2);
-      __builtin_amdgcn_sched_barrier(0);
+      for (int i = 0; i < FM; ++i) sb[w][i] = rb[w][i] >> sh;
     }
+#pragma unroll
+    for (int s = 0; s < 3; ++s)
+#pragma unroll
+      for (int q = 0; q < FN * FM; ++q) {
+        f32x16 &c = acc[q / FM][q % FM];
+        if (s & 1)
+          c = mfma_mx4<2>(a[1][q / FM], b[1][q % FM], c, sa[0][q / FM], sb[0][q % FM]);
+        else
+          c = mfma_mx4<0>(a[0][q / FM], b[0][q % FM], c, sa[s / 2][q / FM], sb[s / 2][q % FM]);
+        if (q < FN + FM) read1(q, st, s + 1);
+        __builtin_amdgcn_sched_barrier(0);
+      }
     pin();
     const bool last_stage = kt + 1 == KT;
-    advance();
-    if (skip) {                                     // the next stage's owners: it has landed
-      vm_wait<0>();
-      if (!WIDE && ktail && (last_stage ? KT == 1 : kt + 2 == KT)) zero_tail(nbuf);
-    }
-    lgkm_barrier();                                 // stage kt + 1 is there, stage kt has been read
+    vm_wait<0>();                                   // the next stage has landed
+    if (!WIDE && ktail && (last_stage ? KT == 1 : kt + 2 == KT)) zero_tail(buf ^ 1);
+    lgkm_barrier();                                 // it is there, this one has been read
     read_scales();                                  // (after the last stage: of a settled buffer)
-    issue_scales((skip ^ 1) | k_issue % SPER);
+    issue_scales();
 #pragma unroll
     for (int q = 0; q < FN * FM; ++q) {
-      acc[q / FM][q % FM] = mfma_mx4<2>(a[1][q / FM], b[1][q % FM], acc[q / FM][q % FM], sa[q / FM], sb[q % FM]);
-      if (q < FN + FM) read1(q, smem + nbuf * STAGE, 0);
-      if (q % 2 == 0) issue_codes(skip ^ 1, q / 2);
+      acc[q / FM][q % FM] = mfma_mx4<2>(a[1][q / FM], b[1][q % FM], acc[q / FM][q % FM], sa[1][q / FM], sb[1][q % FM]);
+      if (q < FN + FM) read1(q, nst, 0);
+      issue_codes(q);
       __builtin_amdgcn_sched_barrier(0);
     }
     pin();
-    buf = nbuf;
-    turn ^= 1;
+    advance();
+    buf ^= 1;
     if (!last_stage) {
       ++kt;
       continue;
