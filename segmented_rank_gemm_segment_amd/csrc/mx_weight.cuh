@@ -4,20 +4,20 @@
 // The tile's W is a quarter of its X in bytes but has as many rows, so W's codes
 // are loaded 128 of K at a time (64-byte rows; 32-byte rows would fetch each
 // 128-byte line four times) and its scales 512 where alignment allows, while X
-// comes in stages of 64.  Three rings in LDS, all filled by direct global -> LDS
-// loads: X three stages, codes and scales two pieces.  A wave has
-// 128 rows of X and 64 of W; per stage it reads each W block once, widens its 32
-// codes in four steps of 8 to bf16 under the block's scale (exact), and lane
-// half h takes K positions [32 h, +32) of the stage of both operands.  Waves 0-3
-// load the even stages and waves 4-7 the odd ones, so a wave waits for all of its
-// loads, one stage's, and no wait depends on the order in which they complete.
-// Loads spread over the products, one barrier per stage, persistent workgroups
-// and stores from registers as in the product of two MXFP4 operands.
+// comes in stages of 64.  Three rings of two in LDS, all filled by direct
+// global -> LDS loads.  A wave has 128 rows of X and 64 of W; per stage it reads
+// each W block once, widens its 32 codes in four steps of 8 to bf16 under the
+// block's scale (exact), and lane half h takes K positions [32 h, +32) of the stage
+// of both operands.  Waits for all loads (a wave has one stage's in flight, and no
+// wait depends on their order), one barrier per stage, loads spread over the
+// products, persistent workgroups and stores from registers as in the product of
+// two MXFP4 operands.
 //
-// 16943 x 4096 x 14336: 1578 us, 1.26 PFLOP/s; 8192^3: 837 us, 1.31 PFLOP/s (a
+// 16943 x 4096 x 14336: 1619 us, 1.23 PFLOP/s; 8192^3: 853 us, 1.29 PFLOP/s (a
 // library's bf16 product reaches 1.36 and 1.17 on the same shapes).  8190 x 8
-// choices on 64 experts of 2048 -> 1536: 435 us, 0.92 PFLOP/s.  An owner's first
-// loads right after its wait, a quarter of a stage earlier, measured 8% slower.
+// choices on 64 experts of 2048 -> 1536: 405 us, 1.0 PFLOP/s.  Loads issued a
+// quarter of a stage later: 1664 us; three stages of X, loaded by the workgroup's
+// halves in turn: 1644 us.
 #pragma once
 
 #include "gemm_tile.cuh"
@@ -39,7 +39,7 @@ __device__ __forceinline__ void tile_at(int t, int tiles_m, int tiles_n, int &mi
 template <bool GROUPED, bool WIDE, bool TAIL>
 __global__ __launch_bounds__(512) void mx_weight_kernel(GemmArgs g) {
   constexpr int BM = 256, BN = 256, WN = 4, TM = 128, TN = 64, FM = 4, FN = 2;
-  constexpr int XST = BM * 128, XN = 3;             // X: bytes of a stage, stages
+  constexpr int XST = BM * 128, XN = 2;             // X: bytes of a stage, stages
   constexpr int WST = BN * 64, WNB = 2;             // W: bytes of 128 of K, pieces
   constexpr int SROW = WIDE ? 16 : 4, SST = BN * SROW, SNB = 2;
   constexpr int WOFF = XN * XST, SOFF = WOFF + WNB * WST, TOFF = SOFF + SNB * SST;
@@ -95,68 +95,71 @@ __global__ __launch_bounds__(512) void mx_weight_kernel(GemmArgs g) {
     }
   };
 
-  // Stages belong to the two halves of the workgroup in turn.  An owner's loads,
-  // X: 8 of 8 rows of 128 bytes; codes, with even stages: 4 of 16 rows of 64 bytes;
-  // scales: 64 rows.
+  // This wave's loads.  X: 4 a stage, 8 rows of 128 bytes each.  Codes: 2 a
+  // piece, one per stage, 16 rows of 64 bytes each.  Scales: 64 rows, waves w and
+  // w + 4 the same (so that all waves issue as many).
   const uint32_t sbase = lds_offset(smem);
-  const int grp = wid / 4, w4 = wid % 4;
   // Rows as 32-bit offsets from the tile's first (leading dimensions are below
-  // 2^22 elements); the experts' X rows lie anywhere.
-  const unsigned char *xbase = nullptr, *wbase = nullptr, *sbase_g = nullptr;
-  uint32_t xoff[8], woff[4], soff;                  // GROUPED: xoff is the row
-  auto xchunk = [&](int i) { return (l & 7) ^ ((i & 1) * 4 + l / 16); };
-  const int wchunk = (l & 3) ^ ((l >> 4) & 3);
+  // 2^22 elements); the experts' X rows lie anywhere and take an address each.
+  const unsigned char *xrow[GROUPED ? 4 : 1], *xbase = nullptr, *wbase = nullptr, *sbase_g = nullptr;
+  uint32_t xoff[4], woff[2], soff;
+  auto xchunk = [&](int i) { return (l & 7) ^ ((((wid * 4 + i) * 8 + l / 8) >> 1) & 7); };
+  auto wchunk = [&](int i) { return (l & 3) ^ ((((wid * 2 + i) * 16 + l / 4) >> 2) & 3); };
   auto aim = [&](int tile) __attribute__((always_inline)) {
     int mi, ni, m0, m1, e;
     tile_at(tile, tiles_m, tiles_n, mi, ni);
     m_tile(mi, m0, m1, e);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int p = min(m0 + (w4 * 8 + i) * 8 + l / 8, m1 - 1);
-      if constexpr (GROUPED)
-        xoff[i] = g.ex.sorted_choice ? g.ex.sorted_choice[p] / g.ex.top_k : p;
-      else
+    for (int i = 0; i < 4; ++i) {
+      const int p = min(m0 + (wid * 4 + i) * 8 + l / 8, m1 - 1);
+      if constexpr (GROUPED) {
+        const int row = g.ex.sorted_choice ? g.ex.sorted_choice[p] / g.ex.top_k : p;
+        xrow[i] = reinterpret_cast<const unsigned char *>(g.X + (int64_t)row * g.ldx) + xchunk(i) * 16;
+      } else {
         xoff[i] = (uint32_t)(p - m0) * (uint32_t)(g.ldx * 2) + xchunk(i) * 16;
+      }
     }
-    xbase = reinterpret_cast<const unsigned char *>(g.X + (GROUPED ? 0 : (int64_t)m0 * g.ldx));
+    if constexpr (!GROUPED) xbase = reinterpret_cast<const unsigned char *>(g.X + (int64_t)m0 * g.ldx);
     const int n0 = ni * BN;
     const int64_t ldw = g.ldw / 2;                  // bytes
     wbase = reinterpret_cast<const unsigned char *>(g.W) + (GROUPED ? e * g.ex.w_stride : 0) + n0 * ldw;
     sbase_g = g.mx.w + (GROUPED ? e * g.ex.s_stride : 0) + n0 * g.mx.ldw;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      woff[i] = (uint32_t)(min((w4 * 4 + i) * 16 + l / 4, N - 1 - n0) * (int)ldw) + wchunk * 16;
-    soff = (uint32_t)(min(w4 * 64 + l, N - 1 - n0) * (int)g.mx.ldw);
+    for (int i = 0; i < 2; ++i)
+      woff[i] = (uint32_t)(min((wid * 2 + i) * 16 + l / 4, N - 1 - n0) * (int)ldw) + wchunk(i) * 16;
+    soff = (uint32_t)(min((wid & 3) * 64 + l, N - 1 - n0) * (int)g.mx.ldw);
   };
   // The next stage to issue: stage k_issue of tile t_issue; the buffers of its X,
   // its piece of codes and its scales.
   int k_issue = 0, xb = 0, wb = 0, sb_i = 0;
   int t_issue = t;
-  auto issue_x = [&](uint32_t skip, int i) __attribute__((always_inline)) {
+  constexpr int SPER = WIDE ? 8 : 2;                // stages per load of scales
+  auto issue_x = [&](int i) __attribute__((always_inline)) {
     // a chunk past K reads the stage's first chunk and is zeroed before use
     const int c = xchunk(i);
     const int back = TAIL && k_issue * 64 + c * 8 >= K ? c * 16 : 0;
-    const uint32_t dst = __builtin_amdgcn_readfirstlane(sbase + xb * XST + (w4 * 8 + i) * 1024);
+    const uint32_t dst = __builtin_amdgcn_readfirstlane(sbase + xb * XST + (wid * 4 + i) * 1024);
     if constexpr (GROUPED)
-      dma16_unless(skip, dst, xbase + xoff[i] * (uint64_t)(g.ldx * 2) + (k_issue * 128 + c * 16 - back));
+      dma16(dst, xrow[i] + (int64_t)k_issue * 128 - back);
     else
-      dma16_s_unless(skip, dst, xoff[i] - back, xbase + (int64_t)k_issue * 128);
+      dma16_s(dst, xoff[i] - back, xbase + (int64_t)k_issue * 128);
   };
-  auto issue_w = [&](uint32_t skip, int i) __attribute__((always_inline)) {
-    const int p = k_issue / 2;
-    const uint32_t back = TAIL && p * 128 + wchunk * 32 >= K ? wchunk * 16 : 0;
-    dma16_s_unless(skip, __builtin_amdgcn_readfirstlane(sbase + WOFF + wb * WST + (w4 * 4 + i) * 1024),
+  auto issue_w = [&](int i) __attribute__((always_inline)) {
+    const int c = wchunk(i), p = k_issue / 2;
+    const uint32_t back = TAIL && p * 128 + c * 32 >= K ? c * 16 : 0;
+    dma16_s_unless(__builtin_amdgcn_readfirstlane(k_issue % 2),
+                   __builtin_amdgcn_readfirstlane(sbase + WOFF + wb * WST + (wid * 2 + i) * 1024),
                    woff[i] - back, wbase + (int64_t)p * 64);
   };
-  auto issue_s = [&](uint32_t skip) __attribute__((always_inline)) {
+  auto issue_s = [&]() __attribute__((always_inline)) {
     const uint32_t dst =
-        __builtin_amdgcn_readfirstlane(sbase + SOFF + sb_i * SST + w4 * 64 * SROW);
+        __builtin_amdgcn_readfirstlane(sbase + SOFF + sb_i * SST + (wid & 3) * 64 * SROW);
+    const uint32_t skip = __builtin_amdgcn_readfirstlane(k_issue % SPER);
     if constexpr (WIDE)
       dma16_s_unless(skip, dst, soff, sbase_g + (int64_t)(k_issue / 8) * 16);
     else
       dma4_s_unless(skip, dst, soff, sbase_g + (int64_t)(k_issue / 2) * 4);
   };
-  constexpr int SPER = WIDE ? 8 : 2;                // stages per load of scales
   // past a stage's loads (its X, and at even stages its piece's codes and scales)
   auto advance = [&]() __attribute__((always_inline)) {
     xb = xb + 1 == XN ? 0 : xb + 1;
@@ -168,36 +171,36 @@ __global__ __launch_bounds__(512) void mx_weight_kernel(GemmArgs g) {
       if (t_issue + stride < t_end) aim(t_issue += stride);
     }
   };
-  // the owner's X stage k in buffer b and, at even k, its piece in buffer w: what lies past
+  // X stage k in buffer b and, at even k, its piece in buffer w: what lies past
   // K to zero, scales there to 1 (a NaN would spoil the zeros)
   auto zero_tail = [&](int k, int b, int w, int s) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < 4; ++i)
       if (k * 64 + xchunk(i) * 8 >= K)
-        *reinterpret_cast<u32x4 *>(smem + b * XST + (w4 * 8 + i) * 1024 + l * 16) = u32x4{0, 0, 0, 0};
+        *reinterpret_cast<u32x4 *>(smem + b * XST + (wid * 4 + i) * 1024 + l * 16) = u32x4{0, 0, 0, 0};
     if (k & 1) return;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (k * 64 + wchunk * 32 >= K)
-        *reinterpret_cast<u32x4 *>(smem + WOFF + w * WST + (w4 * 4 + i) * 1024 + l * 16) = u32x4{0, 0, 0, 0};
+    for (int i = 0; i < 2; ++i)
+      if (k * 64 + wchunk(i) * 32 >= K)
+        *reinterpret_cast<u32x4 *>(smem + WOFF + w * WST + (wid * 2 + i) * 1024 + l * 16) = u32x4{0, 0, 0, 0};
     const int left = K / 32 - k * 2;                // blocks of the piece inside K
     if (left < 4) {
-      uint32_t *p = reinterpret_cast<uint32_t *>(smem + SOFF + s * SST + (w4 * 64 + l) * 4);
+      uint32_t *p = reinterpret_cast<uint32_t *>(smem + SOFF + s * SST + ((wid & 3) * 64 + l) * 4);
       const uint32_t keep = ~0u >> (32 - 8 * left);
       *p = (*p & keep) | (0x7f7f7f7fu & ~keep);
     }
   };
 
   aim(t);
-  for (int s = 0; s < 2; ++s) {                     // two stages ahead
-    const uint32_t skip = __builtin_amdgcn_readfirstlane(s ^ grp);
-    issue_s(skip | k_issue % SPER);
+  auto issue = [&]() __attribute__((always_inline)) {
+    issue_s();
+    issue_w(0);
+    issue_w(1);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) issue_w(skip | k_issue % 2, i);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) issue_x(skip, i);
+    for (int i = 0; i < 4; ++i) issue_x(i);
     advance();
-  }
+  };
+  issue();
 
   // fragment offsets
   const int xo = (wm * TM + (l & 31)) * 128, wo = WOFF + (wn * TN + (l & 31)) * 64;
@@ -249,12 +252,11 @@ __global__ __launch_bounds__(512) void mx_weight_kernel(GemmArgs g) {
 
   // consumer side of the rings: stage kt in X buffer cx; the next stage's piece
   // and scales in rw, rs
-  int kt = 0, cx = 0, rw = 0, rs = 0, turn = 0;     // turn: the owner of stage kt
-  if (grp == 0) {
-    vm_wait<0>();                                   // the first stage has landed
-    if (TAIL && KT <= 2) zero_tail(0, 0, 0, 0);
-  }
+  int kt = 0, cx = 0, rw = 0, rs = 0;
+  vm_wait<0>();                                     // the first stage has landed
+  if (TAIL && KT <= 2) zero_tail(0, 0, 0, 0);
   lgkm_barrier();
+  issue();
 #pragma unroll
   for (int j = 0; j < FN; ++j) read_w(j, 0, 0, 0);
 #pragma unroll
@@ -272,10 +274,6 @@ __global__ __launch_bounds__(512) void mx_weight_kernel(GemmArgs g) {
     const bool np = last || kn % 2 == 0, ns = last || kn % SPER == 0;
     rw = np ? (rw + 1 == WNB ? 0 : rw + 1) : rw;
     rs = ns ? (rs + 1 == SNB ? 0 : rs + 1) : rs;
-    // this iteration's loads: stage kt + 2's, whose owner is stage kt's
-    const uint32_t skip = __builtin_amdgcn_readfirstlane(turn ^ grp);
-    issue_s(skip | k_issue % SPER);
-    const uint32_t skipw = skip | k_issue % 2;
 #pragma unroll
     for (int kk = 0; kk < 3; ++kk)
 #pragma unroll
@@ -284,28 +282,22 @@ __global__ __launch_bounds__(512) void mx_weight_kernel(GemmArgs g) {
             wf[kk & 1][q / FM], xf[kk & 1][q % FM], acc[q / FM][q % FM], 0, 0, 0);
         if (q < FM) read_x((kk + 1) & 1, q, st, kk + 1);
         if (q == 4 || q == 5) widen((kk + 1) & 1, q - 4, kk + 1);
-        if (q % 2 == 0) {                           // 12 slots
-          const int n = kk * 4 + q / 2;
-          if (n < 4)
-            issue_w(skipw, n);
-          else
-            issue_x(skip, n - 4);
-        }
         __builtin_amdgcn_sched_barrier(0);
       }
     pin();
-    if (skip) {                                     // the next stage's owner: it has landed
-      vm_wait<0>();
-      if (TAIL && (kn == KT - 1 || (kn == KT - 2 && kn % 2 == 0))) zero_tail(kn, nx, rw, rs);
-    }
+    vm_wait<0>();                                   // the next stage has landed
+    if (TAIL && (kn == KT - 1 || (kn == KT - 2 && kn % 2 == 0))) zero_tail(kn, nx, rw, rs);
     lgkm_barrier();                                 // the next stage is there, this one has been read
 #pragma unroll
     for (int j = 0; j < FN; ++j) read_w(j, kn, rw, rs);
+    issue_s();
 #pragma unroll
     for (int q = 0; q < FN * FM; ++q) {
       acc[q / FM][q % FM] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
           wf[1][q / FM], xf[1][q % FM], acc[q / FM][q % FM], 0, 0, 0);
       if (q < FM) read_x(0, q, smem + nx * XST, 0);
+      if (q < 2) issue_w(q);
+      if (q >= 2 && q < 6) issue_x(q - 2);
       __builtin_amdgcn_sched_barrier(0);
     }
     pin();
@@ -314,7 +306,6 @@ __global__ __launch_bounds__(512) void mx_weight_kernel(GemmArgs g) {
 #pragma unroll
     for (int j = 0; j < FN; ++j) widen(0, j, 0);
     cx = nx;
-    turn ^= 1;
     if (!last) {
       ++kt;
       continue;
