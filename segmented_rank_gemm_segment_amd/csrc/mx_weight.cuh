@@ -2,9 +2,9 @@
 // products of long segments: 256 x 256 tiles, bound by the bf16 matrix rate.
 //
 // The tile's W is a quarter of its X in bytes but has as many rows, so W's codes
-// are loaded 128 of K at a time (64-byte rows; 32-byte rows would fetch each
-// 128-byte line four times) and its scales 512 where alignment allows, while X
-// comes in stages of 64.  Three rings of two in LDS, all filled by direct
+// are loaded 256 of K at a time (rows of whole 128-byte cache lines; 128 at a time,
+// 2048 x 8192 x 8192 took 221 us against 214) and its scales 512 where alignment
+// allows, while X comes in stages of 64.  Three rings of two in LDS, all filled by direct
 // global -> LDS loads.  A wave has 128 rows of X and 64 of W; per stage it reads
 // each W block once, widens its 32 codes in four steps of 8 to bf16 under the
 // block's scale (exact), and lane half h takes K positions [32 h, +32) of the stage
@@ -13,7 +13,7 @@
 // products, persistent workgroups and stores from registers as in the product of
 // two MXFP4 operands.
 //
-// 16943 x 4096 x 14336: 1619 us, 1.23 PFLOP/s; 8192^3: 853 us, 1.29 PFLOP/s (a
+// 16943 x 4096 x 14336: 1611 us, 1.24 PFLOP/s; 8192^3: 850 us, 1.29 PFLOP/s (a
 // library's bf16 product reaches 1.36 and 1.17 on the same shapes).  8190 x 8
 // choices on 64 experts of 2048 -> 1536: 405 us, 1.0 PFLOP/s.  Loads issued a
 // quarter of a stage later: 1664 us; three stages of X, loaded by the workgroup's
@@ -35,12 +35,12 @@ __device__ __forceinline__ void tile_at(int t, int tiles_m, int tiles_n, int &mi
 }
 
 // WIDE: a load of the scales takes four words a row (K 512).  TAIL: K is no
-// multiple of 128.
+// multiple of 256.
 template <bool GROUPED, bool WIDE, bool TAIL>
 __global__ __launch_bounds__(512) void mx_weight_kernel(GemmArgs g) {
   constexpr int BM = 256, BN = 256, WN = 4, TM = 128, TN = 64, FM = 4, FN = 2;
   constexpr int XST = BM * 128, XN = 2;             // X: bytes of a stage, stages
-  constexpr int WST = BN * 64, WNB = 2;             // W: bytes of 128 of K, pieces
+  constexpr int WST = BN * 128, WNB = 2;            // W: bytes of 256 of K, pieces
   constexpr int SROW = WIDE ? 16 : 4, SST = BN * SROW, SNB = 2;
   constexpr int WOFF = XN * XST, SOFF = WOFF + WNB * WST, TOFF = SOFF + SNB * SST;
   constexpr int TAB = GROUPED ? 4 * (LORA_MAX_EXPERTS + 1) : 0;
@@ -95,16 +95,15 @@ __global__ __launch_bounds__(512) void mx_weight_kernel(GemmArgs g) {
     }
   };
 
-  // This wave's loads.  X: 4 a stage, 8 rows of 128 bytes each.  Codes: 2 a
-  // piece, one per stage, 16 rows of 64 bytes each.  Scales: 64 rows, waves w and
-  // w + 4 the same (so that all waves issue as many).
+  // This wave's loads.  X: 4 a stage, codes: 4 a piece of four stages, 8 rows of
+  // 128 bytes each.  Scales: 64 rows, waves w and w + 4 the same.
   const uint32_t sbase = lds_offset(smem);
   // Rows as 32-bit offsets from the tile's first (leading dimensions are below
   // 2^22 elements); the experts' X rows lie anywhere and take an address each.
   const unsigned char *xrow[GROUPED ? 4 : 1], *xbase = nullptr, *wbase = nullptr, *sbase_g = nullptr;
-  uint32_t xoff[4], woff[2], soff;
+  uint32_t xoff[4], woff[4], soff;
   auto xchunk = [&](int i) { return (l & 7) ^ ((((wid * 4 + i) * 8 + l / 8) >> 1) & 7); };
-  auto wchunk = [&](int i) { return (l & 3) ^ ((((wid * 2 + i) * 16 + l / 4) >> 2) & 3); };
+  auto wchunk = [&](int i) { return (l & 7) ^ ((((wid * 4 + i) * 8 + l / 8) >> 1) & 7); };
   auto aim = [&](int tile) __attribute__((always_inline)) {
     int mi, ni, m0, m1, e;
     tile_at(tile, tiles_m, tiles_n, mi, ni);
@@ -125,8 +124,8 @@ __global__ __launch_bounds__(512) void mx_weight_kernel(GemmArgs g) {
     wbase = reinterpret_cast<const unsigned char *>(g.W) + (GROUPED ? e * g.ex.w_stride : 0) + n0 * ldw;
     sbase_g = g.mx.w + (GROUPED ? e * g.ex.s_stride : 0) + n0 * g.mx.ldw;
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-      woff[i] = (uint32_t)(min((wid * 2 + i) * 16 + l / 4, N - 1 - n0) * (int)ldw) + wchunk(i) * 16;
+    for (int i = 0; i < 4; ++i)
+      woff[i] = (uint32_t)(min((wid * 4 + i) * 8 + l / 8, N - 1 - n0) * (int)ldw) + wchunk(i) * 16;
     soff = (uint32_t)(min((wid & 3) * 64 + l, N - 1 - n0) * (int)g.mx.ldw);
   };
   // The next stage to issue: stage k_issue of tile t_issue; the buffers of its X,
@@ -145,11 +144,11 @@ __global__ __launch_bounds__(512) void mx_weight_kernel(GemmArgs g) {
       dma16_s(dst, xoff[i] - back, xbase + (int64_t)k_issue * 128);
   };
   auto issue_w = [&](int i) __attribute__((always_inline)) {
-    const int c = wchunk(i), p = k_issue / 2;
-    const uint32_t back = TAIL && p * 128 + c * 32 >= K ? c * 16 : 0;
-    dma16_s_unless(__builtin_amdgcn_readfirstlane(k_issue % 2),
-                   __builtin_amdgcn_readfirstlane(sbase + WOFF + wb * WST + (wid * 2 + i) * 1024),
-                   woff[i] - back, wbase + (int64_t)p * 64);
+    const int c = wchunk(i), p = k_issue / 4;
+    const uint32_t back = TAIL && p * 256 + c * 32 >= K ? c * 16 : 0;
+    dma16_s_unless(__builtin_amdgcn_readfirstlane(k_issue % 4),
+                   __builtin_amdgcn_readfirstlane(sbase + WOFF + wb * WST + (wid * 4 + i) * 1024),
+                   woff[i] - back, wbase + (int64_t)p * 128);
   };
   auto issue_s = [&]() __attribute__((always_inline)) {
     const uint32_t dst =
@@ -160,31 +159,32 @@ __global__ __launch_bounds__(512) void mx_weight_kernel(GemmArgs g) {
     else
       dma4_s_unless(skip, dst, soff, sbase_g + (int64_t)(k_issue / 2) * 4);
   };
-  // past a stage's loads (its X, and at even stages its piece's codes and scales)
+  // past a stage's loads (its X, and with the first of their stages codes and scales)
   auto advance = [&]() __attribute__((always_inline)) {
     xb = xb + 1 == XN ? 0 : xb + 1;
     if (k_issue % SPER == 0) sb_i = sb_i + 1 == SNB ? 0 : sb_i + 1;
-    if (k_issue & 1 || k_issue + 1 == KT) wb = wb + 1 == WNB ? 0 : wb + 1;
+    if ((k_issue & 3) == 3 || k_issue + 1 == KT) wb = wb + 1 == WNB ? 0 : wb + 1;
     if (++k_issue == KT) {
       k_issue = 0;
       // past the last tile the rings go round on that one, unread
       if (t_issue + stride < t_end) aim(t_issue += stride);
     }
   };
-  // X stage k in buffer b and, at even k, its piece in buffer w: what lies past
-  // K to zero, scales there to 1 (a NaN would spoil the zeros)
+  // X stage k in buffer b and, where they start with it, its piece of codes in
+  // buffer w and its scales in s: what lies past K to zero, scales there to 1 (a
+  // NaN would spoil the zeros)
   auto zero_tail = [&](int k, int b, int w, int s) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       if (k * 64 + xchunk(i) * 8 >= K)
         *reinterpret_cast<u32x4 *>(smem + b * XST + (wid * 4 + i) * 1024 + l * 16) = u32x4{0, 0, 0, 0};
-    if (k & 1) return;
+    if (k % 4 == 0)
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-      if (k * 64 + wchunk(i) * 32 >= K)
-        *reinterpret_cast<u32x4 *>(smem + WOFF + w * WST + (wid * 2 + i) * 1024 + l * 16) = u32x4{0, 0, 0, 0};
-    const int left = K / 32 - k * 2;                // blocks of the piece inside K
-    if (left < 4) {
+      for (int i = 0; i < 4; ++i)
+        if (k * 64 + wchunk(i) * 32 >= K)
+          *reinterpret_cast<u32x4 *>(smem + WOFF + w * WST + (wid * 4 + i) * 1024 + l * 16) = u32x4{0, 0, 0, 0};
+    const int left = K / 32 - k * 2;                // blocks of the scale word inside K
+    if (k % 2 == 0 && left < 4) {
       uint32_t *p = reinterpret_cast<uint32_t *>(smem + SOFF + s * SST + ((wid & 3) * 64 + l) * 4);
       const uint32_t keep = ~0u >> (32 - 8 * left);
       *p = (*p & keep) | (0x7f7f7f7fu & ~keep);
@@ -194,8 +194,8 @@ __global__ __launch_bounds__(512) void mx_weight_kernel(GemmArgs g) {
   aim(t);
   auto issue = [&]() __attribute__((always_inline)) {
     issue_s();
-    issue_w(0);
-    issue_w(1);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) issue_w(i);
 #pragma unroll
     for (int i = 0; i < 4; ++i) issue_x(i);
     advance();
@@ -203,13 +203,11 @@ __global__ __launch_bounds__(512) void mx_weight_kernel(GemmArgs g) {
   issue();
 
   // fragment offsets
-  const int xo = (wm * TM + (l & 31)) * 128, wo = WOFF + (wn * TN + (l & 31)) * 64;
+  const int xo = (wm * TM + (l & 31)) * 128, wo = WOFF + (wn * TN + (l & 31)) * 128;
   const int so = SOFF + (wn * TN + (l & 31)) * SROW;
-  int xc[4], wc[2];
+  int xc[4];
 #pragma unroll
   for (int kk = 0; kk < 4; ++kk) xc[kk] = ((h * 4 + kk) ^ ((l >> 1) & 7)) * 16;
-#pragma unroll
-  for (int s = 0; s < 2; ++s) wc[s] = ((s * 2 + h) ^ ((l >> 2) & 3)) * 16;
 
   f32x16 acc[FN][FM];
   u32x4 wq[FN], wr[FN];                             // the stage's blocks, the next stage's
@@ -234,7 +232,7 @@ __global__ __launch_bounds__(512) void mx_weight_kernel(GemmArgs g) {
     xf[to][i] = as_bf16x8(*reinterpret_cast<const u32x4 *>(st + xo + i * 32 * 128 + xc[kk]));
   };
   auto read_w = [&](int j, int k, int w, int s) __attribute__((always_inline)) {
-    wr[j] = *reinterpret_cast<const u32x4 *>(smem + wo + w * WST + j * 32 * 64 + (k & 1 ? wc[1] : wc[0]));
+    wr[j] = *reinterpret_cast<const u32x4 *>(smem + wo + w * WST + j * 32 * 128 + (((k & 3) * 2 + h) ^ ((l >> 1) & 7)) * 16);
     sr[j] = *reinterpret_cast<const uint32_t *>(smem + so + s * SST + j * 32 * SROW + (WIDE ? k / 2 % 4 * 4 : 0));
   };
   // block of this lane's half in a scale word at stage k
@@ -254,7 +252,7 @@ __global__ __launch_bounds__(512) void mx_weight_kernel(GemmArgs g) {
   // and scales in rw, rs
   int kt = 0, cx = 0, rw = 0, rs = 0;
   vm_wait<0>();                                     // the first stage has landed
-  if (TAIL && KT <= 2) zero_tail(0, 0, 0, 0);
+  if (TAIL && KT <= 4) zero_tail(0, 0, 0, 0);
   lgkm_barrier();
   issue();
 #pragma unroll
@@ -271,7 +269,7 @@ __global__ __launch_bounds__(512) void mx_weight_kernel(GemmArgs g) {
     const bool last = kt + 1 == KT;
     const int kn = last ? 0 : kt + 1;               // the next stage
     // its piece and scales: the following ones where it starts any
-    const bool np = last || kn % 2 == 0, ns = last || kn % SPER == 0;
+    const bool np = last || kn % 4 == 0, ns = last || kn % SPER == 0;
     rw = np ? (rw + 1 == WNB ? 0 : rw + 1) : rw;
     rs = ns ? (rs + 1 == SNB ? 0 : rs + 1) : rs;
 #pragma unroll
@@ -286,7 +284,7 @@ __global__ __launch_bounds__(512) void mx_weight_kernel(GemmArgs g) {
       }
     pin();
     vm_wait<0>();                                   // the next stage has landed
-    if (TAIL && (kn == KT - 1 || (kn == KT - 2 && kn % 2 == 0))) zero_tail(kn, nx, rw, rs);
+    if (TAIL && kn >= KT - 4) zero_tail(kn, nx, rw, rs);
     lgkm_barrier();                                 // the next stage is there, this one has been read
 #pragma unroll
     for (int j = 0; j < FN; ++j) read_w(j, kn, rw, rs);
@@ -296,8 +294,10 @@ __global__ __launch_bounds__(512) void mx_weight_kernel(GemmArgs g) {
       acc[q / FM][q % FM] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
           wf[1][q / FM], xf[1][q % FM], acc[q / FM][q % FM], 0, 0, 0);
       if (q < FM) read_x(0, q, smem + nx * XST, 0);
-      if (q < 2) issue_w(q);
-      if (q >= 2 && q < 6) issue_x(q - 2);
+      if (q & 1)
+        issue_x(q / 2);
+      else
+        issue_w(q / 2);
       __builtin_amdgcn_sched_barrier(0);
     }
     pin();
@@ -348,7 +348,7 @@ hipError_t launch_mx_weight(const GemmArgs &g, hipStream_t stream) {
   const dim3 grid(kCUs), block(512);
   if (g.K % 512 == 0 && g.mx.ldw % 16 == 0)
     hipLaunchKernelGGL((mx_weight_kernel<GROUPED, true, false>), grid, block, 0, stream, g);
-  else if (g.K % 128 == 0)
+  else if (g.K % 256 == 0)
     hipLaunchKernelGGL((mx_weight_kernel<GROUPED, false, false>), grid, block, 0, stream, g);
   else
     hipLaunchKernelGGL((mx_weight_kernel<GROUPED, false, true>), grid, block, 0, stream, g);
