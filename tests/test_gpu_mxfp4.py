@@ -471,3 +471,38 @@ def test_short_k_fresh_operands_repeated(n, d_in, d_out, x_is_mx):
         else:
             srg.lora_base_gemm_mxfp4w(Xb.to(DEV), *W, out)
         assert bool(((out.double() - Y64).abs() <= tol).all()), rep
+
+
+def test_two_streams_at_once():
+    """Products of every size on two streams at the same time, each with its
+    own operands and outputs: the bits of one call after the other."""
+    d_in, d_out = 544, 2056
+    calls = []
+    for n in (3, 12, 30, 200, 700, 2100):
+        wc, wsc = wl.make_mxfp4(n, d_out, d_in)
+        W = packed(wc, wsc)
+        X = torch.randn(n, d_in, device=DEV, generator=torch.Generator(DEV).manual_seed(n)).bfloat16()
+        Xq = srg.mxfp4_empty(n, d_in)
+        srg.lora_mxfp4_quantize(X, *Xq)
+        calls.append((X, Xq, W))
+    def outputs():
+        return [[torch.full((len(X), d_out), 7.0, dtype=torch.bfloat16, device=DEV) for _ in range(2)]
+                for X, _, _ in calls]
+    def run(outs, order, stream):
+        for i in order:
+            X, Xq, W = calls[i]
+            srg.lora_base_gemm_mxfp4w(X, *W, outs[i][0], stream=stream)
+            srg.lora_base_gemm_mxfp4(*Xq, *W, outs[i][1], stream=stream)
+    want = outputs()
+    run(want, range(len(calls)), None)
+    torch.cuda.synchronize()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    for rep in range(3):
+        a, b = outputs(), outputs()
+        torch.cuda.synchronize()
+        run(a, range(len(calls)), s1)
+        run(b, reversed(range(len(calls))), s2)
+        torch.cuda.synchronize()
+        for got in (a, b):
+            for g, w in zip(got, want):
+                assert all(torch.equal(x, y) for x, y in zip(g, w)), rep
