@@ -54,7 +54,7 @@ hipError_t launch_gemm_mx(const void *X, int64_t ldx, const void *W, int64_t ldw
   }
   GemmArgs g = gemm_args(X, ldx, W, ldw * 2, Y, ldy, M, K, N, H, seg, pool);
   g.mx = mx;
-  if (M <= kStreamRows) return launch_mx_stream(g, lora, stream);
+  if (stream_rows(M, N)) return launch_mx_stream(g, lora, stream);
   // Base-only rows of a batch with adapters have the base product's bits, so both
   // go by the same rule as far as the order of adding up K goes: the 64-tiles', or
   // that of all others.
@@ -83,16 +83,16 @@ hipError_t launch_experts_gemm_mx(const void *X, int64_t ldx, const ExpertView &
     const int64_t t = (int64_t)ex.n_choices / bm + ex.n_experts;
     return (int)(t < ex.n_choices ? t : ex.n_choices);
   };
-  // by the mean rows of an expert, in us.  16 experts of 4096 -> 4096: 2 rows 28 in
-  // tiles of 8 against 38 in tiles of 16, 4 rows 36 against 39, 24 rows 86 streamed
-  // against 61 on the 64-tiles.  64 experts of 2048 -> 1536: 2 rows 25 against 28, 4
-  // rows 31 against 29, 8 rows 38 streamed against 64 on the 64-tiles, 24 rows 69
-  // against 82.  64 rows: 110 on the 64-tiles against 100 on the 256-tiles, and 92
-  // against 104.
+  // by the mean rows of an expert, in us.  2: 16 experts of 4096 -> 4096 28 in tiles
+  // of 8 against 38 in tiles of 16.  Streamed against the 32-row tiles: 3 rows 38
+  // against 31, 8 rows 50 against 33, but where K is short, on 64 experts of 2048 ->
+  // 1536, 4 rows 29 against 35, 8 rows 37 against 38, 16 rows 52 against 43.  Those
+  // against the 256-tiles: 64 rows 89 against 98 and 80 against 97, 96 rows 116
+  // against 100 and 105 against 99.
   const int rows = ex.n_choices / ex.n_experts;
   if (rows <= 2) return launch_experts_stream<4, 2>(g, tiles(8), stream);
-  if (rows <= 16) return launch_experts_stream<4, 1>(g, tiles(16), stream);
-  if (rows < 64) return launch_experts_mid(g, tiles(64), stream);
+  if (rows <= 8 && K <= 2048) return launch_experts_stream<4, 1>(g, tiles(16), stream);
+  if (rows < 80) return launch_experts_mid(g, tiles(32), stream);
   return launch_mx_weight<true>(g, stream);
 }
 

@@ -1,22 +1,24 @@
 // Products with an MXFP4 weight for batches between the streamed and the large
-// ones (decode batches): 64 x 64 tiles, enough of them for every CU at a few
-// hundred rows, under bf16 X (with the LoRA term) or MXFP4 X.
+// ones (decode batches): tiles of 64 x 64, enough of them for every CU at a few
+// hundred rows, or of 32 x 64 where those leave CUs idle and for the experts, under
+// bf16 X (with the LoRA term) or MXFP4 X.
 //
-// Such a tile has little arithmetic for its bytes: at 256 x 4096 x 4096 the
+// A tile has little arithmetic for its bytes: at 256 x 4096 x 4096 the
 // workgroups take 164 MB out of L2 for 8.6 GFLOP, so the kernel is bound by loads
 // and their latency.  K advances in stages of 512 bytes of X row (256 values) or
 // 256 (512 codes): every load instruction covers whole 128-byte lines, and three
-// stages fill the LDS.  Four K groups of two waves take a quarter of a stage each
-// (a wave all 64 rows and 32 columns of it), so a stage costs one barrier for
-// 512 bytes of K (stages are loaded by waves 0-3 and 4-7 in turn, so a wave waits
-// for all of its loads, one stage's, and no wait depends on the order in which
-// they complete); their sums meet in LDS, where each thread then finishes 8
-// columns of one row with its LoRA term, in fp32, and one rounding.
+// stages fill the LDS (half of it with 32 rows: two workgroups share a CU).  Four
+// K groups of two waves take a quarter of a stage each (a wave all of its rows and
+// 32 columns), so a stage costs one barrier for 512 bytes of K (stages are loaded
+// by waves 0-3 and 4-7 in turn, so a wave waits for all of its loads, one stage's,
+// and no wait depends on the order in which they complete); their sums meet in
+// LDS, where each thread then finishes 8 columns of one row with its LoRA term, in
+// fp32, and one rounding.
 //
 // 256 x 4096 x 4096: 12.9 us (16.6 on the tiles of the bf16 product), with a
 // rank-16 adapter a row 18.9 (22.8): 30 MB of B rows from memory; loading them
 // ahead of the last stages, or of all, measured no faster.  Both operands MXFP4:
-// 7.7 us; 333 x 8192 x 1024, 96 tiles, 10.3 us (14).
+// 7.7 us; 333 x 8192 x 1024 8.7 us (10.3 on 96 tiles of 64 rows).
 #pragma once
 
 #include "gemm_tile.cuh"
@@ -24,9 +26,9 @@
 namespace lora {
 namespace {
 
-template <bool XMX, bool LORA, bool DORA, bool GROUPED = false>
+template <int BM, bool XMX, bool LORA, bool DORA, bool GROUPED = false>
 __global__ __launch_bounds__(512) void mx_mid_kernel(GemmArgs g) {
-  constexpr int BM = 64, BN = 64, KG = 4, NST = 3;
+  constexpr int BN = 64, KG = 4, NST = 3, FM = BM / 32;
   constexpr int KS = XMX ? 512 : 256;               // K of a stage
   constexpr int XR = XMX ? 256 : 512, WR = KS / 2;  // bytes of an X and a W row in it
   constexpr int XI = BM * XR / 1024 / 4, WI = BN * WR / 1024 / 4;   // an owner's loads
@@ -35,7 +37,7 @@ __global__ __launch_bounds__(512) void mx_mid_kernel(GemmArgs g) {
   constexpr int WOFF = BM * XR, SOFF = WOFF + BN * WR, STAGE = SOFF + SR * WPR * 4;
   constexpr int SL = SR * WPR / 64, SI = (SL + 3) / 4;   // scales: of a stage, of an owner
   constexpr int RS = BN + 4;
-  static_assert(SR * WPR % 64 == 0 && (SL % 4 == 0 || 4 % SL == 0) && 64 % WPR == 0, "scale loads");
+  static_assert(SR * WPR % 64 == 0 && 64 % WPR == 0, "scale loads");
   static_assert(NST == 3 && NST * STAGE <= 160 * 1024 && KG * BM * RS * 4 <= NST * STAGE, "LDS");
   __shared__ __align__(16) unsigned char smem[NST * STAGE];
 
@@ -63,7 +65,7 @@ __global__ __launch_bounds__(512) void mx_mid_kernel(GemmArgs g) {
   }
 
   // row of this thread's outputs
-  const int e_row = tid / 8, e_c8 = tid % 8 * 8;
+  const int e_row = min(tid / 8, BM - 1), e_c8 = tid % 8 * 8;
   int e_seg = 0;
   if constexpr (LORA) e_seg = g.row_segment[min(m0 + e_row, M - 1)];
 
@@ -103,7 +105,7 @@ __global__ __launch_bounds__(512) void mx_mid_kernel(GemmArgs g) {
   }
   // scales: load i has words [64 si(i), +64) of the stage's (where there are fewer
   // loads than owners, several owners load the same)
-  auto si = [&](int i) { return SL < 4 ? w4 % SL : w4 * SI + i; };
+  auto si = [&](int i) { return SL < 4 ? w4 % SL : min(w4 * SI + i, SL - 1); };
   const int sword = l % WPR;
   const unsigned char *sp[SI];
 #pragma unroll
@@ -162,9 +164,9 @@ __global__ __launch_bounds__(512) void mx_mid_kernel(GemmArgs g) {
   for (int s = 0; s < NST - 1; ++s)
     if (s == grp && s < KT) issue(s, s);
 
-  f32x16 acc[2];
+  f32x16 acc[FM];
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+  for (int i = 0; i < FM; ++i)
 #pragma unroll
     for (int v = 0; v < 16; ++v) acc[i][v] = 0.f;
   int e_r = 0, e_slot = 0;
@@ -183,41 +185,41 @@ __global__ __launch_bounds__(512) void mx_mid_kernel(GemmArgs g) {
   auto multiply = [&]() __attribute__((always_inline)) {
     const unsigned char *st = smem + buf * STAGE;
     if constexpr (XMX) {
-      u32x4 x[2][2], w[2];
-      uint32_t sx[2];
+      u32x4 x[2][FM], w[2];
+      uint32_t sx[FM];
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
         const int c = kg * 4 + s * 2 + h;
         w[s] = *reinterpret_cast<const u32x4 *>(st + WOFF + wrow * WR + wsw(c, wrow) * 16);
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < FM; ++i)
           x[s][i] = *reinterpret_cast<const u32x4 *>(st + (i * 32 + (l & 31)) * XR + xsw(c, l & 31) * 16);
       }
       const uint32_t sw = *reinterpret_cast<const uint32_t *>(st + SOFF + ((BM + wrow) * WPR + kg) * 4) >> (8 * h);
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+      for (int i = 0; i < FM; ++i)
         sx[i] = *reinterpret_cast<const uint32_t *>(st + SOFF + ((i * 32 + (l & 31)) * WPR + kg) * 4) >> (8 * h);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) acc[i] = mfma_mx<0>(x[0][i], w[0], acc[i], sx[i], sw);
+      for (int i = 0; i < FM; ++i) acc[i] = mfma_mx<0>(x[0][i], w[0], acc[i], sx[i], sw);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) acc[i] = mfma_mx<2>(x[1][i], w[1], acc[i], sx[i], sw);
+      for (int i = 0; i < FM; ++i) acc[i] = mfma_mx<2>(x[1][i], w[1], acc[i], sx[i], sw);
     } else {
       const int cw = kg * 2 + h;                    // this half's block of 32 codes
       const u32x4 q = *reinterpret_cast<const u32x4 *>(st + WOFF + wrow * WR + wsw(cw, wrow) * 16);
       const uint32_t s = *reinterpret_cast<const uint32_t *>(st + SOFF + (wrow * WPR + kg / 2) * 4);
       const float sc = __uint_as_float((s >> (((kg & 1) * 2 + h) * 8) & 0xffu) << 23);
-      mfma_bf16x8 x[4][2];
+      mfma_bf16x8 x[4][FM];
 #pragma unroll
       for (int kk = 0; kk < 4; ++kk)
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < FM; ++i)
           x[kk][i] = as_bf16x8(*reinterpret_cast<const u32x4 *>(
               st + (i * 32 + (l & 31)) * XR + xsw(kg * 8 + h * 4 + kk, l & 31) * 16));
 #pragma unroll
       for (int kk = 0; kk < 4; ++kk) {
         const mfma_bf16x8 w = fp4x8_to_bf16x8(q[kk], sc);
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < FM; ++i)
           acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x[kk][i], w, acc[i], 0, 0, 0);
       }
     }
@@ -238,7 +240,7 @@ __global__ __launch_bounds__(512) void mx_mid_kernel(GemmArgs g) {
   lgkm_barrier();                                   // the ring has been read
   float *red = reinterpret_cast<float *>(smem);
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+  for (int i = 0; i < FM; ++i)
 #pragma unroll
     for (int v = 0; v < 16; ++v)
       red[(kg * BM + i * 32 + acc_row(v, l)) * RS + wn * 32 + (l & 31)] = acc[i][v];
@@ -255,7 +257,7 @@ __global__ __launch_bounds__(512) void mx_mid_kernel(GemmArgs g) {
     }
   }
   const int row = m0 + e_row, col = n0 + e_c8;
-  if (row < M && col < N) {                         // N % 8 == 0: all 8 columns or none
+  if (tid / 8 < BM && row < M && col < N) {         // N % 8 == 0: all 8 columns or none
     if constexpr (LORA) {
       if (e_r > 0) lora_row8<DORA>(g, row, col, e_slot, e_r, e_sc, o);
     }
@@ -263,21 +265,31 @@ __global__ __launch_bounds__(512) void mx_mid_kernel(GemmArgs g) {
   }
 }
 
-template <bool XMX>
-hipError_t launch_mx_mid(const GemmArgs &g, bool lora, hipStream_t stream) {
-  const dim3 grid(tile_grid((g.M + 63) / 64, (g.N + 63) / 64)), block(512);
+template <int BM, bool XMX>
+hipError_t launch_mx_mid_rows(const GemmArgs &g, bool lora, hipStream_t stream) {
+  const dim3 grid(tile_grid((g.M + BM - 1) / BM, (g.N + 63) / 64)), block(512);
   if constexpr (!XMX) {
     if (lora && g.dora) {
-      hipLaunchKernelGGL((mx_mid_kernel<false, true, true>), grid, block, 0, stream, g);
+      hipLaunchKernelGGL((mx_mid_kernel<BM, false, true, true>), grid, block, 0, stream, g);
       return hipGetLastError();
     }
     if (lora) {
-      hipLaunchKernelGGL((mx_mid_kernel<false, true, false>), grid, block, 0, stream, g);
+      hipLaunchKernelGGL((mx_mid_kernel<BM, false, true, false>), grid, block, 0, stream, g);
       return hipGetLastError();
     }
   }
-  hipLaunchKernelGGL((mx_mid_kernel<XMX, false, false>), grid, block, 0, stream, g);
+  hipLaunchKernelGGL((mx_mid_kernel<BM, XMX, false, false>), grid, block, 0, stream, g);
   return hipGetLastError();
+}
+template <bool XMX>
+hipError_t launch_mx_mid(const GemmArgs &g, bool lora, hipStream_t stream) {
+  // tiles of 32 rows while they fit the CUs at once, or are no more than those of 64
+  // (in us, 32 against 64: 64 x 4096 x 4096 9.1 against 12.1, 333 x 8192 x 1024 15.4
+  // against 21.5, 32 x 4096 x 14336 9.4 against 12.2; 256 x 4096 x 4096 14.0 against
+  // 13.2, 64 x 8192 x 28672 50 against 44)
+  const int64_t tiles = (int64_t)((g.M + 31) / 32) * ((g.N + 63) / 64);
+  if (tiles <= kCUs || g.M <= 32) return launch_mx_mid_rows<32, XMX>(g, lora, stream);
+  return launch_mx_mid_rows<64, XMX>(g, lora, stream);
 }
 
 // Workgroups for an experts' product of up to tiles_m M-tiles: they find the
@@ -288,7 +300,7 @@ inline int expert_grid(int tiles_m, int tiles_n) {
   return a > b ? a : b;
 }
 inline hipError_t launch_experts_mid(const GemmArgs &g, int tiles_m, hipStream_t stream) {
-  hipLaunchKernelGGL((mx_mid_kernel<false, false, false, true>),
+  hipLaunchKernelGGL((mx_mid_kernel<32, false, false, false, true>),
                      dim3(expert_grid(tiles_m, (g.N + 63) / 64)), dim3(512), 0, stream, g);
   return hipGetLastError();
 }

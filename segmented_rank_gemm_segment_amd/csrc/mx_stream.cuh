@@ -1,5 +1,5 @@
-// Products of few rows with an MXFP4 weight: Y = X dq(W)^T for decode batches,
-// and for the experts' decode products (a few rows on each expert's weight).
+// Products of up to 16 rows with an MXFP4 weight: Y = X dq(W)^T for small decode
+// batches, and the experts' decode products (a few rows on each expert's weight).
 //
 // Bound by reading W (17/32 byte a weight) from HBM, so W goes from memory
 // straight to registers: a workgroup takes NT tiles of W rows, its KW waves every
@@ -8,7 +8,7 @@
 // each widened to bf16 under the block's scale (exact), and the K order inside
 // is the same permutation for X, whose rows are the MFMA's columns.
 //
-// KP 1: a tile is 16 rows of W and up to 16 MT of X; a load takes 64 bytes of each
+// KP 1: a tile is 16 rows of W and up to 16 of X; a load takes 64 bytes of each
 // W row, half of its 128-byte line, and the next load the other half.
 // KP 2: up to 8 rows of X, whose columns the MFMA has twice over.  A tile is 8
 // rows of W, a load takes their whole 128-byte lines: the MFMA's rows (and
@@ -29,16 +29,16 @@
 namespace lora {
 namespace {
 
-template <int NT, int MT>
+template <int NT>
 struct StreamLoad {
-  u32x4 w[NT], x[MT][4];
+  u32x4 w[NT], x[4];
   uint32_t sc[NT];
 };
 
-template <int NT, int KW, int MT, int KP, bool GROUPED, bool LORA, bool DORA>
-__global__ __launch_bounds__(KW *kWave, MT == 1 ? 4 : 2) void mx_stream_kernel(GemmArgs g) {
-  constexpr int T = KW * kWave, RW = 16 / KP, BN = RW * NT, XM = 16 / KP, BM = XM * MT;
-  static_assert(KP == 1 || (KP == 2 && MT == 1), "K parts");
+template <int NT, int KW, int KP, bool GROUPED, bool LORA, bool DORA>
+__global__ __launch_bounds__(KW *kWave, 4) void mx_stream_kernel(GemmArgs g) {
+  constexpr int T = KW * kWave, RW = 16 / KP, BN = RW * NT, BM = 16 / KP;
+  static_assert(KP == 1 || KP == 2, "K parts");
   __shared__ __align__(16) float red[KW][NT][kWave * 4];
   const int tid = threadIdx.x, l = tid & (kWave - 1);
   const int wid = __builtin_amdgcn_readfirstlane(tid / kWave);
@@ -57,7 +57,7 @@ __global__ __launch_bounds__(KW *kWave, MT == 1 ? 4 : 2) void mx_stream_kernel(G
     SW += (int64_t)e * g.ex.s_stride;
   }
   const int n0 = n_idx * BN;
-  const int rows = min(m1 - m0, BM), parts = (rows + XM - 1) / XM;
+  const int rows = min(m1 - m0, BM);
 
   // this lane's W rows and X rows (rows past the ends read the last one), from
   // its block of a load's K on
@@ -70,20 +70,16 @@ __global__ __launch_bounds__(KW *kWave, MT == 1 ? 4 : 2) void mx_stream_kernel(G
     wo[j] = row * (uint32_t)(g.ldw / 2) + kb / 2;
     so[j] = row * (uint32_t)g.mx.ldw;
   }
-  const bf16_t *xp[MT];
-#pragma unroll
-  for (int i = 0; i < MT; ++i) {
-    const int p = m0 + min(i * XM + rw, rows - 1);
-    const int row = GROUPED && g.ex.sorted_choice ? g.ex.sorted_choice[p] / g.ex.top_k : p;
-    xp[i] = g.X + (int64_t)row * g.ldx + kb;
-  }
+  const int p0 = m0 + min(rw, rows - 1);
+  const int x_row = GROUPED && g.ex.sorted_choice ? g.ex.sorted_choice[p0] / g.ex.top_k : p0;
+  const bf16_t *const xp = g.X + (int64_t)x_row * g.ldx + kb;
   const int steps = (K + 255) / 256, last_word = (K / 32 - 1) / 4;
   const int mine = (steps - wid + KW - 1) / KW;     // steps of this wave (negative: none)
   const int loads = KP == 1 ? 2 * mine : mine;
   auto k_of = [&](int p) { return KP == 1 ? ((p >> 1) * KW + wid) * 256 + (p & 1) * 128 : (p * KW + wid) * 256; };
   // blocks past K read their row's start, their X is zeroed and their scale 1 (a
   // NaN would spoil the zeros)
-  auto load = [&](StreamLoad<NT, MT> &t, int p) __attribute__((always_inline)) {
+  auto load = [&](StreamLoad<NT> &t, int p) __attribute__((always_inline)) {
     const int k = k_of(p);
     const bool in = k + kb < K;
     const int kx = in ? k : -kb;
@@ -93,19 +89,15 @@ __global__ __launch_bounds__(KW *kWave, MT == 1 ? 4 : 2) void mx_stream_kernel(G
       t.sc[j] = *reinterpret_cast<const uint32_t *>(sb + (so[j] + 4 * (uint32_t)min(k / 128 + kp, last_word)));
     }
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-      for (int kk = 0; kk < 4; ++kk) {
-        const u32x4 v = *reinterpret_cast<const u32x4 *>(xp[i] + kx + kk * 8);
-        t.x[i][kk] = in ? v : u32x4{0, 0, 0, 0};
-      }
+    for (int kk = 0; kk < 4; ++kk) {
+      const u32x4 v = *reinterpret_cast<const u32x4 *>(xp + kx + kk * 8);
+      t.x[kk] = in ? v : u32x4{0, 0, 0, 0};
+    }
   };
-  f32x4 acc[NT][MT];
+  f32x4 acc[NT];
 #pragma unroll
-  for (int j = 0; j < NT; ++j)
-#pragma unroll
-    for (int i = 0; i < MT; ++i) acc[j][i] = f32x4{0.f, 0.f, 0.f, 0.f};
-  auto multiply = [&](const StreamLoad<NT, MT> &t, int p) __attribute__((always_inline)) {
+  for (int j = 0; j < NT; ++j) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  auto multiply = [&](const StreamLoad<NT> &t, int p) __attribute__((always_inline)) {
     const bool in = k_of(p) + kb < K;
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
@@ -113,14 +105,12 @@ __global__ __launch_bounds__(KW *kWave, MT == 1 ? 4 : 2) void mx_stream_kernel(G
 #pragma unroll
       for (int kk = 0; kk < 4; ++kk) {
         const mfma_bf16x8 w = fp4x8_to_bf16x8(t.w[j][kk], f);
-#pragma unroll
-        for (int i = 0; i < MT; ++i)
-          acc[j][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, as_bf16x8(t.x[i][kk]), acc[j][i], 0, 0, 0);
+        acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, as_bf16x8(t.x[kk]), acc[j], 0, 0, 0);
       }
     }
   };
 
-  StreamLoad<NT, MT> a, b;
+  StreamLoad<NT> a, b;
   if (loads > 0) load(a, 0);
   for (int p = 0; p < loads; p += 2) {
     if (p + 1 < loads) load(b, p + 1);
@@ -129,80 +119,75 @@ __global__ __launch_bounds__(KW *kWave, MT == 1 ? 4 : 2) void mx_stream_kernel(G
     if (p + 1 < loads) multiply(b, p + 1);
   }
 
-  // the waves' sums, XM rows of X at a time: slot (j, lane) holds W rows
-  // [4 (lane / 16), +4) of the MFMA's 16 and its column lane % 16
+  // the waves' sums: slot (j, lane) holds W rows [4 (lane / 16), +4) of the MFMA's
+  // 16 and its column lane % 16
 #pragma unroll
-  for (int i = 0; i < MT; ++i) {
-    if (i >= parts) break;
+  for (int j = 0; j < NT; ++j) *reinterpret_cast<f32x4 *>(&red[wid][j][l * 4]) = acc[j];
+  __syncthreads();
+  // a thread finishes 8 columns of one row
+  for (int q = tid; q < NT * BM * (RW / 8); q += T) {
+    const int r = q % BM, h = q / BM % (RW / 8), j = q / (BM * (RW / 8));
+    float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int j = 0; j < NT; ++j)
-      *reinterpret_cast<f32x4 *>(&red[wid][j][l * 4]) = acc[j][i];
-    __syncthreads();
-    // a thread finishes 8 columns of one row
-    for (int q = tid; q < NT * XM * (RW / 8); q += T) {
-      const int r = q % XM, h = q / XM % (RW / 8), j = q / (XM * (RW / 8));
-      float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    for (int w = 0; w < KW; ++w)
 #pragma unroll
-      for (int w = 0; w < KW; ++w)
+      for (int c = 0; c < KP; ++c) {
+        const int at = r + c * BM + 16 * (c * (4 / KP) + 2 * h);
+        const f32x4 lo = *reinterpret_cast<const f32x4 *>(&red[w][j][at * 4]);
+        const f32x4 hi = *reinterpret_cast<const f32x4 *>(&red[w][j][(at + 16) * 4]);
 #pragma unroll
-        for (int c = 0; c < KP; ++c) {
-          const int at = r + c * XM + 16 * (c * (4 / KP) + 2 * h);
-          const f32x4 lo = *reinterpret_cast<const f32x4 *>(&red[w][j][at * 4]);
-          const f32x4 hi = *reinterpret_cast<const f32x4 *>(&red[w][j][(at + 16) * 4]);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            o[e] += lo[e];
-            o[4 + e] += hi[e];
-          }
+        for (int e = 0; e < 4; ++e) {
+          o[e] += lo[e];
+          o[4 + e] += hi[e];
         }
-      const int row = m0 + i * XM + r, col = n0 + j * RW + h * 8;
-      if (i * XM + r < rows && col < N) {           // N % 8 == 0: all 8 columns or none
-        if constexpr (LORA) {
-          const int sg = g.row_segment[row], rank = g.seg_rank[sg];
-          if (rank > 0) lora_row8<DORA>(g, row, col, g.seg_slot[sg], rank, g.seg_scale[sg], o);
-        }
-        stg16(g.Y + (int64_t)row * g.ldy + col, Elem<bf16_t>::pack(o));
       }
+    const int row = m0 + r, col = n0 + j * RW + h * 8;
+    if (r < rows && col < N) {                      // N % 8 == 0: all 8 columns or none
+      if constexpr (LORA) {
+        const int sg = g.row_segment[row], rank = g.seg_rank[sg];
+        if (rank > 0) lora_row8<DORA>(g, row, col, g.seg_slot[sg], rank, g.seg_scale[sg], o);
+      }
+      stg16(g.Y + (int64_t)row * g.ldy + col, Elem<bf16_t>::pack(o));
     }
-    if (i + 1 < parts) __syncthreads();
   }
 }
 
-template <int NT, int KW, int MT, int KP>
+template <int NT, int KW, int KP>
 hipError_t launch_stream(const GemmArgs &g, bool lora, hipStream_t stream) {
   constexpr int BN = 16 / KP * NT;
   const dim3 grid((g.N + BN - 1) / BN), block(KW * kWave);
   if (lora && g.dora)
-    hipLaunchKernelGGL((mx_stream_kernel<NT, KW, MT, KP, false, true, true>), grid, block, 0, stream, g);
+    hipLaunchKernelGGL((mx_stream_kernel<NT, KW, KP, false, true, true>), grid, block, 0, stream, g);
   else if (lora)
-    hipLaunchKernelGGL((mx_stream_kernel<NT, KW, MT, KP, false, true, false>), grid, block, 0, stream, g);
+    hipLaunchKernelGGL((mx_stream_kernel<NT, KW, KP, false, true, false>), grid, block, 0, stream, g);
   else
-    hipLaunchKernelGGL((mx_stream_kernel<NT, KW, MT, KP, false, false, false>), grid, block, 0, stream, g);
+    hipLaunchKernelGGL((mx_stream_kernel<NT, KW, KP, false, false, false>), grid, block, 0, stream, g);
   return hipGetLastError();
 }
 
-// Most rows of a dense batch that the kernel takes.
-constexpr int kStreamRows = 32;
+// Whether a dense batch is the kernel's: up to 8 rows; up to 16 where the 32-row
+// tiles would leave half of the CUs idle (16 rows, streamed against those: 4096 ->
+// 4096 7.8 us against 9.0, 8192 -> 1024 12.7 against 14.8, 4096 -> 14336 16.6 against
+// 9.6, 8192 -> 28672 45 against 42).
+inline bool stream_rows(int M, int N) { return M <= 8 || (M <= 16 && N < 64 * kCUs / 2); }
 
 // The widest workgroups that still give every CU one.
-template <int MT, int KP>
+template <int KP>
 hipError_t launch_stream_rows(const GemmArgs &g, bool lora, hipStream_t stream) {
   constexpr int RW = 16 / KP;
-  if (g.N >= 4 * RW * kCUs) return launch_stream<4, 8, MT, KP>(g, lora, stream);
-  if (g.N >= 2 * RW * kCUs) return launch_stream<2, 8, MT, KP>(g, lora, stream);
-  return launch_stream<1, 8, MT, KP>(g, lora, stream);
+  if (g.N >= 4 * RW * kCUs) return launch_stream<4, 8, KP>(g, lora, stream);
+  if (g.N >= 2 * RW * kCUs) return launch_stream<2, 8, KP>(g, lora, stream);
+  return launch_stream<1, 8, KP>(g, lora, stream);
 }
 inline hipError_t launch_mx_stream(const GemmArgs &g, bool lora, hipStream_t stream) {
-  if (g.M <= 8) return launch_stream_rows<1, 2>(g, lora, stream);
-  if (g.M <= 16) return launch_stream_rows<1, 1>(g, lora, stream);
-  return launch_stream_rows<2, 1>(g, lora, stream);
+  return g.M <= 8 ? launch_stream_rows<2>(g, lora, stream) : launch_stream_rows<1>(g, lora, stream);
 }
 
 template <int NT, int KP>
 hipError_t launch_experts_stream(const GemmArgs &g, int tiles_m, hipStream_t stream) {
   constexpr int BN = 16 / KP * NT;
   const int64_t tn = (g.N + BN - 1) / BN;
-  hipLaunchKernelGGL((mx_stream_kernel<NT, 4, 1, KP, true, false, false>), dim3((unsigned)(tn * tiles_m)),
+  hipLaunchKernelGGL((mx_stream_kernel<NT, 4, KP, true, false, false>), dim3((unsigned)(tn * tiles_m)),
                      dim3(4 * kWave), 0, stream, g);
   return hipGetLastError();
 }

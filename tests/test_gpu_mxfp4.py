@@ -133,6 +133,8 @@ SHAPES = [
     (1, 32, 8), (1, 4096, 264), (2, 96, 16), (5, 1056, 40), (16, 512, 64), (17, 544, 72),
     (33, 2080, 200), (64, 1024, 128), (100, 160, 264), (300, 736, 264), (512, 256, 384),
     (700, 224, 136), (1100, 352, 520), (1100, 96, 8200), (2040, 288, 7944),
+    # 32-row tiles: up to 32 rows, and few tiles of 64
+    (12, 544, 8200), (16, 96, 16392), (25, 1056, 8200), (32, 2080, 200), (60, 800, 8136),
 ]
 
 
@@ -228,6 +230,9 @@ LORA_CASES = [
     (606, 700, 224, 136, 7, 64, 0.1, True),
     (607, 1100, 96, 8200, 7, 64, 0.1, True),
     (608, 2040, 96, 7944, 7, 32, 0.1, True),
+    (609, 20, 544, 264, 9, 64, 0.2, False),
+    (610, 12, 96, 8200, 5, 32, 0.2, False),
+    (611, 60, 608, 8136, 20, 16, 0.1, False),
 ]
 
 
