@@ -58,7 +58,7 @@ hipError_t launch_gemm_mx(const void *X, int64_t ldx, const void *W, int64_t ldw
   // Base-only rows of a batch with adapters have the base product's bits, so both
   // go by the same rule as far as the order of adding up K goes: the 64-tiles', or
   // that of all others.
-  const TileCost c = tile_cost(M, N, 15, 50, 86);
+  const TileCost c = tile_cost(M, N, 12.8, 46.5, 85);
   if (c.t64 <= c.t128 && c.t64 <= c.t256) return launch_mx_mid<false>(g, lora, stream);
   if (!lora)
     return c.t256 <= c.t128 ? launch_mx_weight<false>(g, stream)
@@ -67,7 +67,7 @@ hipError_t launch_gemm_mx(const void *X, int64_t ldx, const void *W, int64_t ldw
   // memory into each wave's fragments instead, at the end of the persistent
   // kernel's tiles, it cost 11 us a tile, and the two were level (16943 x 4096 x
   // 14336, 8 slots: 1.69 ms).
-  if (c.t128 <= c.t256 * (109. / 86)) return launch_tile<LORA_GEMM_MID, kMxW>(g, true, stream);
+  if (c.t128 <= c.t256 * (109. / 85)) return launch_tile<LORA_GEMM_MID, kMxW>(g, true, stream);
   if (large192_tiles(M, N)) return launch_tile<LORA_GEMM_LARGE192, kMxW>(g, true, stream);
   return launch_tile<LORA_GEMM_LARGE, kMxW>(g, true, stream);
 }
