@@ -33,6 +33,7 @@
 #include "lds_dma.cuh"
 #include "lora_device.cuh"
 #include "lora_kernels.h"
+#include "tile_choice.h"
 
 namespace lora {
 namespace {
@@ -104,11 +105,6 @@ struct GemmArgs {
 #endif
 #ifndef LORA_GEMM_LARGE192_F8
 #define LORA_GEMM_LARGE192_F8 LORA_GEMM_LARGE192
-#endif
-// Relative cost per output element of a 192 x 256 tile against a 256 x 256
-// one (more LDS fragment reads per flop), in percent.
-#ifndef LORA_GEMM_192_COST
-#define LORA_GEMM_192_COST 110
 #endif
 // Large and mid tiles with more LoRA runs than this (consecutive rows of one
 // segment; decode rows make one each) finish row by row on the VALU instead
@@ -369,7 +365,6 @@ __device__ __forceinline__ void lora_row8_pair(const GemmArgs &g, const int (&gr
 constexpr int kTileGroup = 8;
 constexpr int kTileGroupSplit = 16;   // M-tiles per group with the N split
 constexpr int kHeavyMaxTilesM = 32;
-constexpr int kCUs = 256;   // compute units of an MI355X
 __host__ __device__ inline bool n_split(int tiles_m, int tiles_n) {
   return tiles_n >= 8 && tiles_m <= kHeavyMaxTilesM;
 }
@@ -1587,18 +1582,9 @@ hipError_t launch_rows_split(GemmArgs g, bool lora, Launch launch) {
   return e != hipSuccess ? e : launch(g2);
 }
 
-// Whether a batch of M rows takes the mid-size tiles, and whether its large
-// tiles are 192 x 256: those are taken when their rounds of kCUs tiles cost
-// less (rounds times tile area, the narrower tile charged its extra LDS
-// traffic per flop).
+// Whether a batch of M rows takes the mid-size tiles.
 inline bool mid_tiles(int M, int N) {
   return ((int64_t)(M + 255) / 256) * ((N + 255) / 256) <= LORA_GEMM_MID_TILES;
-}
-inline bool large192_tiles(int M, int N) {
-  const int64_t tn256 = (N + 255) / 256;
-  const int64_t r256 = ((int64_t)(M + 255) / 256 * tn256 + kCUs - 1) / kCUs;
-  const int64_t r192 = ((int64_t)(M + 191) / 192 * tn256 + kCUs - 1) / kCUs;
-  return r192 * 192 * LORA_GEMM_192_COST < r256 * 256 * 100;
 }
 
 }  // namespace

@@ -282,14 +282,9 @@ hipError_t launch_mx_mid_rows(const GemmArgs &g, bool lora, hipStream_t stream) 
   return hipGetLastError();
 }
 template <bool XMX>
-hipError_t launch_mx_mid(const GemmArgs &g, bool lora, hipStream_t stream) {
-  // tiles of 32 rows while they fit the CUs at once, or are no more than those of 64
-  // (in us, 32 against 64: 64 x 4096 x 4096 9.1 against 12.1, 333 x 8192 x 1024 15.4
-  // against 21.5, 32 x 4096 x 14336 9.4 against 12.2; 256 x 4096 x 4096 14.0 against
-  // 13.2, 64 x 8192 x 28672 50 against 44)
-  const int64_t tiles = (int64_t)((g.M + 31) / 32) * ((g.N + 63) / 64);
-  if (tiles <= kCUs || g.M <= 32) return launch_mx_mid_rows<32, XMX>(g, lora, stream);
-  return launch_mx_mid_rows<64, XMX>(g, lora, stream);
+hipError_t launch_mx_mid(const GemmArgs &g, MxKernel k, bool lora, hipStream_t stream) {
+  return k == kMxTiles32 ? launch_mx_mid_rows<32, XMX>(g, lora, stream)
+                         : launch_mx_mid_rows<64, XMX>(g, lora, stream);
 }
 
 // Workgroups for an experts' product of up to tiles_m M-tiles: they find the

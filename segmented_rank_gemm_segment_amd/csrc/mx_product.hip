@@ -29,6 +29,7 @@
 #include "lds_dma.cuh"
 #include "lora_device.cuh"
 #include "lora_kernels.h"
+#include "tile_choice.h"
 
 namespace lora {
 namespace {
@@ -43,7 +44,6 @@ struct MxGemmArgs {
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 
-constexpr int kProductCUs = 256;
 constexpr int kProductGroup = 8;   // M-tiles per group of the tile order
 
 // SEL: the scale words' byte of this product's block (lds_dma.cuh's fragment
@@ -329,11 +329,10 @@ hipError_t launch_mx_product(const void *X, int64_t ldx, const void *W, int64_t 
                              hipStream_t stream) {
   const MxGemmArgs g{(const unsigned char *)X, mx.x, (const unsigned char *)W, mx.w,
                      ldx, mx.ldx, ldw, mx.ldw, (bf16_t *)Y, ldy, M, K, N};
-  // four scale words at a time where every row's are whole and aligned to that
-  if (K % 512 == 0 && mx.ldx % 16 == 0 && mx.ldw % 16 == 0)
-    hipLaunchKernelGGL((mx_product_kernel<256, 256, 4, 2, true>), dim3(kProductCUs), dim3(512), 0, stream, g);
+  if (mx_wide_scales(K, mx.ldw, mx.ldx))
+    hipLaunchKernelGGL((mx_product_kernel<256, 256, 4, 2, true>), dim3(kCUs), dim3(512), 0, stream, g);
   else
-    hipLaunchKernelGGL((mx_product_kernel<256, 256, 4, 2, false>), dim3(kProductCUs), dim3(512), 0, stream, g);
+    hipLaunchKernelGGL((mx_product_kernel<256, 256, 4, 2, false>), dim3(kCUs), dim3(512), 0, stream, g);
   return hipGetLastError();
 }
 

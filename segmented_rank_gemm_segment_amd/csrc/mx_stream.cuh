@@ -165,22 +165,15 @@ hipError_t launch_stream(const GemmArgs &g, bool lora, hipStream_t stream) {
   return hipGetLastError();
 }
 
-// Whether a dense batch is the kernel's: up to 8 rows; up to 16 where the 32-row
-// tiles would leave half of the CUs idle (16 rows, streamed against those: 4096 ->
-// 4096 7.8 us against 9.0, 8192 -> 1024 12.7 against 14.8, 4096 -> 14336 16.6 against
-// 9.6, 8192 -> 28672 45 against 42).
-inline bool stream_rows(int M, int N) { return M <= 8 || (M <= 16 && N < 64 * kCUs / 2); }
-
-// The widest workgroups that still give every CU one.
 template <int KP>
-hipError_t launch_stream_rows(const GemmArgs &g, bool lora, hipStream_t stream) {
-  constexpr int RW = 16 / KP;
-  if (g.N >= 4 * RW * kCUs) return launch_stream<4, 8, KP>(g, lora, stream);
-  if (g.N >= 2 * RW * kCUs) return launch_stream<2, 8, KP>(g, lora, stream);
+hipError_t launch_stream_rows(const GemmArgs &g, int tiles, bool lora, hipStream_t stream) {
+  if (tiles == 4) return launch_stream<4, 8, KP>(g, lora, stream);
+  if (tiles == 2) return launch_stream<2, 8, KP>(g, lora, stream);
   return launch_stream<1, 8, KP>(g, lora, stream);
 }
-inline hipError_t launch_mx_stream(const GemmArgs &g, bool lora, hipStream_t stream) {
-  return g.M <= 8 ? launch_stream_rows<2>(g, lora, stream) : launch_stream_rows<1>(g, lora, stream);
+inline hipError_t launch_mx_stream(const GemmArgs &g, MxKernel k, bool lora, hipStream_t stream) {
+  if (k == kMxStream8) return launch_stream_rows<2>(g, mx_stream8_tiles(g.N), lora, stream);
+  return launch_stream_rows<1>(g, g.N >= 64 * kCUs ? 4 : g.N >= 32 * kCUs ? 2 : 1, lora, stream);
 }
 
 template <int NT, int KP>

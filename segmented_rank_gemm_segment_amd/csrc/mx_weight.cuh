@@ -346,7 +346,7 @@ __global__ __launch_bounds__(512) void mx_weight_kernel(GemmArgs g) {
 template <bool GROUPED>
 hipError_t launch_mx_weight(const GemmArgs &g, hipStream_t stream) {
   const dim3 grid(kCUs), block(512);
-  if (g.K % 512 == 0 && g.mx.ldw % 16 == 0)
+  if (mx_wide_scales(g.K, g.mx.ldw))
     hipLaunchKernelGGL((mx_weight_kernel<GROUPED, true, false>), grid, block, 0, stream, g);
   else if (g.K % 256 == 0)
     hipLaunchKernelGGL((mx_weight_kernel<GROUPED, false, false>), grid, block, 0, stream, g);

@@ -1,0 +1,89 @@
+"""The shapes of the MXFP4 GPU tests against the rules that choose a kernel
+(csrc/tile_choice.h, compiled here for the host): every kernel that a call can
+reach has a shape, so a changed border cannot leave one untested."""
+import ctypes
+import os
+import subprocess
+
+import pytest
+
+import segmented_rank_gemm_segment_amd as srg
+import test_gpu_experts as experts
+import test_gpu_mxfp4_kernels as kernels
+
+WRAP = """
+#include "tile_choice.h"
+extern "C" int weight(int M, int N, int lora) { return lora::mx_weight_kernel_of(M, N, lora != 0); }
+extern "C" int both(int M, int N) { return lora::mx_both_kernel_of(M, N); }
+extern "C" int experts(int n, int E, int K) { return lora::mx_experts_kernel_of(n, E, K); }
+extern "C" int tiles8(int N) { return lora::mx_stream8_tiles(N); }
+extern "C" int wide(int K, long ldw, long ldx) { return lora::mx_wide_scales(K, ldw, ldx); }
+"""
+STREAM8, STREAM16, T32, T64, T128, T192, T256, PERSISTENT = range(8)
+DIMS = [8, 136, 1024, 2048, 2056, 4096, 4104, 6144, 8192, 8200, 14336, 28672]
+ROWS = [1, 8, 9, 16, 17, 32, 33, 64, 100, 256, 300, 512, 700, 1024, 1500, 2048, 2304, 4096, 8192, 16384, 65536]
+
+
+@pytest.fixture(scope="module")
+def rules(tmp_path_factory):
+    d = tmp_path_factory.mktemp("rules")
+    (d / "wrap.cpp").write_text(WRAP)
+    csrc = os.path.join(os.path.dirname(os.path.abspath(srg.__file__)), "csrc")
+    subprocess.run(["g++", "-std=c++17", "-O1", "-Wall", "-Werror", "-shared", "-fPIC", "-I" + csrc,
+                    str(d / "wrap.cpp"), "-o", str(d / "rules.so")], check=True)
+    L = ctypes.CDLL(str(d / "rules.so"))
+    L.wide.argtypes = [ctypes.c_int, ctypes.c_long, ctypes.c_long]
+    return L
+
+
+def weight_key(L, n, d_in, d_out, lora):
+    k = L.weight(n, d_out, int(lora))
+    if k == STREAM8:
+        return k, L.tiles8(d_out)
+    if k == PERSISTENT:                      # the scale rows' width, and a tail of K
+        return k, bool(L.wide(d_in, (d_in // 32 + 15) // 16 * 16, 0)), d_in % 256 != 0
+    return (k,)
+
+
+@pytest.mark.parametrize("lora", [False, True])
+def test_every_weight_kernel_has_a_shape(rules, lora):
+    reached = {weight_key(rules, n, d_in, d_out, lora)
+               for n in ROWS for d_out in DIMS for d_in in (512, 768, 608)}
+    shapes = [s[:3] for s in kernels.LORA_SHAPES] if lora else kernels.WEIGHT_SHAPES
+    tested = {weight_key(rules, *s, lora) for s in shapes}
+    assert reached <= tested, sorted(reached - tested)
+    assert (T192 in {k[0] for k in reached}) == lora and (PERSISTENT in {k[0] for k in reached}) != lora
+
+
+def test_every_kernel_of_two_mxfp4_operands_has_a_shape(rules):
+    def key(n, d_in, d_out, pad):
+        k = rules.both(n, d_out)
+        ld = (d_in // 32 + 15) // 16 * 16 + pad
+        return (k, bool(rules.wide(d_in, ld, ld))) if k == PERSISTENT else (k,)
+    reached = {key(n, d_in, d_out, 0) for n in ROWS for d_out in DIMS for d_in in (512, 608)}
+    tested = {key(*s, pad) for s in kernels.BOTH_SHAPES for pad in (0, 4)}
+    assert reached <= tested and len(reached) == 5, sorted(reached - tested)
+
+
+def test_every_experts_kernel_has_a_shape(rules):
+    def key(n, E, d_in):
+        k = rules.experts(n, E, d_in)
+        if k == PERSISTENT:
+            return k, bool(rules.wide(d_in, (d_in // 32 + 15) // 16 * 16, 0)), d_in % 256 != 0
+        return (k,)
+    tested = {key(n * k, E, d_in) for n, k, E, d_in, _ in kernels.EXPERT_SHAPES}
+    reached = {key(n * k, E, d_in) for n in ROWS for k in (1, 8) for E in (1, 8, 64, 1000)
+               for d_in in (512, 2048, 4096, 768, 608)}
+    assert reached <= tested | {(STREAM8,)}, sorted(reached - tested)
+    shapes = [m.args[1] for m in experts.test_experts_product.pytestmark
+              if m.name == "parametrize" and "d_in" in m.args[0]]
+    assert STREAM8 in {rules.experts(n * k, E, d_in) for s in shapes for n, k, E, d_in, _, _ in s}
+
+
+def test_base_rows_share_a_k_order(rules):
+    """With adapters or without, a batch's kernel adds K up in one order: streamed,
+    the four groups of the 32- and 64-row tiles, or that of all others."""
+    order = {STREAM8: 8, STREAM16: 16, T32: 4, T64: 4, T128: 1, T192: 1, T256: 1, PERSISTENT: 1}
+    for n in range(1, 3000, 7):
+        for d_out in DIMS:
+            assert order[rules.weight(n, d_out, 0)] == order[rules.weight(n, d_out, 1)], (n, d_out)
