@@ -755,7 +755,8 @@ def lora_linear_fused_mxfp4w(X: torch.Tensor, Wq: torch.Tensor, w_scale: torch.T
         raise ValueError("shapes: X [n, d_in], Wq [d_out, d_in / 2], Y [n, d_out]")
     if H.dtype != torch.float32 or tuple(H.shape) != (seg.n_rows, pool.r_max) or not H.is_contiguous():
         raise ValueError("H: contiguous float32 [n_rows, r_max]")
-    st = _launch_stream(stream, X, Wq, w_scale, H, Y)
+    # (what a pool allocates is on its A's device, and a batch's segments on one)
+    st = _launch_stream(stream, X, Wq, w_scale, H, Y, pool.A, pool.Bt, seg.row_segment)
     _check(lib().lora_linear_fused_mxfp4w(_ptr(X), _ld(X), *w, _ptr(H), seg.c, pool.c, _ptr(Y),
                                           _ld(Y), st))
 

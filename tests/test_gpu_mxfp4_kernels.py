@@ -248,3 +248,16 @@ def test_experts(n, k, E, d_in, d_out, gathered):
         Y64[p] = X64 @ W64.t()
         acc[p] = d_in * U * (X64.abs() @ W64.abs().t())
     check(Y[:len(order)], Y64, acc, "experts")
+
+
+def test_segments_on_the_host_are_refused():
+    n, d_in, d_out = 5, 64, 16
+    w = wl.make_random(3, n, d_in, d_out, 2, 8, dtype="bf16")
+    d = wl.device_tensors(w, DEV)
+    pool = srg.Pool(d["A"], d["Bt"], d["slot_rank"], w.slot_alpha)
+    Wq, ws = srg.mxfp4_empty(d_out, d_in, DEV)
+    Y = torch.full((n, d_out), 7.0, dtype=torch.bfloat16, device=DEV)
+    H = torch.zeros((n, 8), device=DEV)
+    with pytest.raises(ValueError):
+        srg.lora_linear_fused_mxfp4w(d["X"], Wq, ws, H, srg.Segments(n, 2, "cpu"), pool, Y)
+    assert bool((Y == 7.0).all())
