@@ -646,7 +646,7 @@ __global__ __launch_bounds__(WM *WN *KG *kWave) void gemm_bf16_kernel(GemmArgs g
         WQ == kMxXW && row < BM
             ? g.mx.x + (int64_t)min(m0 + row, M - 1) * g.mx.ldx
             : g.mx.w + (int64_t)min(n0 + row - (WQ == kMxXW ? BM : 0), N - 1) * g.mx.ldw;
-    dma4(__builtin_amdgcn_readfirstlane(slice + C::SOFF + q * 256), src + w * 4);
+    dma4(__builtin_amdgcn_readfirstlane(slice + q * 256), C::SOFF, src + w * 4);
   };
   // blocks past K: scale 1 (their codes are zeroed; a NaN scale would spoil them)
   auto fix_scales = [&](int q, unsigned char *slice, int k0) __attribute__((always_inline)) {
@@ -662,10 +662,10 @@ __global__ __launch_bounds__(WM *WN *KG *kWave) void gemm_bf16_kernel(GemmArgs g
     // zeroed in LDS before use
 #pragma unroll
     for (int i = 0; i < C::AI; ++i)
-      dma16(a_dst + stage * C::STAGE + i * 1024,
+      dma16(a_dst + stage * C::STAGE, i * 1024,
             asrc[i] + ((k0 + alc[i] * 8 < K) ? k0 : -alc[i] * 8));
 #pragma unroll
-    for (int i = 0; i < C::BI; ++i) dma16(b_dst + stage * C::STAGE + i * 1024, bsrc[i] + boff(i, k0));
+    for (int i = 0; i < C::BI; ++i) dma16(b_dst + stage * C::STAGE, i * 1024, bsrc[i] + boff(i, k0));
     if constexpr (MX) {
 #pragma unroll
       for (int i = 0; i < C::SI; ++i)
@@ -676,10 +676,10 @@ __global__ __launch_bounds__(WM *WN *KG *kWave) void gemm_bf16_kernel(GemmArgs g
   // instruction q of a stage's DMA (A rows first, then B rows)
   auto issue_one = [&](int q, int stage, int k0) __attribute__((always_inline)) {
     if (q < C::AI)
-      dma16(a_dst + stage * C::STAGE + q * 1024,
+      dma16(a_dst + stage * C::STAGE, q * 1024,
             asrc[q] + ((k0 + alc[q] * 8 < K) ? k0 : -alc[q] * 8));
     else if (q < C::AI + C::BI)
-      dma16(b_dst + stage * C::STAGE + (q - C::AI) * 1024, bsrc[q - C::AI] + boff(q - C::AI, k0));
+      dma16(b_dst + stage * C::STAGE, (q - C::AI) * 1024, bsrc[q - C::AI] + boff(q - C::AI, k0));
     else if (MX && wid * C::SI + q - C::AI - C::BI < C::SCI)
       issue_scales(wid * C::SI + q - C::AI - C::BI, sbase + kgrp * C::GSTAGE + stage * C::STAGE, k0);
   };
@@ -722,26 +722,25 @@ __global__ __launch_bounds__(WM *WN *KG *kWave) void gemm_bf16_kernel(GemmArgs g
   // buffer buf; `tail`: the stage reaches past K, where a chunk past K reads
   // its row's first chunk instead (in bounds; zeroed before use)
   auto issue_own_one = [&](int t, int buf, int k0, bool tail) __attribute__((always_inline)) {
-    const uint32_t dst =
-        __builtin_amdgcn_readfirstlane(sbase + buf * C::STAGE + kgrp * C::GSTAGE + t * 1024);
+    const uint32_t dst = __builtin_amdgcn_readfirstlane(sbase + buf * C::STAGE + kgrp * C::GSTAGE);
     if (t >= NIB) {
       if constexpr (MX) issue_scales(t - NIB, sbase + buf * C::STAGE + kgrp * C::GSTAGE, k0);
     } else if (t < AIG) {
       if (!tail) {
-        dma16_s(dst, own_off[t], xa + (int64_t)k0 * 2);
+        dma16_s(dst, t * 1024, own_off[t], xa + (int64_t)k0 * 2);
       } else {
         // the base stays scalar: the K position goes into the lane offsets
         const int row = t * C::RPI + rr;
         const int c = C::swz(l % C::CH, row);
-        dma16_s(dst, k0 + c * 8 < K ? own_off[t] + k0 * 2 : own_off[t] - c * 16, xa);
+        dma16_s(dst, t * 1024, k0 + c * 8 < K ? own_off[t] + k0 * 2 : own_off[t] - c * 16, xa);
       }
     } else {
       if (!tail) {
-        dma16_s(dst, own_off[t], wb + wbytes((int64_t)k0));
+        dma16_s(dst, t * 1024, own_off[t], wb + wbytes((int64_t)k0));
       } else {
         const int row = (t - AIG) * C::RPIB + rrb;
         const int c = C::swzb(l % C::CHB, row);
-        dma16_s(dst, k0 + c * C::EPCB < K ? own_off[t] + wbytes(k0) : own_off[t] - c * 16, wb);
+        dma16_s(dst, t * 1024, k0 + c * C::EPCB < K ? own_off[t] + wbytes(k0) : own_off[t] - c * 16, wb);
       }
     }
   };

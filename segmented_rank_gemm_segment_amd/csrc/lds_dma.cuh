@@ -12,58 +12,59 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 // ---------------------------------------------------------------------------
 // Direct global -> LDS loads (gfx950 global_load_lds_dwordx4).  Each
-// instruction moves 64 lanes x 16 bytes into 1 KB of LDS starting at M0.
-// Issued through inline asm so that the compiler does not add conservative
-// waits on them; completion is tracked by hand with s_waitcnt vmcnt(0) only
-// (a wave waits for all of its loads, never for a count of them, so no wait
-// depends on the order in which loads complete).  Between the write of M0 and the
-// load that reads it the ISA asks for one wait state, which the compiler does not
-// add inside asm.
+// instruction moves 64 lanes x 16 bytes into 1 KB of LDS starting at M0, here
+// the scalar `base` plus the constant `at` (known once the loop around is
+// unrolled).  Issued through inline asm so that the compiler does not add
+// conservative waits on them; completion is tracked by hand with s_waitcnt
+// vmcnt(0) only (a wave waits for all of its loads, never for a count of them, so
+// no wait depends on the order in which loads complete).  Between the write of M0
+// and the load that reads it the ISA asks for one wait state, which the compiler
+// does not add inside asm; the addition in the write of M0 pays for it.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ uint32_t lds_offset(const void *p) {
   return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void *)p;
 }
 
-__device__ __forceinline__ void dma16(uint32_t m0, const void *src) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(m0), "v"(src)
-               : "memory", "m0");
+#define LORA_SET_M0 "s_add_u32 m0, %0, %1\n\ts_nop 0\n\t"
+__device__ __forceinline__ void dma16(uint32_t base, int at, const void *src) {
+  asm volatile(LORA_SET_M0 "global_load_lds_dwordx4 %2, off" ::"s"(base), "i"(at), "v"(src)
+               : "memory", "m0", "scc");
 }
 
 // The same with the source given as a 64-bit scalar base plus a 32-bit
 // per-lane byte offset (the instruction's saddr form).
-__device__ __forceinline__ void dma16_s(uint32_t m0, uint32_t off, const void *base) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(m0), "v"(off), "s"(base)
-               : "memory", "m0");
-}
-
-// The same unless `skip` (a wave's scalar) is other than 0.  The branch is inside the asm:
-// one that the compiler saw would split the block of products around it.
-__device__ __forceinline__ void dma16_s_unless(uint32_t skip, uint32_t m0, uint32_t off, const void *base) {
-  asm volatile("s_cmp_lg_u32 %0, 0\n\ts_cbranch_scc1 .Ldma16_skip_%=\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\t"
-               "global_load_lds_dwordx4 %2, %3\n.Ldma16_skip_%=:" ::"s"(skip), "s"(m0), "v"(off), "s"(base)
-               : "memory", "m0", "scc");
-}
-
-__device__ __forceinline__ void dma4_s(uint32_t m0, uint32_t off, const void *base) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2" ::"s"(m0), "v"(off), "s"(base)
-               : "memory", "m0");
-}
-__device__ __forceinline__ void dma4_s_unless(uint32_t skip, uint32_t m0, uint32_t off, const void *base) {
-  asm volatile("s_cmp_lg_u32 %0, 0\n\ts_cbranch_scc1 .Ldma4_skip_%=\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\t"
-               "global_load_lds_dword %2, %3\n.Ldma4_skip_%=:" ::"s"(skip), "s"(m0), "v"(off), "s"(base)
-               : "memory", "m0", "scc");
-}
-__device__ __forceinline__ void dma16_unless(uint32_t skip, uint32_t m0, const void *src) {
-  asm volatile("s_cmp_lg_u32 %0, 0\n\ts_cbranch_scc1 .Ldma16v_skip_%=\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\t"
-               "global_load_lds_dwordx4 %2, off\n.Ldma16v_skip_%=:" ::"s"(skip), "s"(m0), "v"(src)
+__device__ __forceinline__ void dma16_s(uint32_t base, int at, uint32_t off, const void *src) {
+  asm volatile(LORA_SET_M0 "global_load_lds_dwordx4 %2, %3" ::"s"(base), "i"(at), "v"(off), "s"(src)
                : "memory", "m0", "scc");
 }
 
 // One dword per lane: 64 lanes x 4 bytes into 256 bytes of LDS.
-__device__ __forceinline__ void dma4(uint32_t m0, const void *src) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(m0), "v"(src)
-               : "memory", "m0");
+__device__ __forceinline__ void dma4(uint32_t base, int at, const void *src) {
+  asm volatile(LORA_SET_M0 "global_load_lds_dword %2, off" ::"s"(base), "i"(at), "v"(src)
+               : "memory", "m0", "scc");
 }
+__device__ __forceinline__ void dma4_s(uint32_t base, int at, uint32_t off, const void *src) {
+  asm volatile(LORA_SET_M0 "global_load_lds_dword %2, %3" ::"s"(base), "i"(at), "v"(off), "s"(src)
+               : "memory", "m0", "scc");
+}
+#undef LORA_SET_M0
+
+// The same unless `skip` (a wave's scalar) is other than 0.  The branch is inside the
+// asm: one that the compiler saw would split the block of products around it.  The
+// comparison and the branch are the wait state.
+#define LORA_SET_M0_UNLESS \
+  "s_add_u32 m0, %0, %1\n\ts_cmp_lg_u32 %2, 0\n\ts_cbranch_scc1 .Ldma_skip_%=\n\t"
+__device__ __forceinline__ void dma16_s_unless(uint32_t skip, uint32_t base, int at, uint32_t off, const void *src) {
+  asm volatile(LORA_SET_M0_UNLESS "global_load_lds_dwordx4 %3, %4\n.Ldma_skip_%=:" ::"s"(base), "i"(at), "s"(skip),
+               "v"(off), "s"(src)
+               : "memory", "m0", "scc");
+}
+__device__ __forceinline__ void dma4_s_unless(uint32_t skip, uint32_t base, int at, uint32_t off, const void *src) {
+  asm volatile(LORA_SET_M0_UNLESS "global_load_lds_dword %3, %4\n.Ldma_skip_%=:" ::"s"(base), "i"(at), "s"(skip),
+               "v"(off), "s"(src)
+               : "memory", "m0", "scc");
+}
+#undef LORA_SET_M0_UNLESS
 
 // Wait until at most N of this wave's vector-memory operations are
 // outstanding, then LDS-fence and barrier the workgroup.

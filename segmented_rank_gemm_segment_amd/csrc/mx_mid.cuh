@@ -122,20 +122,20 @@ __global__ __launch_bounds__(512) void mx_mid_kernel(GemmArgs g) {
     const int k0 = k * KS;
 #pragma unroll
     for (int i = 0; i < XI; ++i) {
-      const uint32_t dst = __builtin_amdgcn_readfirstlane(st + (w4 * XI + i) * 1024);
+      const uint32_t dst = __builtin_amdgcn_readfirstlane(st + w4 * XI * 1024);
       const uint32_t off = xoff[i] - (k0 + xc[i] * XE >= K ? xc[i] * 16 : 0);
       if constexpr (GROUPED)
-        dma16(dst, xrow[i] + (int64_t)k * XR + off);
+        dma16(dst, i * 1024, xrow[i] + (int64_t)k * XR + off);
       else
-        dma16_s(dst, off, xb + (int64_t)k * XR);
+        dma16_s(dst, i * 1024, off, xb + (int64_t)k * XR);
     }
 #pragma unroll
     for (int i = 0; i < WI; ++i)
-      dma16_s(__builtin_amdgcn_readfirstlane(st + WOFF + (w4 * WI + i) * 1024),
+      dma16_s(__builtin_amdgcn_readfirstlane(st + w4 * WI * 1024), WOFF + i * 1024,
               woff[i] - (k0 + wc[i] * 32 >= K ? wc[i] * 16 : 0), wb + (int64_t)k * WR);
 #pragma unroll
     for (int i = 0; i < SI; ++i)
-      dma4(__builtin_amdgcn_readfirstlane(st + SOFF + si(i) * 256), sp[i] + min(k * WPR + sword, (blocks - 1) / 4) * 4);
+      dma4(__builtin_amdgcn_readfirstlane(st + si(i) * 256), SOFF, sp[i] + min(k * WPR + sword, (blocks - 1) / 4) * 4);
   };
   const int KT = (K + KS - 1) / KS;
   auto zero_tail = [&](int buf) {

@@ -126,19 +126,19 @@ __global__ __launch_bounds__(WM *WN *kWave) void mx_product_kernel(MxGemmArgs g)
     // before K) and is zeroed before use
     const uint32_t back =
         !WIDE && ktail && k_issue == KT - 1 && k_issue * 256 + chunk(i) * 32 >= g.K ? chunk(i) * 16 : 0;
-    dma16_s(__builtin_amdgcn_readfirstlane(sbase + b_issue * STAGE + (wid * CI + i) * 1024),
-            off[i] - back, base + (int64_t)k_issue * 128);
+    dma16_s(__builtin_amdgcn_readfirstlane(sbase + b_issue * STAGE + wid * CI * 1024), i * 1024, off[i] - back,
+            base + (int64_t)k_issue * 128);
   };
   auto issue_scales = [&]() __attribute__((always_inline)) {
-    const uint32_t dst = sbase + SOFF + s_issue * SSTAGE;
+    const uint32_t dst = sbase + s_issue * SSTAGE;
     if constexpr (WIDE) {
       // (a branch inside the asm: see the loop)
       dma16_s_unless(__builtin_amdgcn_readfirstlane(k_issue % SPER),
-                     __builtin_amdgcn_readfirstlane(dst + wid * 64 * 16), offs, bases + (int64_t)k_issue * 8);
+                     __builtin_amdgcn_readfirstlane(dst + wid * 64 * 16), SOFF, offs, bases + (int64_t)k_issue * 8);
     } else {
 #pragma unroll
       for (int w = 0; w < 2; ++w)
-        dma4_s(__builtin_amdgcn_readfirstlane(dst + w * R * 4 + wid * 64 * 4), offs,
+        dma4_s(__builtin_amdgcn_readfirstlane(dst + wid * 64 * 4), SOFF + w * R * 4, offs,
                bases + (int64_t)min(k_issue * 2 + w, last_word) * 4);
     }
   };

@@ -137,27 +137,27 @@ __global__ __launch_bounds__(512) void mx_weight_kernel(GemmArgs g) {
     // a chunk past K reads the stage's first chunk and is zeroed before use
     const int c = xchunk(i);
     const int back = TAIL && k_issue * 64 + c * 8 >= K ? c * 16 : 0;
-    const uint32_t dst = __builtin_amdgcn_readfirstlane(sbase + xb * XST + (wid * 4 + i) * 1024);
+    const uint32_t dst = __builtin_amdgcn_readfirstlane(sbase + xb * XST + wid * 4 * 1024);
     if constexpr (GROUPED)
-      dma16(dst, xrow[i] + (int64_t)k_issue * 128 - back);
+      dma16(dst, i * 1024, xrow[i] + (int64_t)k_issue * 128 - back);
     else
-      dma16_s(dst, xoff[i] - back, xbase + (int64_t)k_issue * 128);
+      dma16_s(dst, i * 1024, xoff[i] - back, xbase + (int64_t)k_issue * 128);
   };
   auto issue_w = [&](int i) __attribute__((always_inline)) {
     const int c = wchunk(i), p = k_issue / 4;
     const uint32_t back = TAIL && p * 256 + c * 32 >= K ? c * 16 : 0;
     dma16_s_unless(__builtin_amdgcn_readfirstlane(k_issue % 4),
-                   __builtin_amdgcn_readfirstlane(sbase + WOFF + wb * WST + (wid * 4 + i) * 1024),
+                   __builtin_amdgcn_readfirstlane(sbase + wb * WST + wid * 4 * 1024), WOFF + i * 1024,
                    woff[i] - back, wbase + (int64_t)p * 128);
   };
   auto issue_s = [&]() __attribute__((always_inline)) {
     const uint32_t dst =
-        __builtin_amdgcn_readfirstlane(sbase + SOFF + sb_i * SST + (wid & 3) * 64 * SROW);
+        __builtin_amdgcn_readfirstlane(sbase + sb_i * SST + (wid & 3) * 64 * SROW);
     const uint32_t skip = __builtin_amdgcn_readfirstlane(k_issue % SPER);
     if constexpr (WIDE)
-      dma16_s_unless(skip, dst, soff, sbase_g + (int64_t)(k_issue / 8) * 16);
+      dma16_s_unless(skip, dst, SOFF, soff, sbase_g + (int64_t)(k_issue / 8) * 16);
     else
-      dma4_s_unless(skip, dst, soff, sbase_g + (int64_t)(k_issue / 2) * 4);
+      dma4_s_unless(skip, dst, SOFF, soff, sbase_g + (int64_t)(k_issue / 2) * 4);
   };
   // past a stage's loads (its X, and with the first of their stages codes and scales)
   auto advance = [&]() __attribute__((always_inline)) {

@@ -177,16 +177,16 @@ __global__ __launch_bounds__(kSStages * kWave) void shrink_mfma_kernel(
       const uint32_t dst = __builtin_amdgcn_readfirstlane(sbase + stage * STAGE);
       if (k0 + BK <= d_in) {
 #pragma unroll
-        for (int i = 0; i < AI; ++i) dma16(dst + i * 1024, asrc[i] + k0);
+        for (int i = 0; i < AI; ++i) dma16(dst, i * 1024, asrc[i] + k0);
 #pragma unroll
-        for (int i = 0; i < BI; ++i) dma16(dst + SM * 128 + i * 1024, bsrc[i] + k0);
+        for (int i = 0; i < BI; ++i) dma16(dst, SM * 128 + i * 1024, bsrc[i] + k0);
       } else {
 #pragma unroll
         for (int i = 0; i < AI; ++i)
-          dma16(dst + i * 1024, asrc[i] + ((k0 + alc[i] * 8 < d_in) ? k0 : -alc[i] * 8));
+          dma16(dst, i * 1024, asrc[i] + ((k0 + alc[i] * 8 < d_in) ? k0 : -alc[i] * 8));
 #pragma unroll
         for (int i = 0; i < BI; ++i)
-          dma16(dst + SM * 128 + i * 1024, bsrc[i] + ((k0 + blc[i] * 8 < d_in) ? k0 : -blc[i] * 8));
+          dma16(dst, SM * 128 + i * 1024, bsrc[i] + ((k0 + blc[i] * 8 < d_in) ? k0 : -blc[i] * 8));
       }
     };
     f32x16 acc;
