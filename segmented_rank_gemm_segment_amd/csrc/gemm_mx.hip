@@ -6,17 +6,6 @@
 #include "mx_weight.cuh"
 
 namespace lora {
-namespace {
-
-template <int BM, int BN, int WM, int WN, int BK, int STAGES, int KG>
-hipError_t launch_codes(const GemmArgs &g, hipStream_t stream) {
-  hipLaunchKernelGGL((gemm_bf16_kernel<BM, BN, WM, WN, BK, STAGES, KG, 0, false, kMxXW>),
-                     dim3(tile_grid((g.M + BM - 1) / BM, (g.N + BN - 1) / BN)),
-                     dim3(WM * WN * KG * kWave), 0, stream, g);
-  return hipGetLastError();
-}
-
-}  // namespace
 
 hipError_t launch_gemm_mx(const void *X, int64_t ldx, const void *W, int64_t ldw,
                           const MxScales &mx, void *Y, int64_t ldy, int M, int K, int N,
@@ -29,7 +18,7 @@ hipError_t launch_gemm_mx(const void *X, int64_t ldx, const void *W, int64_t ldw
       // in units of four codes
       GemmArgs g = gemm_args(X, ldx / 2, W, ldw / 2, Y, ldy, M, K / 4, N, nullptr, nullptr, nullptr);
       g.mx = mx;
-      return launch_codes<LORA_GEMM_MID>(g, stream);
+      return launch_tile_plain<LORA_GEMM_MID, kMxXW>(g, stream);
     }
     GemmArgs g = gemm_args(X, ldx, W, ldw * 2, Y, ldy, M, K, N, nullptr, nullptr, nullptr);
     g.mx = mx;
@@ -45,8 +34,8 @@ hipError_t launch_gemm_mx(const void *X, int64_t ldx, const void *W, int64_t ldw
     case kMxTiles32:
     case kMxTiles64: return launch_mx_mid<false>(g, k, lora, stream);
     case kMxTiles128: return launch_tile<LORA_GEMM_MID, kMxW>(g, lora, stream);
-    case kMxTiles192: return launch_tile<LORA_GEMM_LARGE192, kMxW>(g, true, stream);
-    case kMxTiles256: return launch_tile<LORA_GEMM_LARGE, kMxW>(g, true, stream);
+    case kMxTiles192: return launch_tile_lora<LORA_GEMM_LARGE192, kMxW>(g, stream);
+    case kMxTiles256: return launch_tile_lora<LORA_GEMM_LARGE, kMxW>(g, stream);
     default: return launch_mx_weight<false>(g, stream);
   }
 }

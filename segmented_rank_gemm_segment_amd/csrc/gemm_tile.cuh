@@ -33,6 +33,7 @@
 #include "lds_dma.cuh"
 #include "lora_device.cuh"
 #include "lora_kernels.h"
+#include "mx_common.cuh"
 #include "tile_choice.h"
 
 namespace lora {
@@ -215,18 +216,6 @@ __device__ __forceinline__ mfma_bf16x8 fp4x8_to_bf16x8(uint32_t q, float sc) {
       __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, sc, 1)),
       __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, sc, 2)),
       __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, sc, 3))});
-}
-
-// 32 x 32 x 64 product of MXFP4 fragments: lane l holds row l % 32 of each
-// operand at codes [32 (l / 32), 32 (l / 32) + 32), one block, whose scale is
-// byte SEL of its scale word.
-template <int SEL>
-__device__ __forceinline__ f32x16 mfma_mx(u32x4 a, u32x4 b, f32x16 c, uint32_t sa, uint32_t sb) {
-  typedef int i32x8 __attribute__((ext_vector_type(8)));
-  const i32x8 av = {(int)a[0], (int)a[1], (int)a[2], (int)a[3], 0, 0, 0, 0};
-  const i32x8 bv = {(int)b[0], (int)b[1], (int)b[2], (int)b[3], 0, 0, 0, 0};
-  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(av, bv, c, 4, 4, SEL, (int)sa, SEL,
-                                                         (int)sb);
 }
 
 // LoRA term of one output row over 8 consecutive columns, added to o in fp32:
@@ -1526,27 +1515,35 @@ inline GemmArgs gemm_args(const void *X, int64_t ldx, const void *W, int64_t ldw
   return g;
 }
 
+// The tiles with the LoRA term, without it, and either.
 template <int BM, int BN, int WM, int WN, int BK, int STAGES, int KG, int WQ>
-hipError_t launch_tile(const GemmArgs &g, bool lora, hipStream_t stream) {
-  dim3 grid(tile_grid((g.M + BM - 1) / BM, (g.N + BN - 1) / BN));
-  dim3 block(WM * WN * KG * kWave);
-  const bool dora = lora && g.dora;
-  if (lora && g.Bn && dora)
+hipError_t launch_tile_lora(const GemmArgs &g, hipStream_t stream) {
+  const dim3 grid(tile_grid((g.M + BM - 1) / BM, (g.N + BN - 1) / BN)), block(WM * WN * KG * kWave);
+  if (g.Bn && g.dora)
     hipLaunchKernelGGL((gemm_bf16_kernel<BM, BN, WM, WN, BK, STAGES, KG, 2, true, WQ>), grid,
                        block, 0, stream, g);
-  else if (lora && g.Bn)
+  else if (g.Bn)
     hipLaunchKernelGGL((gemm_bf16_kernel<BM, BN, WM, WN, BK, STAGES, KG, 2, false, WQ>), grid,
                        block, 0, stream, g);
-  else if (lora && dora)
+  else if (g.dora)
     hipLaunchKernelGGL((gemm_bf16_kernel<BM, BN, WM, WN, BK, STAGES, KG, 1, true, WQ>), grid,
                        block, 0, stream, g);
-  else if (lora)
+  else
     hipLaunchKernelGGL((gemm_bf16_kernel<BM, BN, WM, WN, BK, STAGES, KG, 1, false, WQ>), grid,
                        block, 0, stream, g);
-  else
-    hipLaunchKernelGGL((gemm_bf16_kernel<BM, BN, WM, WN, BK, STAGES, KG, 0, false, WQ>), grid,
-                       block, 0, stream, g);
   return hipGetLastError();
+}
+template <int BM, int BN, int WM, int WN, int BK, int STAGES, int KG, int WQ>
+hipError_t launch_tile_plain(const GemmArgs &g, hipStream_t stream) {
+  const dim3 grid(tile_grid((g.M + BM - 1) / BM, (g.N + BN - 1) / BN)), block(WM * WN * KG * kWave);
+  hipLaunchKernelGGL((gemm_bf16_kernel<BM, BN, WM, WN, BK, STAGES, KG, 0, false, WQ>), grid, block,
+                     0, stream, g);
+  return hipGetLastError();
+}
+template <int BM, int BN, int WM, int WN, int BK, int STAGES, int KG, int WQ>
+hipError_t launch_tile(const GemmArgs &g, bool lora, hipStream_t stream) {
+  return lora ? launch_tile_lora<BM, BN, WM, WN, BK, STAGES, KG, WQ>(g, stream)
+              : launch_tile_plain<BM, BN, WM, WN, BK, STAGES, KG, WQ>(g, stream);
 }
 
 // Rows that go to the large tiles when the batch is split (0: no split).

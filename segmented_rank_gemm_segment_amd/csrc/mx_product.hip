@@ -26,9 +26,9 @@
 // 16943 x 4096 x 14336: 523 us, 3.8 PFLOP/s; 8192^3: 261 us, 4.2 PFLOP/s; 2048 x
 // 8192 x 8192: 70 us.  The clock falls as the matrix pipe gets busier (1.84 GHz at
 // 48%); the products alone take 283 us of the first, the stores 100.
-#include "lds_dma.cuh"
 #include "lora_device.cuh"
 #include "lora_kernels.h"
+#include "mx_common.cuh"
 #include "tile_choice.h"
 
 namespace lora {
@@ -41,29 +41,6 @@ struct MxGemmArgs {
   int64_t ldy;
   int M, K, N;
 };
-
-typedef int i32x8 __attribute__((ext_vector_type(8)));
-
-constexpr int kProductGroup = 8;   // M-tiles per group of the tile order
-
-// SEL: the scale words' byte of this product's block (lds_dma.cuh's fragment
-// layout: lane l holds row l % 32, codes [32 (l / 32), +32) of 64).
-template <int SEL>
-__device__ __forceinline__ f32x16 mfma_mx4(u32x4 a, u32x4 b, f32x16 c, uint32_t sa, uint32_t sb) {
-  const i32x8 av = {(int)a[0], (int)a[1], (int)a[2], (int)a[3], 0, 0, 0, 0};
-  const i32x8 bv = {(int)b[0], (int)b[1], (int)b[2], (int)b[3], 0, 0, 0, 0};
-  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(av, bv, c, 4, 4, SEL, (int)sa, SEL,
-                                                         (int)sb);
-}
-
-// Tile t of the order: groups of kProductGroup M-tiles, each sweeping N.
-__device__ __forceinline__ void tile_at(int t, int tiles_m, int tiles_n, int &mi, int &ni) {
-  const int grp = t / (kProductGroup * tiles_n), first = grp * kProductGroup;
-  const int cnt = min(kProductGroup, tiles_m - first);
-  const int in = t - grp * kProductGroup * tiles_n;
-  mi = first + in % cnt;
-  ni = in / cnt;
-}
 
 // WIDE: a load of the scales takes four words a row and serves two stages.
 template <int BM, int BN, int WM, int WN, bool WIDE>
@@ -263,9 +240,9 @@ __global__ __launch_bounds__(WM *WN *kWave) void mx_product_kernel(MxGemmArgs g)
       for (int q = 0; q < FN * FM; ++q) {
         f32x16 &c = acc[q / FM][q % FM];
         if (s & 1)
-          c = mfma_mx4<2>(a[1][q / FM], b[1][q % FM], c, sa[0][q / FM], sb[0][q % FM]);
+          c = mfma_mx<2>(a[1][q / FM], b[1][q % FM], c, sa[0][q / FM], sb[0][q % FM]);
         else
-          c = mfma_mx4<0>(a[0][q / FM], b[0][q % FM], c, sa[s / 2][q / FM], sb[s / 2][q % FM]);
+          c = mfma_mx<0>(a[0][q / FM], b[0][q % FM], c, sa[s / 2][q / FM], sb[s / 2][q % FM]);
         if (q < FN + FM) read1(q, st, s + 1);
         __builtin_amdgcn_sched_barrier(0);
       }
@@ -278,7 +255,7 @@ __global__ __launch_bounds__(WM *WN *kWave) void mx_product_kernel(MxGemmArgs g)
     issue_scales();
 #pragma unroll
     for (int q = 0; q < FN * FM; ++q) {
-      acc[q / FM][q % FM] = mfma_mx4<2>(a[1][q / FM], b[1][q % FM], acc[q / FM][q % FM], sa[1][q / FM], sb[1][q % FM]);
+      acc[q / FM][q % FM] = mfma_mx<2>(a[1][q / FM], b[1][q % FM], acc[q / FM][q % FM], sa[1][q / FM], sb[1][q % FM]);
       if (q < FN + FM) read1(q, nst, 0);
       issue_codes(q);
       __builtin_amdgcn_sched_barrier(0);

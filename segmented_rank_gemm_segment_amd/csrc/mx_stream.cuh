@@ -20,8 +20,8 @@
 //
 // 1 x 8192 -> 28672 (125 MB): 28.1 us, 4.5 TB/s (KP 1: 35.4, as W's rows, a power of
 // two apart, share few cache sets and the second half of a line was often fetched
-// again); 16 rows 45 us.  Non-temporal loads of W, which lose half lines: 41 us
-// with KP 1.  64 x 8 choices on 128 experts of 2048 -> 1536 (212 MB): 58 us.
+// again).  Non-temporal loads of W, which lose half lines: 41 us with KP 1.  64 x 8
+// choices on 128 experts of 2048 -> 1536 (212 MB): 58 us.
 #pragma once
 
 #include "gemm_tile.cuh"
@@ -165,15 +165,14 @@ hipError_t launch_stream(const GemmArgs &g, bool lora, hipStream_t stream) {
   return hipGetLastError();
 }
 
-template <int KP>
-hipError_t launch_stream_rows(const GemmArgs &g, int tiles, bool lora, hipStream_t stream) {
-  if (tiles == 4) return launch_stream<4, 8, KP>(g, lora, stream);
-  if (tiles == 2) return launch_stream<2, 8, KP>(g, lora, stream);
-  return launch_stream<1, 8, KP>(g, lora, stream);
-}
 inline hipError_t launch_mx_stream(const GemmArgs &g, MxKernel k, bool lora, hipStream_t stream) {
-  if (k == kMxStream8) return launch_stream_rows<2>(g, mx_stream8_tiles(g.N), lora, stream);
-  return launch_stream_rows<1>(g, g.N >= 64 * kCUs ? 4 : g.N >= 32 * kCUs ? 2 : 1, lora, stream);
+  // (kMxStream16: N below 64 kCUs / 2, where one tile of 16 a workgroup gives no more
+  // than two workgroups to a CU)
+  if (k == kMxStream16) return launch_stream<1, 8, 1>(g, lora, stream);
+  const int tiles = mx_stream8_tiles(g.N);
+  if (tiles == 4) return launch_stream<4, 8, 2>(g, lora, stream);
+  if (tiles == 2) return launch_stream<2, 8, 2>(g, lora, stream);
+  return launch_stream<1, 8, 2>(g, lora, stream);
 }
 
 template <int NT, int KP>

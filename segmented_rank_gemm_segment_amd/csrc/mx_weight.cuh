@@ -25,15 +25,6 @@
 namespace lora {
 namespace {
 
-// Tile t of an order in groups of 8 M-tiles, each sweeping N.
-__device__ __forceinline__ void tile_at(int t, int tiles_m, int tiles_n, int &mi, int &ni) {
-  const int grp = t / (kTileGroup * tiles_n), first = grp * kTileGroup;
-  const int cnt = min(kTileGroup, tiles_m - first);
-  const int in = t - grp * kTileGroup * tiles_n;
-  mi = first + in % cnt;
-  ni = in / cnt;
-}
-
 // WIDE: a load of the scales takes four words a row (K 512).  TAIL: K is no
 // multiple of 256.
 template <bool GROUPED, bool WIDE, bool TAIL>
