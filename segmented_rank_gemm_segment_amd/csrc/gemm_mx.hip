@@ -51,7 +51,7 @@ hipError_t launch_experts_gemm_mx(const void *X, int64_t ldx, const ExpertView &
     const int64_t t = (int64_t)ex.n_choices / bm + ex.n_experts;
     return (int)(t < ex.n_choices ? t : ex.n_choices);
   };
-  switch (mx_experts_kernel_of(ex.n_choices, ex.n_experts, K)) {
+  switch (mx_experts_kernel_of(ex.n_choices, ex.n_experts, K, N)) {
     case kMxStream8: return launch_experts_stream<4, 2>(g, tiles(8), stream);
     case kMxStream16: return launch_experts_stream<4, 1>(g, tiles(16), stream);
     case kMxTiles32: return launch_experts_mid(g, tiles(32), stream);

@@ -98,16 +98,28 @@ inline MxKernel mx_both_kernel_of(int M, int N) {
   return c.t256 <= c.t128 ? kMxPersistent : kMxTiles128;
 }
 
-// The experts' products, by the mean rows of an expert, in us.  2: 16 experts of
-// 4096 -> 4096 28 in tiles of 8 against 38 in tiles of 16.  Streamed against the
-// 32-row tiles: 3 rows 38 against 31, 8 rows 50 against 33, but where K is short, on
-// 64 experts of 2048 -> 1536, 4 rows 29 against 35, 8 rows 37 against 38, 16 rows 52
-// against 43.  Those against the 256-tiles: 64 rows 89 against 98 and 80 against 97,
-// 96 rows 116 against 100 and 105 against 99.
-inline MxKernel mx_experts_kernel_of(int n_choices, int n_experts, int K) {
+// The experts' products, by the mean rows of an expert (all choices over all
+// experts: which experts the batch names, and how often, is not known on the host).
+// `many`: more tiles of 32 x 64 than two rounds of two workgroups to a CU, which
+// those tiles need to follow each other without a gap, while the streamed kernels
+// have fewer bytes of X for each of W to fetch.  In us, streamed 8 rows / streamed 16 /
+// 32-row tiles, one size varied at a time:
+//   K, 128 experts, N 2048, 6 rows: 1024 61 / 46 / 66, 2560 104 / 94 / 109, 3584 138 /
+//     139 / 146, 4096 163 / 164 / 174; 4 rows 52 / 42 / 64 to 129 / 145 / 160; 8 rows
+//     71 / 50 / 69 to 196 / 180 / 178
+//   N, 32 experts, K 2048, 6 rows: 1024 16 / 15 / 13, 2048 28 / 25 / 24, 4096 50 / 44 /
+//     46, 8192 93 / 82 / 85; 8 rows 18 / 19 / 13 to 110 / 94 / 90
+//   experts, K and N 2048, 6 rows: 8 11 / 10 / 9, 48 39 / 35 / 42, 64 52 / 46 / 53, 128
+//     94 / 80 / 101; K and N 4096: 16 47 / 47 / 41, 64 167 / 173 / 169
+//   up to 3 rows streaming 8 is within 4% of the best on all of these, 10 rows and
+//   more in tiles on all but short K with many tiles (64 of K and N 2048 55 against 60)
+// The tiles against the 256-tiles, 64 experts of 2048 -> 1536 and 16 of 4096 -> 4096:
+// 64 rows 89 against 98 and 80 against 97, 96 rows 116 against 100 and 105 against 99.
+inline MxKernel mx_experts_kernel_of(int n_choices, int n_experts, int K, int N) {
   const int rows = n_choices / n_experts;
-  if (rows <= 2) return kMxStream8;
-  if (rows <= 8 && K <= 2048) return kMxStream16;
+  const bool many = (int64_t)n_experts * ((N + 63) / 64) > 4 * kCUs;
+  if (many && K <= 2560 && rows >= 4 && rows <= 8) return kMxStream16;
+  if (rows <= (many ? 6 : 4)) return kMxStream8;
   return rows < 80 ? kMxTiles32 : kMxPersistent;
 }
 

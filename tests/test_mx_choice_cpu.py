@@ -8,14 +8,13 @@ import subprocess
 import pytest
 
 import segmented_rank_gemm_segment_amd as srg
-import test_gpu_experts as experts
 import test_gpu_mxfp4_kernels as kernels
 
 WRAP = """
 #include "tile_choice.h"
 extern "C" int weight(int M, int N, int lora) { return lora::mx_weight_kernel_of(M, N, lora != 0); }
 extern "C" int both(int M, int N) { return lora::mx_both_kernel_of(M, N); }
-extern "C" int experts(int n, int E, int K) { return lora::mx_experts_kernel_of(n, E, K); }
+extern "C" int experts(int n, int E, int K, int N) { return lora::mx_experts_kernel_of(n, E, K, N); }
 extern "C" int tiles8(int N) { return lora::mx_stream8_tiles(N); }
 extern "C" int wide(int K, long ldw, long ldx) { return lora::mx_wide_scales(K, ldw, ldx); }
 """
@@ -66,18 +65,15 @@ def test_every_kernel_of_two_mxfp4_operands_has_a_shape(rules):
 
 
 def test_every_experts_kernel_has_a_shape(rules):
-    def key(n, E, d_in):
-        k = rules.experts(n, E, d_in)
+    def key(n, E, d_in, d_out):
+        k = rules.experts(n, E, d_in, d_out)
         if k == PERSISTENT:
             return k, bool(rules.wide(d_in, (d_in // 32 + 15) // 16 * 16, 0)), d_in % 256 != 0
         return (k,)
-    tested = {key(n * k, E, d_in) for n, k, E, d_in, _ in kernels.EXPERT_SHAPES}
-    reached = {key(n * k, E, d_in) for n in ROWS for k in (1, 8) for E in (1, 8, 64, 1000)
-               for d_in in (512, 2048, 4096, 768, 608)}
-    assert reached <= tested | {(STREAM8,)}, sorted(reached - tested)
-    shapes = [m.args[1] for m in experts.test_experts_product.pytestmark
-              if m.name == "parametrize" and "d_in" in m.args[0]]
-    assert STREAM8 in {rules.experts(n * k, E, d_in) for s in shapes for n, k, E, d_in, _, _ in s}
+    tested = {key(n * k, E, d_in, d_out) for n, k, E, d_in, d_out in kernels.EXPERT_SHAPES}
+    reached = {key(n * k, E, d_in, d_out) for n in ROWS for k in (1, 8) for E in (1, 8, 64, 1000)
+               for d_in in (512, 2048, 4096, 768, 608) for d_out in (136, 2048, 8200)}
+    assert reached <= tested and len(reached) == 6, sorted(reached - tested)
 
 
 def test_base_rows_share_a_k_order(rules):
