@@ -416,7 +416,8 @@ lora_status lora_mxfp4_dequantize(const void *Xq, int64_t ldq, const void *x_sca
  * Base product with an MXFP4 weight and bf16 activations, Y = X dq(Wq)^T:
  * Wq, w_scale an MXFP4 matrix of d_out rows of d_in values, X [n][d_in] and
  * Y [n][d_out] bf16.  Codes are widened with their scale to bf16 in registers
- * (exact), multiplied on MFMA and accumulated in fp32, with one rounding.
+ * (exact; scales of 2^126 and more can pass bf16's range: infinity), multiplied on
+ * MFMA and accumulated in fp32, with one rounding.
  * lora_linear_fused_mxfp4w adds each row's LoRA term as lora_linear_fused_fp8w
  * does: from the unquantized activations, in fp32, before the one rounding;
  * rows of base-only and rank-0 segments equal lora_base_gemm_mxfp4w's output
@@ -435,7 +436,8 @@ lora_status lora_linear_fused_mxfp4w(const void *X, int64_t ldx, const void *Wq,
  * Base product of two MXFP4 matrices, Y = dq(Xq) dq(Wq)^T (activations from
  * lora_mxfp4_quantize): the codes and scales go to the matrix cores as they
  * are, products accumulate in fp32, Y [n_rows][d_out] is bf16 and rounded once.
- * The low-rank term of the unquantized activations is added by lora_expand.
+ * The low-rank term of the unquantized activations is added by lora_expand, which
+ * reads this rounded Y, adds in fp32 and rounds a second time.
  */
 lora_status lora_base_gemm_mxfp4(const void *Xq, int64_t ldx, const void *x_scale, int64_t ldxs,
                                  const void *Wq, int64_t ldw, const void *w_scale, int64_t ldws,

@@ -262,3 +262,51 @@ def test_segments_on_the_host_are_refused():
     with pytest.raises(ValueError):
         srg.lora_linear_fused_mxfp4w(d["X"], Wq, ws, H, srg.Segments(n, 2, "cpu"), pool, Y)
     assert bool((Y == 7.0).all())
+
+
+@pytest.mark.parametrize("n,d_in,d_out,n_slots,r,runs", [
+    (9, 544, 264, 4, 16, False), (300, 544, 4168, 7, 64, True), (300, 1056, 4168, 40, 32, False),
+    (1024, 608, 4096, 9, 64, True), (2100, 512, 8200, 5, 64, True)])
+def test_two_mxfp4_operands_with_adapters(n, d_in, d_out, n_slots, r, runs):
+    """quantise, build and shrink, the product of the codes, expand: the term comes
+    from the unquantised activations and is added to the rounded product, so two
+    roundings to bf16, of the base and of the sum."""
+    say("both with adapters", n, d_in, d_out, n_slots, r, runs)
+    w = wl.make_random(660 + n, n, d_in, d_out, n_slots, r, p_base=0.15, dtype="bf16", runs=runs)
+    w.slot_rank[1] = 0
+    d = wl.device_tensors(w, DEV)
+    pool = srg.Pool(d["A"], d["Bt"], d["slot_rank"], w.slot_alpha)
+    seg = srg.Segments(n, n_slots, DEV)
+    H = torch.full((n, r), float("nan"), device=DEV)
+    X, slot = d["X"], torch.from_numpy(w.row_slot).to(DEV)
+    codes, scales = wl.make_mxfp4(661, d_out, d_in)
+    W = packed(codes, scales)
+    Xq = srg.mxfp4_empty(n, d_in)
+    Y = torch.full((n + 1, d_out + 8), 7.0, dtype=torch.bfloat16, device=DEV)
+    srg.lora_mxfp4_quantize(X, *Xq)
+    srg.lora_build_shrink(d["row_slot"], X, pool, seg, H)
+    srg.lora_base_gemm_mxfp4(*Xq, *W, Y[:n, :d_out])
+    base = Y.clone()
+    srg.lora_expand(H, seg, pool, Y[:n, :d_out])
+    assert bool((Y[n] == 7.0).all()) and bool((Y[:, d_out:] == 7.0).all())
+
+    Xd = values(*oracle.quantize_mxfp4(X.double().cpu().numpy()))
+    W64, X64 = values(codes, scales), X.double()
+    sums = Xd.abs() @ W64.abs().t()
+    Y64, acc = Xd @ W64.t(), d_in * U * sums
+    check(base[:n, :d_out], Y64, acc, "base")
+    acc += 2.0 ** -8 * Y64.abs()                         # the base's own rounding
+    plain = slot < 0
+    for a in range(n_slots):
+        k, rows = int(w.slot_rank[a]), (slot == a).nonzero().squeeze(1)
+        if k == 0:
+            plain |= slot == a
+            continue
+        s = float(w.slot_alpha[a]) / k
+        A, B = d["A"][a, :k].double(), d["Bt"][a, :k].double()
+        h, h_abs = X64[rows] @ A.t(), X64[rows].abs() @ A.abs().t()
+        Y64[rows] += s * (h @ B)
+        acc[rows] += s * ((h_abs * (d_in + k + 2) * U + h.abs() * 2.0 ** -16) @ B.abs())
+        acc[rows] += (2 * k + 2) * U * (sums[rows] + s * (h_abs @ B.abs()))
+    check(Y[:n, :d_out], Y64, acc, "sum")
+    assert torch.equal(Y[:n][plain], base[:n][plain])
