@@ -310,3 +310,75 @@ def test_two_mxfp4_operands_with_adapters(n, d_in, d_out, n_slots, r, runs):
         acc[rows] += (2 * k + 2) * U * (sums[rows] + s * (h_abs @ B.abs()))
     check(Y[:n, :d_out], Y64, acc, "sum")
     assert torch.equal(Y[:n][plain], base[:n][plain])
+
+
+def test_experts_layer_in_a_graph_against_float64():
+    """An expert layer (sort, two products, combine, the combine's gradients),
+    captured once and replayed on new inputs: each call's output against float64
+    from the stored inputs of that call."""
+    n, k, E, d, f = 72, 4, 9, 160, 96
+    c1, s1 = wl.make_mxfp4(31, E * 2 * f, d, 120, 124)
+    c2, s2 = wl.make_mxfp4(32, E * d, f, 120, 124)
+    W1, W2 = values(c1, s1).view(E, 2 * f, d), values(c2, s2).view(E, d, f)
+    (q1, w1), (q2, w2) = packed(c1, s1), packed(c2, s2)
+    q1, q2 = q1.view(E, 2 * f, d // 2), q2.view(E, d, f // 2)
+    w1 = w1.as_strided((E, 2 * f, d // 32), (2 * f * w1.stride(0), w1.stride(0), 1))
+    w2 = w2.as_strided((E, d, f // 32), (d * w2.stride(0), w2.stride(0), 1))
+    z = lambda *s, t=torch.bfloat16: torch.zeros(*s, dtype=t, device=DEV)   # noqa: E731
+    X, dY, h, a, y, out, dys = z(n, d), z(n, d), z(n * k, 2 * f), z(n * k, f), z(n * k, d), z(n, d), z(n * k, d)
+    ids, wt, dw = z(n, k, t=torch.int32), z(n, k, t=torch.float32), z(n, k, t=torch.float32)
+    ex = srg.Experts(n, k, E, DEV)
+
+    def step():
+        srg.lora_experts_sort(ids, ex)
+        srg.lora_experts_gemm_mxfp4w(X, ex, q1, w1, h)
+        a.copy_(torch.nn.functional.silu(h[:, :f].float()) * h[:, f:].float())
+        srg.lora_experts_gemm_mxfp4w(a, ex, q2, w2, y, gathered=False)
+        srg.lora_experts_combine(y, wt, ex, out)
+        srg.lora_experts_combine_backward(dY, y, wt, ex, dys, dw)
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for rep in range(4):
+        say("graph", rep)
+        host = np.random.default_rng(rep).integers(-1, E, size=(n, k)).astype(np.int32)
+        ids.copy_(torch.from_numpy(host))
+        g = torch.Generator(DEV).manual_seed(rep)
+        for t in (X, dY, wt):
+            t.copy_(torch.randn(t.shape, device=DEV, generator=g))
+        for t in (h, y, dys):
+            t.fill_(3.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        ref = oracle.expert_routing(host, E)
+        order, off = ref["sorted_choice"], ref["expert_offsets"]
+        kept = len(order)
+        assert np.array_equal(ex.choice_position.cpu().numpy(), ref["choice_position"])
+        tok = torch.from_numpy(order // k).long().to(DEV)
+        expert = torch.from_numpy(np.repeat(np.arange(E), np.diff(off))).to(DEV)
+        x64, a64, y64 = X[tok].double(), a[:kept].double(), y[:kept].double()
+
+        def product(v, W):
+            r = [torch.zeros((kept, W.shape[1]), dtype=torch.float64, device=DEV) for _ in range(2)]
+            for e in range(E):
+                m = expert == e
+                r[0][m], r[1][m] = v[m] @ W[e].t(), v.shape[1] * U * (v[m].abs() @ W[e].abs().t())
+            return r
+        check(h[:kept], *product(x64, W1), "h")
+        check(y[:kept], *product(a64, W2), "y")
+        wc = wt.double().reshape(-1)[torch.from_numpy(order).long().to(DEV)]
+        o64, o_abs = (torch.zeros((n, d), dtype=torch.float64, device=DEV).index_add_(0, tok, t)
+                      for t in (wc[:, None] * y64, (wc[:, None] * y64).abs()))
+        check(out, o64, (k + 1) * U * o_abs, "out")
+        dy64 = dY[tok].double()
+        check(dys[:kept], wc[:, None] * dy64, U * (wc[:, None] * dy64).abs(), "dys")
+        flat = torch.zeros(n * k, dtype=torch.float64, device=DEV)
+        bound = flat.clone()
+        at = torch.from_numpy(order).long().to(DEV)
+        flat[at], bound[at] = (dy64 * y64).sum(1), (d + 2) * U * (dy64 * y64).abs().sum(1)
+        assert bool(((dw.double().reshape(-1) - flat).abs() <= bound).all())
+        for t in (h, y, dys):
+            assert bool((t[kept:] == 3.0).all())
