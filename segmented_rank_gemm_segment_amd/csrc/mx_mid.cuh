@@ -3,9 +3,10 @@
 // hundred rows, or of 32 x 64 where those leave CUs idle and for the experts, under
 // bf16 X (with the LoRA term) or MXFP4 X.
 //
-// A tile has little arithmetic for its bytes: at 256 x 4096 x 4096 the
-// workgroups take 164 MB out of L2 for 8.6 GFLOP, so the kernel is bound by loads
-// and their latency.  K advances in stages of 512 bytes of X row (256 values) or
+// A tile has little arithmetic for its bytes: at 256 x 4096 x 4096 each of the 256
+// workgroups asks L2 for 0.67 MB (64 rows of X and of W) for 34 MFLOP, the matrix pipe
+// is busy in under a quarter of the time, and the kernel is bound by loads and their
+// latency.  K advances in stages of 512 bytes of X row (256 values) or
 // 256 (512 codes): every load instruction covers whole 128-byte lines, and three
 // stages fill the LDS (half of it with 32 rows: two workgroups share a CU).  Four
 // K groups of two waves take a quarter of a stage each (a wave all of its rows and
@@ -15,10 +16,14 @@
 // LDS, where each thread then finishes 8 columns of one row with its LoRA term, in
 // fp32, and one rounding.
 //
-// 256 x 4096 x 4096: 12.9 us (16.6 on the tiles of the bf16 product), with a
-// rank-16 adapter a row 18.9 (22.8): 30 MB of B rows from memory; loading them
-// ahead of the last stages, or of all, measured no faster.  Both operands MXFP4:
-// 7.7 us; 333 x 8192 x 1024 8.7 us (10.3 on 96 tiles of 64 rows).
+// 256 x 4096 x 4096: 12.7 us on weights that stay in the caches behind L2, 15.1 to
+// 16.2 from memory (16.6 on the tiles of the bf16 product, 12.9 here, when both were
+// timed alike); with a rank-16 adapter a row 18.0 to 18.6 (22.8 against 18.9): 30 MB of
+// B rows, 11 MB of them past L2; loading them ahead of the last stages, or of all,
+// measured no faster.  Both operands MXFP4: 7.7 us; 333 x 8192 x 1024 8.5 us, from
+// memory 9.8 to 10.0.  One row's B rows are read again by every row that shares its
+// adapter: 400 x 4096 x 14336 takes 109 us with 128 adapters of rank 16 and 122 with 8
+// of up to rank 64 that hold runs of rows.
 #pragma once
 
 #include "gemm_tile.cuh"

@@ -18,10 +18,10 @@
 // The next loads are issued before a load's products; registers for two
 // workgroups of eight waves on a CU.
 //
-// 1 x 8192 -> 28672 (125 MB): 28.1 us, 4.5 TB/s (KP 1: 35.4, as W's rows, a power of
+// 1 x 8192 -> 28672 (125 MB): 28.4 us, 4.4 TB/s (KP 1: 35.4, as W's rows, a power of
 // two apart, share few cache sets and the second half of a line was often fetched
 // again).  Non-temporal loads of W, which lose half lines: 41 us with KP 1.  64 x 8
-// choices on 128 experts of 2048 -> 1536 (212 MB): 58 us.
+// choices on 128 experts of 2048 -> 1536 (212 MB): 56 to 58 us.
 #pragma once
 
 #include "gemm_tile.cuh"

@@ -13,11 +13,13 @@
 // products, persistent workgroups and stores from registers as in the product of
 // two MXFP4 operands.
 //
-// 16943 x 4096 x 14336: 1611 us, 1.24 PFLOP/s; 8192^3: 850 us, 1.29 PFLOP/s (a
-// library's bf16 product reaches 1.36 and 1.17 on the same shapes).  8190 x 8
-// choices on 64 experts of 2048 -> 1536: 405 us, 1.0 PFLOP/s.  Loads issued a
-// quarter of a stage later: 1664 us; three stages of X, loaded by the workgroup's
-// halves in turn: 1644 us.
+// 16943 x 4096 x 14336: 1.64 to 1.82 ms over the passes of a trace (the clock falls from
+// one to the next, to 1.7 GHz; the matrix pipe is busy in 64% of the clocks), 1.1 to 1.2
+// PFLOP/s, and 1.45 ms for 16384 rows in a graph, 1.33 PFLOP/s; 8192^3: 0.83 to 0.94 ms
+// (a library's bf16 product reaches 1.36 and 1.17 PFLOP/s on these shapes).  8190 x 8
+// choices on 64 experts of 2048 -> 1536: 394 to 413 us, 1.0 PFLOP/s.  On the first,
+// when it took 1611 us, loads issued a quarter of a stage later took 1664, and three
+// stages of X, loaded by the workgroup's halves in turn, 1644.
 #pragma once
 
 #include "gemm_tile.cuh"
