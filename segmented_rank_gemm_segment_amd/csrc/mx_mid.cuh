@@ -292,13 +292,6 @@ hipError_t launch_mx_mid(const GemmArgs &g, MxKernel k, bool lora, hipStream_t s
                          : launch_mx_mid_rows<64, XMX>(g, lora, stream);
 }
 
-// Workgroups for an experts' product of up to tiles_m M-tiles: they find the
-// number there are themselves, and either tile order of it has to fit.
-inline int expert_grid(int tiles_m, int tiles_n) {
-  const int split = tiles_m < kHeavyMaxTilesM ? tiles_m : kHeavyMaxTilesM;
-  const int a = (tiles_m * tiles_n + 7) / 8 * 8, b = 8 * ((tiles_n + 7) / 8) * split;
-  return a > b ? a : b;
-}
 inline hipError_t launch_experts_mid(const GemmArgs &g, int tiles_m, hipStream_t stream) {
   hipLaunchKernelGGL((mx_mid_kernel<32, false, false, false, true>),
                      dim3(expert_grid(tiles_m, (g.N + 63) / 64)), dim3(512), 0, stream, g);

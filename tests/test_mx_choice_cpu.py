@@ -83,3 +83,53 @@ def test_base_rows_share_a_k_order(rules):
     for n in range(1, 3000, 7):
         for d_out in DIMS:
             assert order[rules.weight(n, d_out, 0)] == order[rules.weight(n, d_out, 1)], (n, d_out)
+
+
+ORDER = """
+#include "tile_order.h"
+using namespace lora;
+static int walk(int grid, int tm, int tn, int heavy, int *count) {
+  for (int b = 0; b < grid; ++b) {
+    int m = -1, n = -1;
+    if (!tile_order(b, tm, tn, heavy, m, n)) continue;
+    if (m < 0 || m >= tm || n < 0 || n >= tn) return -1;
+    ++count[m * tn + n];
+  }
+  return 0;
+}
+extern "C" int dense(int tm, int tn, int heavy, int *count) { return walk(tile_grid(tm, tn), tm, tn, heavy, count); }
+extern "C" int layer(int tm, int tn, int rows, int *count) {
+  const int g = tile_grid(tm, tn);
+  return walk(g > rows ? g : rows, tm, tn, -1, count);
+}
+extern "C" int experts(int bound, int tm, int tn, int *count) { return walk(expert_grid(bound, tn), tm, tn, -1, count); }
+"""
+
+
+@pytest.fixture(scope="module")
+def order(tmp_path_factory):
+    d = tmp_path_factory.mktemp("order")
+    (d / "wrap.cpp").write_text(ORDER)
+    csrc = os.path.join(os.path.dirname(os.path.abspath(srg.__file__)), "csrc")
+    subprocess.run(["g++", "-std=c++17", "-O1", "-Wall", "-Werror", "-shared", "-fPIC", "-I" + csrc,
+                    str(d / "wrap.cpp"), "-o", str(d / "order.so")], check=True)
+    return ctypes.CDLL(str(d / "order.so"))
+
+
+def once(f, tm, tn, *args):
+    count = (ctypes.c_int * (tm * tn))()
+    assert f(*args, count) == 0
+    assert all(c == 1 for c in count), (tm, tn, args, max(count), min(count))
+
+
+@pytest.mark.parametrize("tn", [1, 4, 7, 8, 9, 24, 32, 129])
+def test_every_tile_is_taken_once(order, tn):
+    """By the grid of a dense batch; by that of the one-launch layer, which has a
+    workgroup a row; and by the experts', which is sized by a bound on the M-tiles."""
+    for tm in (1, 2, 8, 31, 32, 33, 45, 130):
+        for heavy in (-1, 0, tm - 1):
+            once(order.dense, tm, tn, tm, tn, heavy)
+        if tm <= 8:
+            once(order.layer, tm, tn, tm, tn, 64 * tm)
+        for bound in (tm, tm + 1, tm + 20, 4 * tm + 100):
+            once(order.experts, tm, tn, bound, tm, tn)
