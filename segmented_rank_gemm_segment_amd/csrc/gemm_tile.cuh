@@ -493,7 +493,7 @@ __global__ __launch_bounds__(WM *WN *KG *kWave) void gemm_bf16_kernel(GemmArgs g
       heavy = heavier_end_tile(g.row_segment, M, BM, tiles_m, reinterpret_cast<int *>(smem));
   }
   int m_idx = 0, n_idx = 0;
-  const bool has_tile = tile_order(blockIdx.x, tiles_m, tiles_n, heavy, m_idx, n_idx);
+  const bool has_tile = tile_order<LAYER>(blockIdx.x, tiles_m, tiles_n, heavy, m_idx, n_idx);
   // (a layer workgroup without a tile still has its row of the layer to do)
   if (!LAYER && !has_tile) return;
   if (LAYER && !has_tile) m_idx = n_idx = 0;

@@ -57,7 +57,7 @@ __global__ __launch_bounds__(512) void mx_mid_kernel(GemmArgs g) {
     et = expert_tiles<BM, 512>(g.ex, reinterpret_cast<int *>(smem));
     tiles_m = et.total;
   }
-  if (!tile_order(blockIdx.x, tiles_m, (N + BN - 1) / BN, -1, mi, ni)) return;
+  if (!tile_order<GROUPED>(blockIdx.x, tiles_m, (N + BN - 1) / BN, -1, mi, ni)) return;
   int m0 = mi * BM;
   const int n0 = ni * BN;
   // the experts' product: rows [m0, M) are the tile's expert's, W its weight

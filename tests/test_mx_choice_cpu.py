@@ -88,21 +88,22 @@ def test_base_rows_share_a_k_order(rules):
 ORDER = """
 #include "tile_order.h"
 using namespace lora;
+template <bool SPARE>
 static int walk(int grid, int tm, int tn, int heavy, int *count) {
   for (int b = 0; b < grid; ++b) {
     int m = -1, n = -1;
-    if (!tile_order(b, tm, tn, heavy, m, n)) continue;
+    if (!tile_order<SPARE>(b, tm, tn, heavy, m, n)) continue;
     if (m < 0 || m >= tm || n < 0 || n >= tn) return -1;
     ++count[m * tn + n];
   }
   return 0;
 }
-extern "C" int dense(int tm, int tn, int heavy, int *count) { return walk(tile_grid(tm, tn), tm, tn, heavy, count); }
+extern "C" int dense(int tm, int tn, int heavy, int *count) { return walk<false>(tile_grid(tm, tn), tm, tn, heavy, count); }
 extern "C" int layer(int tm, int tn, int rows, int *count) {
   const int g = tile_grid(tm, tn);
-  return walk(g > rows ? g : rows, tm, tn, -1, count);
+  return walk<true>(g > rows ? g : rows, tm, tn, -1, count);
 }
-extern "C" int experts(int bound, int tm, int tn, int *count) { return walk(expert_grid(bound, tn), tm, tn, -1, count); }
+extern "C" int experts(int bound, int tm, int tn, int *count) { return walk<true>(expert_grid(bound, tn), tm, tn, -1, count); }
 """
 
 
