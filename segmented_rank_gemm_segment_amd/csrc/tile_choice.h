@@ -99,28 +99,43 @@ inline MxKernel mx_both_kernel_of(int M, int N) {
 }
 
 // The experts' products, by the mean rows of an expert (all choices over all
-// experts: which experts the batch names, and how often, is not known on the host).
-// `many`: more tiles of 32 x 64 than two rounds of two workgroups to a CU, which
-// those tiles need to follow each other without a gap, while the streamed kernels
-// have fewer bytes of X for each of W to fetch.  In us, streamed 8 rows / streamed 16 /
-// 32-row tiles, one size varied at a time:
-//   K, 128 experts, N 2048, 6 rows: 1024 61 / 46 / 66, 2560 104 / 94 / 109, 3584 138 /
-//     139 / 146, 4096 163 / 164 / 174; 4 rows 52 / 42 / 64 to 129 / 145 / 160; 8 rows
-//     71 / 50 / 69 to 196 / 180 / 178
-//   N, 32 experts, K 2048, 6 rows: 1024 16 / 15 / 13, 2048 28 / 25 / 24, 4096 50 / 44 /
-//     46, 8192 93 / 82 / 85; 8 rows 18 / 19 / 13 to 110 / 94 / 90
-//   experts, K and N 2048, 6 rows: 8 11 / 10 / 9, 48 39 / 35 / 42, 64 52 / 46 / 53, 128
-//     94 / 80 / 101; K and N 4096: 16 47 / 47 / 41, 64 167 / 173 / 169
-//   up to 3 rows streaming 8 is within 4% of the best on all of these, 10 rows and
-//   more in tiles on all but short K with many tiles (64 of K and N 2048 55 against 60)
-// The tiles against the 256-tiles, 64 experts of 2048 -> 1536 and 16 of 4096 -> 4096:
-// 64 rows 89 against 98 and 80 against 97, 96 rows 116 against 100 and 105 against 99.
+// experts: which experts the batch names, and how often, is not known on the host, so
+// each border is that of loads between even ones and a router's with experts twice as
+// likely as others).  In us, streamed 8 rows / streamed 16 / 32-row tiles, experts
+// equally likely and exp(normal / 2):
+//   3 rows: 128 experts, N 2048, K 2048 71 / 74 / 82 and 60 / 58 / 60, K 4096 119 / 151 /
+//     142 and 103 / 114 / 103; 64 of 4096 -> 4096 121 / 154 / 149 and 114 / 136 / 127
+//   4 rows: 128 experts, N 2048, K 1536 64 / 59 / 73 and 60 / 52 / 60, K 2048 80 / 80 / 88
+//     and 76 / 72 / 74, K 2560 90 / 96 / 99 and 82 / 79 / 80, K 4096 136 / 164 / 153 and
+//     129 / 146 / 129
+//   6 rows, the same: K 1024 58 / 48 / 60 and 61 / 46 / 53, K 1536 71 / 63 / 74 and 75 / 59 /
+//     64, K 2048 89 / 85 / 90 and 95 / 81 / 80, K 2560 102 / 103 / 104 and 104 / 94 / 89;
+//     32 experts: K 1024 17 / 14 / 17 and 17 / 14 / 16, K 2560 31 / 29 / 28 and 32 / 29 / 28,
+//     K 2048, N 8192 89 / 84 / 91 and 94 / 82 / 86
+//   8 rows: K 1536 87 / 66 / 74 and 87 / 63 / 66, K 2048 111 / 89 / 92 and 112 / 88 / 81, K
+//     4096 195 / 185 / 156 and 197 / 181 / 144
+// The more uneven the load the more the tiles gain (128 of 4096 -> 2048, 6 rows,
+// exp(2 normal): 130 / 101 / 62), as a streamed expert's weight is read once per 8 or
+// 16 of its rows.
+//
+// The 32-row tiles against the persistent kernel's of 256 x 256: each expert has half a
+// tile more than its rows fill, a small one takes 1.6 us and 1.8 per 1024 of K, a CU's
+// large one 2 us and 26, and up to two rounds of those count whole, as do a few tiles
+// past one (32 experts of 2048 -> 2048, 256 large tiles or a few more: 96 rows 72
+// against 58 evenly, 74 against 98 not).  Small / large, evenly and exp(normal / 2):
+// 128 of 2048 -> 2048: 64 rows 203 / 218 and 203 / 236, 96 rows 269 / 227 and 271 / 254;
+// of 4096 -> 2048: 80 rows 408 / 428 and 419 / 479, 128 rows 594 / 449 and 594 / 527;
+// of 1024 -> 2048: 48 rows 111 / 109 and 112 / 116, 80 rows 158 / 116 and 161 / 136;
+// 8 of 2048 -> 2048: 160 rows 30 / 48 and 30 / 49.
 inline MxKernel mx_experts_kernel_of(int n_choices, int n_experts, int K, int N) {
   const int rows = n_choices / n_experts;
-  const bool many = (int64_t)n_experts * ((N + 63) / 64) > 4 * kCUs;
-  if (many && K <= 2560 && rows >= 4 && rows <= 8) return kMxStream16;
-  if (rows <= (many ? 6 : 4)) return kMxStream8;
-  return rows < 80 ? kMxTiles32 : kMxPersistent;
+  if (rows <= 3) return kMxStream8;
+  if (rows <= (K <= 1536 ? 8 : K <= 2048 ? 5 : 3)) return kMxStream16;
+  const double m = (double)n_choices / n_experts, E = n_experts;
+  const double small = E * (m / 32 + 0.5) * ((N + 63) / 64) / kCUs * (1.6 + K * 1.76e-3);
+  const double rounds = E * (m < 128 ? 1 : m / 256 + 0.5) * ((N + 255) / 256) / kCUs;
+  const double large = (rounds <= 2 ? std::ceil(1.05 * rounds) : 1.05 * rounds + 0.3) * (2 + K * 0.0254);
+  return small <= large ? kMxTiles32 : kMxPersistent;
 }
 
 // Whether the persistent kernels load the scales four words (16 blocks) a row at a

@@ -219,8 +219,8 @@ def test_nan_stays_in_its_row_and_column(n, d_out):
 
 # n, top_k, E, d_in, d_out: the persistent kernel's ways of loading scales, and more
 # experts than a workgroup has threads
-EXPERT_SHAPES = [(3000, 2, 5, 768, 264), (2000, 2, 3, 512, 520), (1500, 4, 9, 608, 136),
-                 (12000, 4, 590, 256, 72), (30, 4, 8, 2080, 264), (30, 4, 30, 4640, 136), (40, 1, 7, 1056, 520),
+EXPERT_SHAPES = [(4800, 2, 64, 768, 1032), (5000, 2, 64, 512, 1032), (2600, 4, 64, 608, 1032),
+                 (12000, 4, 590, 256, 72), (3000, 2, 5, 768, 264), (1500, 4, 9, 608, 136), (30, 4, 8, 2080, 264), (30, 4, 30, 4640, 136), (40, 1, 7, 1056, 520),
                  (150, 4, 100, 544, 776), (500, 4, 1000, 96, 136), (20, 2, 6, 4640, 264)]
 
 
