@@ -17,12 +17,12 @@
 // fp32, and one rounding.
 //
 // 256 x 4096 x 4096: 12.7 us on weights that stay in the caches behind L2, 15.1 to
-// 16.2 from memory (16.6 on the tiles of the bf16 product, 12.9 here, when both were
+// 17.6 from memory (16.6 on the tiles of the bf16 product, 12.9 here, when both were
 // timed alike); with a rank-16 adapter a row 18.0 to 18.6 (22.8 against 18.9): 30 MB of
 // B rows, 11 MB of them past L2; loading them ahead of the last stages, or of all,
 // measured no faster.  Both operands MXFP4: 7.7 us; 333 x 8192 x 1024 8.5 us, from
 // memory 9.8 to 10.0.  One row's B rows are read again by every row that shares its
-// adapter: 400 x 4096 x 14336 takes 109 us with 128 adapters of rank 16 and 122 with 8
+// adapter: 400 x 4096 x 14336 takes 107 us with 128 adapters of rank 16 and 120 with 8
 // of up to rank 64 that hold runs of rows.
 #pragma once
 

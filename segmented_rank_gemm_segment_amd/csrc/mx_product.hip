@@ -23,10 +23,10 @@
 // W is the MFMA's row operand and X its column operand, so a lane ends up with
 // one row of Y and runs of columns; two lanes swap halves (v_permlane32_swap)
 // and each stores 16 bytes, without LDS, which the ring keeps.
-// 16943 x 4096 x 14336: 512 to 530 us, 3.8 PFLOP/s; 8192^3: 264 to 270 us, 4.1 PFLOP/s;
-// 2048 x 8192 x 8192: 70 us.  Of the first's clocks (1.76 GHz under this load) the matrix
+// 16943 x 4096 x 14336: 490 to 530 us, 3.8 to 4.1 PFLOP/s; 8192^3: 264 to 270 us, 4.1 PFLOP/s;
+// 2048 x 8192 x 8192: 70 us.  Of the first's clocks (1.75 to 1.87 GHz under this load) the matrix
 // pipe is busy in 52%, LDS with the fragments' reads in 29%, a sixth of it bank
-// conflicts; 916 MB come from past L2, 1.7 TB/s.  With loads and stores left out the
+// conflicts; 0.91 GB comes from past L2, 1.8 TB/s.  With loads and stores left out the
 // products take 283 us, the stores alone 100: no one of these fills the time, and the
 // counters do not show what the rest waits for.
 #include "lora_device.cuh"

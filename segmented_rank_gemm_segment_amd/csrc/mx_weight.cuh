@@ -17,7 +17,7 @@
 // one to the next, to 1.7 GHz; the matrix pipe is busy in 64% of the clocks), 1.1 to 1.2
 // PFLOP/s, and 1.45 ms for 16384 rows in a graph, 1.33 PFLOP/s; 8192^3: 0.83 to 0.94 ms
 // (a library's bf16 product reaches 1.36 and 1.17 PFLOP/s on these shapes).  8190 x 8
-// choices on 64 experts of 2048 -> 1536: 394 to 413 us, 1.0 PFLOP/s.  On the first,
+// choices on 64 experts of 2048 -> 1536: 389 to 413 us, 1.0 PFLOP/s.  On the first,
 // when it took 1611 us, loads issued a quarter of a stage later took 1664, and three
 // stages of X, loaded by the workgroup's halves in turn, 1644.
 #pragma once
