@@ -1,0 +1,664 @@
+"""Cases for training with the multi-LoRA layer: gradients and their optimizer.
+
+Three operators, each in its plain form (elementary torch operations in 32
+bits, rounded once at the end) and, with ``own`` true, through the calls of
+``segmented_rank_gemm_segment_amd``:
+
+* ``adapters``  the gradients of Y = X W^T + s_a (X A_a^T) B_a^T for a batch whose
+                rows use many adapters: of the adapters and, over the frozen
+                base weight, of X
+* ``experts``   the experts' products on bf16 weights, Y[p] = X[row of p] W_e^T
+                over every expert's rows, or the gradients of both operands
+* ``adamw``     an AdamW step over many tensors at once, moments in 32 bits, or
+                in 8 bits with a scale per block of 256; tensors that the batch
+                did not train are left alone
+
+The 8-bit moments: a block of 256 consecutive elements of a tensor has the scale
+s = max |x|.  First moment: codes c in -127..127, value s (c / 127) |c / 127|.
+Second moment: codes 0..255, value s (c / 255)^4.  A value between two codes
+takes the upper one with the probability that makes its expectation the value
+itself; the uniform numbers are a hash of (seed, step, tensor, element).  A
+second moment above 0 takes code 1 at least.
+"""
+import math
+
+import torch
+
+own = False
+
+DEV = "cuda"
+DTYPES = {"bf16": torch.bfloat16, "f32": torch.float32}
+BLOCK = 256
+LR, BETA1, BETA2, EPS, DECAY, SEED = 3e-4, 0.9, 0.999, 1e-8, 0.01, 1234
+ALPHA = 16.0
+
+
+# ---------------------------------------------------------------------------
+# cases
+# ---------------------------------------------------------------------------
+def listed():
+    return [
+        # a step over many tenants' short examples: two rows an adapter, latency counts
+        dict(name="adapters_tenants", op="adapters", n=256, d_in=4096, d_out=4096, slots=128,
+             r_max=16, dtype="bf16", dx=True, acc=False),
+        # long examples of eight tenants through an up projection, odd number of rows
+        dict(name="adapters_long", op="adapters", n=16943, d_in=4096, d_out=14336, slots=8,
+             r_max=64, dtype="bf16", dx=True, acc=False),
+        # a first layer, whose input takes no gradient: a narrow projection's adapters alone,
+        # added to the gradients of an earlier part of the batch
+        dict(name="adapters_first", op="adapters", n=2303, d_in=8192, d_out=1024, slots=37,
+             r_max=32, dtype="bf16", dx=False, acc=True),
+        # fp32 adapters, odd sizes
+        dict(name="adapters_f32", op="adapters", n=517, d_in=4104, d_out=1032, slots=7, r_max=8,
+             dtype="f32", dx=False, acc=False),
+        # a decode batch: few rows on every expert's weight
+        dict(name="experts_decode", op="experts", n=64, top_k=8, experts=128, d_in=2048,
+             d_out=1536, drop=0.0, back=False, gathered=True, dw="bf16", acc=False),
+        # a prefill or a training step's forward: long, uneven segments
+        dict(name="experts_forward", op="experts", n=8190, top_k=8, experts=64, d_in=2048,
+             d_out=1536, drop=0.0, back=False, gathered=True, dw="bf16", acc=False),
+        # its backward: gradients of the rows and of every expert's weight
+        dict(name="experts_backward", op="experts", n=8190, top_k=8, experts=64, d_in=2048,
+             d_out=1536, drop=0.0, back=True, gathered=True, dw="bf16", acc=False),
+        # rows in sorted order already, padded tokens, odd widths, fp32 weight gradients added to
+        # those of an earlier part of the batch
+        dict(name="experts_ragged", op="experts", n=333, top_k=2, experts=8, d_in=1032, d_out=520,
+             drop=0.1, back=True, gathered=False, dw="f32", acc=True),
+        # a few small tensors of odd sizes: latency counts
+        dict(name="adamw_small", op="adamw", tensors=9, numel=4099, ragged=True, p="f32", g="f32",
+             master=False, bits=32, live=1.0),
+        # every slot's A and B of a pool, fp32 gradients; half of the tenants had rows
+        dict(name="adamw_pool", op="adamw", tensors=256, numel=65536, ragged=False, p="bf16",
+             g="f32", master=True, bits=32, live=0.5),
+        # the experts' weights, bf16 gradients, with an fp32 copy of the weights
+        dict(name="adamw_experts", op="adamw", tensors=64, numel=1536 * 2048, ragged=False,
+             p="bf16", g="bf16", master=True, bits=32, live=1.0),
+        # an MLP's weights of uneven sizes with moments of 8 bits
+        dict(name="adamw_8bit", op="adamw", tensors=5, numel=14336 * 4096, ragged=True, p="bf16",
+             g="bf16", master=False, bits=8, live=1.0),
+    ]
+
+
+def _log(rng, lo, hi):
+    """A whole number in [lo, hi], spread over the logarithm."""
+    return min(hi, max(lo, int(round(lo * (hi / lo) ** rng.random()))))
+
+
+def _steps(rng, lo, hi, step):
+    """A multiple of step in [lo, hi], spread over the logarithm."""
+    return min(hi // step, max(lo // step, _log(rng, lo, hi) // step)) * step
+
+
+def draw(rng):
+    op = rng.choice(["adapters", "experts", "adamw"])
+    if op == "adapters":
+        while True:
+            dtype = rng.choice(["bf16", "bf16", "f32"])
+            c = dict(op=op, n=_log(rng, 1, 16943), d_in=_steps(rng, 256, 8192, 8),
+                     d_out=_steps(rng, 256, 14336, 8), slots=_log(rng, 1, 128),
+                     r_max=rng.choice([8, 16, 32, 64]), dtype=dtype,
+                     dx=dtype == "bf16" and rng.random() < 0.5, acc=rng.random() < 0.3)
+            if c["n"] * c["d_in"] * c["d_out"] <= 16943 * 4096 * 14336 and \
+                    c["n"] * c["slots"] * c["r_max"] * (c["d_in"] + c["d_out"]) <= \
+                    16943 * 512 * 18432:
+                return c
+    if op == "experts":
+        while True:
+            experts = _log(rng, 2, 256)
+            c = dict(op=op, n=_log(rng, 1, 8190), top_k=rng.randint(1, min(8, experts)),
+                     experts=experts, d_in=_steps(rng, 256, 4096, 8),
+                     d_out=_steps(rng, 256, 4096, 8), drop=rng.choice([0.0, 0.05, 0.3]),
+                     back=rng.random() < 0.6, gathered=rng.random() < 0.6,
+                     dw=rng.choice(["bf16", "f32"]), acc=rng.random() < 0.3)
+            if experts * c["d_in"] * c["d_out"] <= 128 * 2048 * 1536 and \
+                    c["n"] * c["top_k"] * c["d_in"] * c["d_out"] <= 8190 * 8 * 2048 * 1536:
+                return c
+    while True:
+        p = rng.choice(["bf16", "f32"])
+        c = dict(op=op, tensors=_log(rng, 1, 256), numel=_log(rng, 1, 14336 * 4096),
+                 ragged=rng.random() < 0.6, p=p, g=rng.choice(["bf16", "f32"]),
+                 master=p == "bf16" and rng.random() < 0.5, bits=rng.choice([8, 32]),
+                 live=rng.choice([1.0, 1.0, 0.5]))
+        if c["tensors"] * c["numel"] <= 64 * 1536 * 2048 // 2:
+            return c
+
+
+def _sizes(case):
+    """Elements of every tensor."""
+    t, n = case["tensors"], case["numel"]
+    if not case["ragged"]:
+        return [n] * t
+    return [max(1, n * (i + 1) // t - 7 * i % 11) for i in range(t)]
+
+
+def _starts(sizes):
+    """Where each tensor starts in a buffer of all of them (whole blocks), and
+    the buffer's length."""
+    at, out = 0, []
+    for n in sizes:
+        out.append(at)
+        at += (n + BLOCK - 1) // BLOCK * BLOCK
+    return out, at
+
+
+# ---------------------------------------------------------------------------
+# inputs
+# ---------------------------------------------------------------------------
+def _activations(g, n, d, dtype):
+    """Normal rows with a few large channels and a row scale each, as a
+    layer's activations have."""
+    x = torch.randn(n, d, generator=g, device=DEV)
+    x *= torch.exp2(torch.randint(-2, 3, (n, 1), generator=g, device=DEV).float())
+    x *= torch.where(torch.rand(1, d, generator=g, device=DEV) < 0.01, 8.0, 1.0)
+    return x.to(dtype)
+
+
+def _choices(g, c):
+    """The router's choices: top_k distinct experts a token, some experts more
+    popular than others; padded tokens name none (-1)."""
+    n, k, e = c["n"], c["top_k"], c["experts"]
+    liking = 0.5 * torch.randn(1, e, generator=g, device=DEV)
+    noise = -torch.log(-torch.log(torch.rand(n, e, generator=g, device=DEV).clamp(1e-9, 1 - 1e-7)))
+    ids = (liking + noise).topk(k, dim=1).indices.to(torch.int32)
+    if c["drop"]:
+        ids[torch.rand(n, generator=g, device=DEV) < c["drop"]] = -1
+    return ids.contiguous()
+
+
+def _prepare_adapters(s, g):
+    n, d_in, d_out, S, r = s["n"], s["d_in"], s["d_out"], s["slots"], s["r_max"]
+    dt = DTYPES[s["dtype"]]
+    s["X"] = _activations(g, n, d_in, dt)
+    s["dY"] = (_activations(g, n, d_out, torch.float32) * 2.0 ** -10).to(dt)
+    pick = torch.randint(-1, S, (n,), generator=g, device=DEV, dtype=torch.int32)
+    # a batch longer than the slots is examples of many rows each, otherwise single rows
+    s["slot"] = pick if n <= 4 * S else torch.sort(pick).values
+    s["rank"] = torch.randint(1, r // 8 + 1, (S,), generator=g, device=DEV, dtype=torch.int32) * 8
+    live = (torch.arange(r, device=DEV) < s["rank"].unsqueeze(1)).unsqueeze(-1)
+    s["A"] = torch.where(live, torch.randn(S, r, d_in, generator=g, device=DEV) * 0.02, 0).to(dt)
+    s["Bt"] = torch.where(live, torch.randn(S, r, d_out, generator=g, device=DEV) * 0.02, 0).to(dt)
+    # the forward pass's H, of which rows of no adapter and ranks past a slot's are unused
+    s["H"] = _low(s, s["X"], s["A"])
+    # the frozen base weight, transposed once when the model is loaded
+    if s["dx"]:
+        s["Wt"] = (torch.randn(d_in, d_out, generator=g, device=DEV) * 0.02).to(dt)
+        s["dX"] = torch.empty(n, d_in, dtype=dt, device=DEV)
+    s["dH"] = torch.zeros(n, r, device=DEV)
+    # an optimizer's gradients: those of slots without rows stay
+    s["dA"] = torch.randn(S, r, d_in, generator=g, device=DEV) * 2.0 ** -6
+    s["dBt"] = torch.randn(S, r, d_out, generator=g, device=DEV) * 2.0 ** -6
+
+
+def _prepare_experts(s, g):
+    n, k, E, d_in, d_out = s["n"], s["top_k"], s["experts"], s["d_in"], s["d_out"]
+    s["ids"] = _choices(g, s)
+    rows = n if s["gathered"] else n * k
+    s["X"] = _activations(g, rows, d_in, torch.bfloat16)
+    s["W"] = torch.empty(E, d_out, d_in, dtype=torch.bfloat16, device=DEV)
+    for e in range(E):
+        s["W"][e] = torch.randn(d_out, d_in, generator=g, device=DEV) * 0.02
+    # rows behind the last routed one are never written
+    if s["back"]:
+        s["dY"] = (torch.randn(n * k, d_out, generator=g, device=DEV) * 2.0 ** -8).bfloat16()
+        s["dXs"] = torch.zeros(n * k, d_in, dtype=torch.bfloat16, device=DEV)
+        s["dW"] = torch.zeros(E, d_out, d_in, dtype=DTYPES[s["dw"]], device=DEV)
+        if s["acc"]:
+            s["dW"].copy_(torch.randn(d_out, d_in, generator=g, device=DEV) * 2.0 ** -5)
+    else:
+        s["Y"] = torch.zeros(n * k, d_out, dtype=torch.bfloat16, device=DEV)
+    # rows of the fullest expert: the padding of the plain form's batched product
+    flat = s["ids"].reshape(-1).long()
+    s["most"] = max(1, int(torch.bincount(flat + 1, minlength=E + 1)[1:].max()))
+
+
+def _prepare_adamw(s, g):
+    sizes = _sizes(s)
+    starts, total = _starts(sizes)
+    s["sizes"], s["starts"], s["total"] = sizes, starts, total
+    inside = torch.zeros(total, dtype=torch.bool, device=DEV)
+    scale = torch.empty(total // BLOCK, device=DEV)
+    for i, (a, n) in enumerate(zip(starts, sizes)):
+        inside[a:a + n] = True
+        scale[a // BLOCK:(a + n + BLOCK - 1) // BLOCK] = 2.0 ** -(8 + i % 5)
+    scale = scale.repeat_interleave(BLOCK)             # gradients of a tensor's own size
+
+    def normal():
+        return torch.where(inside, torch.randn(total, generator=g, device=DEV), 0)
+
+    w = normal() * 0.02
+    s["p"] = w.to(DTYPES[s["p"]])
+    if s["master"]:
+        s["w"] = w
+    s["g"] = (normal() * scale).to(DTYPES[s["g"]])
+    # moments as after some hundred steps: the first a fraction of the gradients' size
+    m = normal() * scale * 0.2
+    v = torch.where(inside, (scale * (0.5 + torch.rand(total, generator=g, device=DEV))) ** 2, 0)
+    if s["bits"] == 32:
+        s["m"], s["v"] = m, v
+    else:
+        sm, sv = m.reshape(-1, BLOCK).abs().amax(1), v.reshape(-1, BLOCK).amax(1)
+        x = m.reshape(-1, BLOCK) / sm.clamp(min=1e-30).unsqueeze(1)
+        s["mc"] = (torch.sign(x) * torch.round(x.abs().sqrt() * 127)).to(torch.int8).reshape(-1)
+        y = v.reshape(-1, BLOCK) / sv.clamp(min=1e-30).unsqueeze(1)
+        s["vc"] = torch.round(y ** 0.25 * 255).to(torch.uint8).reshape(-1)
+        s["ms"], s["vs"] = sm, sv
+        # eight bits hold no more than bf16 does
+        s["m_out"], s["v_out"] = (torch.empty(total, dtype=torch.bfloat16, device=DEV)
+                                  for _ in range(2))
+    T = len(sizes)
+    s["step"] = torch.randint(1, 2000, (T,), generator=g, device=DEV, dtype=torch.int32)
+    s["active"] = (torch.rand(T, generator=g, device=DEV) < s["live"]).to(torch.int32)
+
+
+def prepare(case, seed):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(int(seed))
+    s = dict(case)
+    {"adapters": _prepare_adapters, "experts": _prepare_experts,
+     "adamw": _prepare_adamw}[case["op"]](s, g)
+    if own:
+        # the handles a program keeps beside its buffers
+        import segmented_rank_gemm_segment_amd as srg
+        if case["op"] == "adapters":
+            s["pool"] = srg.Pool(s["A"], s["Bt"], s["rank"], ALPHA)
+            s["seg"] = srg.Segments(case["n"], case["slots"], DEV)
+        elif case["op"] == "experts":
+            s["ex"] = srg.Experts(case["n"], case["top_k"], case["experts"], DEV)
+        else:
+            def parts(buf):
+                return [buf[a:a + n] for a, n in zip(s["starts"], s["sizes"])]
+            opt = srg.AdamW(parts(s["p"]), parts(s["g"]), bits=case["bits"],
+                            masters=parts(s["w"]) if case["master"] else None)
+            if case["bits"] == 32:
+                opt.m.copy_(s.pop("m"))
+                opt.v.copy_(s.pop("v"))
+            else:
+                opt.m.copy_(s.pop("mc"))
+                opt.v.copy_(s.pop("vc"))
+                opt.m_scale.copy_(s.pop("ms"))
+                opt.v_scale.copy_(s.pop("vs"))
+            opt.step.copy_(s["step"])
+            s["opt"] = opt
+    return s
+
+
+# ---------------------------------------------------------------------------
+# plain forms
+# ---------------------------------------------------------------------------
+def _live(s):
+    """Which (row, slot, rank) triples count: [n, slots r_max]."""
+    S, r = s["slots"], s["r_max"]
+    live = torch.arange(r, device=DEV) < s["rank"].unsqueeze(1)                   # [S, r]
+    mine = s["slot"].unsqueeze(1) == torch.arange(S, device=DEV)                  # [n, S]
+    return (mine.unsqueeze(-1) & live).reshape(-1, S * r)
+
+
+def _low(s, Z, P):
+    """Each row's product with its own slot's rank rows of P, [n, r_max]."""
+    S, r = s["slots"], s["r_max"]
+    full = Z.float() @ P.float().reshape(S * r, -1).t()
+    return torch.where(_live(s), full, 0).reshape(-1, S, r).sum(1)
+
+
+def _plain_adapters(s):
+    S, r = s["slots"], s["r_max"]
+    live = _live(s)
+    dY, X = s["dY"].float(), s["X"].float()
+    dH = _low(s, dY, s["Bt"])
+    scale = (ALPHA / s["rank"].float()).repeat_interleave(r)                      # [S r]
+    spread_h = torch.where(live, s["H"].repeat(1, S) * scale, 0)                  # [n, S r]
+    spread_d = torch.where(live, dH.repeat(1, S) * scale, 0)
+    written = live.any(0).reshape(S, r, 1)
+    out = {"dH": dH}
+    for name, spread, Z in (("dA", spread_d, X), ("dBt", spread_h, dY)):
+        new = (spread.t() @ Z).reshape(S, r, -1)
+        out[name] = torch.where(written, new + s[name] if s["acc"] else new, s[name])
+    if s["dx"]:
+        dX = dY @ s["Wt"].float().t() + spread_d @ s["A"].float().reshape(S * r, -1)
+        out["dX"] = dX.to(s["X"].dtype)
+    return out
+
+
+def _sort(s):
+    """Choices by expert, in order within one: sorted -> choice, whether a sorted
+    row is a routed one, and its place in a batch of `most` rows an expert."""
+    flat = s["ids"].reshape(-1).long()
+    E = s["experts"]
+    key = torch.where((flat >= 0) & (flat < E), flat, E)
+    order = torch.argsort(key, stable=True)
+    off = torch.searchsorted(key[order].contiguous(), torch.arange(E + 1, device=DEV))
+    e = key[order]
+    place = e * s["most"] + torch.arange(e.numel(), device=DEV) - off[e]
+    return order, e < E, torch.where(e < E, place, E * s["most"]), off
+
+
+def _plain_experts(s):
+    order, routed, place, off = _sort(s)
+    E, most = s["experts"], s["most"]
+
+    def batch(rows):
+        b = torch.zeros(E * most + 1, rows.shape[1], device=DEV)
+        b[place] = rows.float()
+        return b[:-1].reshape(E, most, -1)
+
+    def unbatch(b):
+        rows = b.reshape(E * most, -1)[place.clamp(max=E * most - 1)]
+        return torch.where(routed.unsqueeze(1), rows, 0).bfloat16()
+
+    X = batch(s["X"][order // s["top_k"]] if s["gathered"] else s["X"])
+    out = {"offsets": off.int()}
+    if not s["back"]:
+        out["Y"] = unbatch(torch.bmm(X, s["W"].float().transpose(1, 2).contiguous()))
+        return out
+    dY = batch(s["dY"])
+    out["dXs"] = unbatch(torch.bmm(dY, s["W"].float()))
+    dW = torch.bmm(dY.transpose(1, 2).contiguous(), X)
+    out["dW"] = (dW + s["dW"].float() if s["acc"] else dW).to(s["dW"].dtype)
+    return out
+
+
+_K1, _K2, _LOW = 0x9E3779B1, 0x6A09E667, 0xFFFFFFFF
+
+
+def _mix(x):
+    """A 32-bit mixing of whole numbers: shifts and odd factors, in turn."""
+    x = x ^ (x >> 16)
+    x = (x * _K1) & _LOW
+    x = x ^ (x >> 15)
+    x = (x * _K2) & _LOW
+    return x ^ (x >> 16)
+
+
+def _uniform(t, step, n):
+    """The uniform numbers of n elements of tensor t (of fewer than 2^32): for the
+    first moment, for the second."""
+    key = _mix(_mix(SEED ^ ((step * _K1) & _LOW)) + t & _LOW)
+    i = torch.arange(n, device=DEV)
+    h = _mix(i ^ _mix(key))
+    return (h & 0xFFFF).float() * 2.0 ** -16, (h >> 16).float() * 2.0 ** -16
+
+
+def _blocks(x):
+    """[blocks, 256], the last one filled up with zeros."""
+    pad = -x.numel() % BLOCK
+    return torch.cat([x, x.new_zeros(pad)]).reshape(-1, BLOCK) if pad else x.reshape(-1, BLOCK)
+
+
+def _read_m(c, scale):
+    t = _blocks(c).float() * (1 / 127)
+    return (scale.unsqueeze(1) * (t * t.abs())).reshape(-1)[:c.numel()]
+
+
+def _read_v(c, scale):
+    t = _blocks(c).float() * (1 / 255)
+    t = t * t
+    return (scale.unsqueeze(1) * (t * t)).reshape(-1)[:c.numel()]
+
+
+def _code_m(m, u):
+    b, u = _blocks(m), _blocks(u)
+    scale = b.abs().amax(1)
+    z = b.abs() * (1 / scale.clamp(min=2.0 ** -100)).unsqueeze(1) * 16129.0
+    c = torch.floor(torch.sqrt(z)).clamp(max=127)
+    c = c + (z - c * c > u * (2 * c + 1))
+    live = scale >= 2.0 ** -100
+    c = torch.where(live.unsqueeze(1), torch.sign(b) * c.clamp(max=127), 0)
+    return c.to(torch.int8).reshape(-1)[:m.numel()], torch.where(live, scale, 0)
+
+
+def _code_v(v, u):
+    b, u = _blocks(v), _blocks(u)
+    scale = b.amax(1)
+    z = b * (1 / scale.clamp(min=2.0 ** -100)).unsqueeze(1) * 4228250625.0
+    c = torch.floor(torch.sqrt(torch.sqrt(z))).clamp(max=255)
+    lo, hi = (c * c) * (c * c), ((c + 1) * (c + 1)) * ((c + 1) * (c + 1))
+    c = (c + (z - lo > u * (hi - lo))).clamp(max=255)
+    live = scale >= 2.0 ** -100
+    c = torch.where(live.unsqueeze(1), torch.where(b > 0, c.clamp(min=1), 0), 0)
+    return c.to(torch.uint8).reshape(-1)[:v.numel()], torch.where(live, scale, 0)
+
+
+def _plain_adamw(s):
+    eight = s["bits"] == 8
+    for i, (a, n) in enumerate(zip(s["starts"], s["sizes"])):
+        at, blk = slice(a, a + n), slice(a // BLOCK, (a + n + BLOCK - 1) // BLOCK)
+        on = s["active"][i] != 0
+        step = s["step"][i] + on.int()
+        t = step.double()
+        rate = (LR / (1 - BETA1 ** t)).float()
+        root = (1 / torch.sqrt(1 - BETA2 ** t)).float()
+        g = s["g"][at].float()
+        m = _read_m(s["mc"][at], s["ms"][blk]) if eight else s["m"][at]
+        v = _read_v(s["vc"][at], s["vs"][blk]) if eight else s["v"][at]
+        m = m * BETA1 + g * (1 - BETA1)
+        v = v * BETA2 + (g * g) * (1 - BETA2)
+        w = s["w"][at] if s["master"] else s["p"][at].float()
+        w = w * (1 - LR * DECAY) - rate * (m / (torch.sqrt(v) * root + EPS))
+        if s["master"]:
+            s["w"][at] = torch.where(on, w, s["w"][at])
+        s["p"][at] = torch.where(on, w.to(s["p"].dtype), s["p"][at])
+        if eight:
+            um, uv = _uniform(i, step.long(), n)
+            (mc, ms), (vc, vs) = _code_m(m, um), _code_v(v, uv)
+            s["mc"][at] = torch.where(on, mc, s["mc"][at])
+            s["vc"][at] = torch.where(on, vc, s["vc"][at])
+            s["ms"][blk] = torch.where(on, ms, s["ms"][blk])
+            s["vs"][blk] = torch.where(on, vs, s["vs"][blk])
+        else:
+            s["m"][at] = torch.where(on, m, s["m"][at])
+            s["v"][at] = torch.where(on, v, s["v"][at])
+        s["step"][i] = step
+    out = {"p": s["p"], "step": s["step"]}
+    if s["master"]:
+        out["w"] = s["w"]
+    out["m"] = _read_m(s["mc"], s["ms"]).bfloat16() if eight else s["m"]
+    out["v"] = _read_v(s["vc"], s["vs"]).bfloat16() if eight else s["v"]
+    return out
+
+
+# ---------------------------------------------------------------------------
+# one pass
+# ---------------------------------------------------------------------------
+def _own(s):
+    import segmented_rank_gemm_segment_amd as srg
+    op = s["op"]
+    if op == "adapters":
+        srg.lora_build_segments(s["slot"], s["pool"], s["seg"])
+        srg.lora_linear_backward(s["dY"], s.get("Wt"), s["X"], s["H"], s["seg"], s["pool"],
+                                 s["dH"], s.get("dX"), s["dA"], s["dBt"], accumulate=s["acc"])
+        out = {"dH": s["dH"], "dA": s["dA"], "dBt": s["dBt"]}
+        if s["dx"]:
+            out["dX"] = s["dX"]
+        return out
+    if op == "experts":
+        ex = s["ex"]
+        srg.lora_experts_sort(s["ids"], ex)
+        if not s["back"]:
+            srg.lora_experts_gemm(s["X"], ex, s["W"], s["Y"], gathered=s["gathered"])
+            return {"offsets": ex.expert_offsets, "Y": s["Y"]}
+        srg.lora_experts_gemm_backward(s["dY"], s["X"], ex, s["W"], s["dXs"], s["dW"],
+                                       gathered=s["gathered"], accumulate=s["acc"])
+        return {"offsets": ex.expert_offsets, "dXs": s["dXs"], "dW": s["dW"]}
+    opt = s["opt"]
+    srg.lora_adamw_step(opt, LR, BETA1, BETA2, EPS, DECAY, active=s["active"], seed=SEED)
+    out = {"p": s["p"], "step": opt.step}
+    if s["master"]:
+        out["w"] = s["w"]
+    if s["bits"] == 32:
+        out["m"], out["v"] = opt.m, opt.v
+    else:
+        # the moments as values, as for a checkpoint of another format
+        srg.lora_adamw_read(opt, s["m_out"], s["v_out"])
+        out["m"], out["v"] = s["m_out"], s["v_out"]
+    return out
+
+
+def run(state):
+    if own:
+        return _own(state)
+    return {"adapters": _plain_adapters, "experts": _plain_experts,
+            "adamw": _plain_adamw}[state["op"]](state)
+
+
+# ---------------------------------------------------------------------------
+# what a pass cannot do without
+# ---------------------------------------------------------------------------
+def work(case):
+    op = case["op"]
+    if op == "adapters":
+        n, d_in, d_out = case["n"], case["d_in"], case["d_out"]
+        e = 2 if case["dtype"] == "bf16" else 4
+        r = case["r_max"] / 2 + 4                     # ranks are multiples of 8 up to r_max
+        used = case["slots"] * (1 - (1 - 1 / (case["slots"] + 1)) ** n)
+        kept = n * case["slots"] / (case["slots"] + 1)
+        # dY, X and H, the slots' B, dH and the gradients
+        size = n * (d_in + d_out) * e + 8 * kept * r + 4 * n + used * r * d_out * e
+        size += used * r * (d_in + d_out) * (8 if case["acc"] else 4)
+        flops = 2 * kept * r * (d_in + 2 * d_out)
+        if case["dx"]:
+            size += (d_in * d_out + n * d_in + used * r * d_in) * e
+            flops += 2 * n * d_in * d_out + 2 * kept * r * d_in
+        return {"bytes": size, "flops": flops}
+    if op == "experts":
+        n, k, E, d_in, d_out = (case[x] for x in ("n", "top_k", "experts", "d_in", "d_out"))
+        kept = n * k * (1 - case["drop"])
+        used = E * (1 - (1 - 1 / E) ** kept)
+        rows = n * (1 - case["drop"]) if case["gathered"] else kept
+        size = 4 * n * k + 2 * rows * d_in + 2 * used * d_in * d_out + 2 * kept * d_out
+        if not case["back"]:
+            return {"bytes": size, "flops": 2 * kept * d_in * d_out}
+        size += 2 * kept * d_in
+        size += E * d_in * d_out * (2 if case["dw"] == "bf16" else 4) * (2 if case["acc"] else 1)
+        return {"bytes": size, "flops": 4 * kept * d_in * d_out}
+    live = sum(_sizes(case)) * case["live"]
+    e = {"bf16": 2, "f32": 4}
+    per = e[case["g"]] + (8 + e["bf16"] if case["master"] else 2 * e[case["p"]])
+    if case["bits"] == 32:
+        return {"bytes": live * (per + 16), "flops": 0}
+    # the moments' codes and scales, and the values they are read back as
+    return {"bytes": live * (per + 4 + 16 / BLOCK) + sum(_sizes(case)) * (2 + 4 + 8 / BLOCK),
+            "flops": 0}
+
+
+# ---------------------------------------------------------------------------
+# from the definitions, in 64 bits
+# ---------------------------------------------------------------------------
+def _exact_adapters(s):
+    n, S, r = s["n"], s["slots"], s["r_max"]
+    dY, X = s["dY"].double(), s["X"].double()
+    out = {"dH": torch.zeros(n, r, dtype=torch.float64, device=DEV),
+           "dA": s["dA"].double(), "dBt": s["dBt"].double()}
+    if s["dx"]:
+        out["dX"] = dY @ s["Wt"].double().t()
+    for a, k in enumerate(s["rank"].tolist()):
+        rows = (s["slot"] == a).nonzero().squeeze(1)
+        if not rows.numel():
+            continue
+        scale = ALPHA / k
+        dh = dY[rows] @ s["Bt"][a, :k].double().t()
+        out["dH"][rows, :k] = dh
+        new_a = scale * (dh.t() @ X[rows])
+        new_b = scale * (s["H"][rows, :k].double().t() @ dY[rows])
+        keep = 1.0 if s["acc"] else 0.0
+        out["dA"][a, :k] = keep * out["dA"][a, :k] + new_a
+        out["dBt"][a, :k] = keep * out["dBt"][a, :k] + new_b
+        if s["dx"]:
+            out["dX"][rows] += scale * (dh @ s["A"][a, :k].double())
+    return out
+
+
+def _exact_experts(s):
+    n, k, E = s["n"], s["top_k"], s["experts"]
+    ids = s["ids"].reshape(-1)
+    by_expert = [(ids == e).nonzero().squeeze(1) for e in range(E)]
+    out = {"offsets": None}
+    if s["back"]:
+        out["dXs"] = torch.zeros(n * k, s["d_in"], dtype=torch.float64, device=DEV)
+        out["dW"] = s["dW"].double() if s["acc"] else torch.zeros_like(s["dW"],
+                                                                       dtype=torch.float64)
+    else:
+        out["Y"] = torch.zeros(n * k, s["d_out"], dtype=torch.float64, device=DEV)
+    at = 0
+    for e, choice in enumerate(by_expert):
+        end = at + choice.numel()
+        if end > at:
+            X = (s["X"][choice // k] if s["gathered"] else s["X"][at:end]).double()
+            W = s["W"][e].double()
+            if s["back"]:
+                dY = s["dY"][at:end].double()
+                out["dXs"][at:end] = dY @ W
+                out["dW"][e] += dY.t() @ X
+            else:
+                out["Y"][at:end] = X @ W.t()
+        at = end
+    return out
+
+
+def _exact_codes(x, power, levels, u):
+    """Codes 0..levels of the magnitudes x >= 0 whose value is (c / levels)^power
+    times the block's largest, a value between two codes going up with its
+    share of the way; and the value they stand for."""
+    n = x.numel()
+    pad = -n % BLOCK
+    b = torch.nn.functional.pad(x, (0, pad)).reshape(-1, BLOCK)
+    u = torch.nn.functional.pad(u.double(), (0, pad)).reshape(-1, BLOCK)
+    top = b.amax(1, keepdim=True)
+    share = torch.where(top > 0, b / top.clamp(min=1e-300), 0)
+    code = torch.floor(share ** (1 / power) * levels + 1e-12).clamp(0, levels)
+
+    def value(c):
+        return (c / levels) ** power
+
+    up = (share - value(code)) > u * (value(code + 1) - value(code))
+    code = (code + up).clamp(max=levels)
+    if power == 4:
+        code = torch.where(b > 0, code.clamp(min=1), code)
+    return (top * value(code)).reshape(-1)[:n]
+
+
+def _exact_adamw(s):
+    eight = s["bits"] == 8
+    out = {"p": s["p"].double(), "step": None}
+    if s["master"]:
+        out["w"] = s["w"].double()
+
+    def values(codes, scales, levels, power):
+        x = codes.double() / levels
+        x = torch.sign(x) * x.abs() ** power
+        return (x.reshape(-1, BLOCK) * scales.double().unsqueeze(1)).reshape(-1)
+
+    out["m"] = values(s["mc"], s["ms"], 127, 2) if eight else s["m"].double()
+    out["v"] = values(s["vc"], s["vs"], 255, 4) if eight else s["v"].double()
+    active, steps = s["active"].tolist(), s["step"].tolist()
+    for i, (a, n) in enumerate(zip(s["starts"], s["sizes"])):
+        if not active[i]:
+            continue
+        at, t = slice(a, a + n), steps[i] + 1
+        g = s["g"][at].double()
+        m = BETA1 * out["m"][at] + (1 - BETA1) * g
+        v = BETA2 * out["v"][at] + (1 - BETA2) * g ** 2
+        w = (s["w"] if s["master"] else s["p"])[at].double()
+        mean, square = m / (1 - BETA1 ** t), v / (1 - BETA2 ** t)
+        w = w - LR * DECAY * w - LR * mean / (torch.sqrt(square) + EPS)
+        out["p"][at] = w
+        if s["master"]:
+            out["w"][at] = w
+        if eight:
+            um, uv = _uniform(i, t, n)
+            m = torch.sign(m) * _exact_codes(m.abs(), 2, 127, um)
+            v = _exact_codes(v, 4, 255, uv)
+        out["m"][at], out["v"][at] = m, v
+    return out
+
+
+def exact(case, seed):
+    s = prepare(case, seed)
+    if own:
+        # the handle took the moments; the definition needs them as they were
+        opt = s["opt"] if "opt" in s else None
+        if opt is not None and case["bits"] == 32:
+            s["m"], s["v"] = opt.m, opt.v
+        elif opt is not None:
+            s["mc"], s["vc"], s["ms"], s["vs"] = opt.m, opt.v, opt.m_scale, opt.v_scale
+    return {"adapters": _exact_adapters, "experts": _exact_experts,
+            "adamw": _exact_adamw}[case["op"]](s)
