@@ -17,8 +17,8 @@ The 8-bit moments: a block of 256 consecutive elements of a tensor has the scale
 s = max |x|.  First moment: codes c in -127..127, value s (c / 127) |c / 127|.
 Second moment: codes 0..255, value s (c / 255)^4.  A value between two codes
 takes the upper one with the probability that makes its expectation the value
-itself; the uniform numbers are a hash of (seed, step, tensor, element).  A
-second moment above 0 takes code 1 at least.
+itself; the uniform number of an element, for both of its moments, is a hash of
+(seed, step, tensor, element).  A second moment above 0 takes code 1 at least.
 """
 import math
 
@@ -370,12 +370,11 @@ def _mix(x):
 
 
 def _uniform(t, step, n):
-    """The uniform numbers of n elements of tensor t (of fewer than 2^32): for the
-    first moment, for the second."""
+    """The uniform numbers of n elements of tensor t (of fewer than 2^32), the low
+    and the high half of a hash for two elements."""
     key = _mix(_mix(SEED ^ ((step * _K1) & _LOW)) + t & _LOW)
-    i = torch.arange(n, device=DEV)
-    h = _mix(i ^ _mix(key))
-    return (h & 0xFFFF).float() * 2.0 ** -16, (h >> 16).float() * 2.0 ** -16
+    h = _mix(torch.arange((n + 1) // 2, device=DEV) ^ _mix(key))
+    return (torch.stack([h & 0xFFFF, h >> 16], 1).reshape(-1)[:n]).float() * 2.0 ** -16
 
 
 def _blocks(x):
@@ -438,8 +437,8 @@ def _plain_adamw(s):
             s["w"][at] = torch.where(on, w, s["w"][at])
         s["p"][at] = torch.where(on, w.to(s["p"].dtype), s["p"][at])
         if eight:
-            um, uv = _uniform(i, step.long(), n)
-            (mc, ms), (vc, vs) = _code_m(m, um), _code_v(v, uv)
+            u = _uniform(i, step.long(), n)
+            (mc, ms), (vc, vs) = _code_m(m, u), _code_v(v, u)
             s["mc"][at] = torch.where(on, mc, s["mc"][at])
             s["vc"][at] = torch.where(on, vc, s["vc"][at])
             s["ms"][blk] = torch.where(on, ms, s["ms"][blk])
@@ -644,9 +643,9 @@ def _exact_adamw(s):
         if s["master"]:
             out["w"][at] = w
         if eight:
-            um, uv = _uniform(i, t, n)
-            m = torch.sign(m) * _exact_codes(m.abs(), 2, 127, um)
-            v = _exact_codes(v, 4, 255, uv)
+            u = _uniform(i, t, n)
+            m = torch.sign(m) * _exact_codes(m.abs(), 2, 127, u)
+            v = _exact_codes(v, 4, 255, u)
         out["m"][at], out["v"][at] = m, v
     return out
 
