@@ -532,6 +532,86 @@ lora_status lora_experts_gemm_mxfp4w(const void *X, int64_t ldx, int32_t gathere
                                      int32_t d_in, int32_t d_out, void *stream);
 
 /*
+ * AdamW over many tensors at once (decoupled weight decay), for adapters and
+ * experts in training: per element, with t the tensor's own step count,
+ *   m = beta1 m + (1 - beta1) g,   v = beta2 v + (1 - beta2) g^2,
+ *   w = (1 - lr weight_decay) w - lr / (1 - beta1^t) m / (sqrt(v / (1 - beta2^t)) + eps)
+ * in fp32 (the bias corrections in 64 bits).  Tensors and gradients are contiguous,
+ * of one dtype each (bf16 or fp32); with a master, an fp32 copy, the master is what
+ * is updated and the bf16 tensor its rounding, otherwise each step rounds the tensor.
+ *
+ * state_bits 32: m and v are fp32.  state_bits 8: blocks of LORA_ADAMW_BLOCK
+ * consecutive elements of a tensor share an fp32 scale, their largest magnitude; m
+ * holds int8 codes c of values scale (c / 127) |c / 127|, v uint8 codes of values
+ * scale (c / 255)^4.  A value between two codes takes the upper one with the
+ * probability that makes the expectation the value itself, by a hash of (seed, t,
+ * tensor, element): the same call gives the same codes.  A v above 0 takes code 1
+ * at least.  A block whose largest is below 2^-100 becomes zeros; one with an
+ * infinity or NaN gets a NaN scale and codes 0.
+ *
+ * Tensor i's moments start at element start(i), the sum of the earlier tensors'
+ * numel, each rounded up to whole blocks; m and v hold lora_adamw_state_numel
+ * elements, the scales one value a block.  Elements between tensors are scratch.
+ *
+ * lora_adamw_table fills a HOST table of lora_adamw_table_bytes bytes from a HOST
+ * array of tensors, and checks them: a NULL tensor or gradient of numel > 0
+ * (LORA_ERR_NULL), a numel outside [0, LORA_ADAMW_MAX_NUMEL], n_tensors outside
+ * [1, LORA_ADAMW_MAX_TENSORS], masters for some tensors only or beside fp32
+ * tensors, a tensor or master that overlaps another one or a gradient
+ * (LORA_ERR_SHAPE), an unknown dtype (LORA_ERR_DTYPE), a pointer off 16 bytes
+ * (LORA_ERR_ALIGN).  The caller copies it to the device once and keeps it with the
+ * rest of the lora_adamw; a part of it is written by every step, so steps
+ * on one lora_adamw (replays of graphs among them) have to be ordered.
+ * The sizes functions return -1 for sizes out of range.
+ *
+ * lora_adamw_step: active, NULL or device int32 [n_tensors]: a tensor whose entry is
+ * 0 (an adapter with no rows in the batch) is left as it is, its moments and step
+ * count too.  lr is read from lr_dev (device fp32) where that is not NULL;
+ * grad_scale, NULL or device fp32: multiplies every gradient.  Errors: sizes, lr
+ * not finite, beta outside [0, 1), eps <= 0, weight_decay not finite or negative (LORA_ERR_SHAPE),
+ * state_bits other than 8 or 32 (LORA_ERR_DTYPE), NULL, alignment of 16 bytes (4
+ * for step, active, lr_dev and grad_scale).
+ *
+ * lora_adamw_read: the values of 8-bit moments as `dtype`, into m_out and v_out
+ * [state_numel] (LORA_ERR_DTYPE for 32-bit moments, which are values already).
+ */
+#define LORA_ADAMW_BLOCK 256
+#define LORA_ADAMW_MAX_TENSORS (1 << 20)
+#define LORA_ADAMW_MAX_NUMEL ((int64_t)1 << 40)
+typedef struct {
+  void *param;
+  const void *grad;
+  float *master; /* NULL: none */
+  int64_t numel;
+} lora_adamw_tensor;
+typedef struct {
+  int32_t n_tensors;
+  int32_t param_dtype;   /* lora_dtype */
+  int32_t grad_dtype;    /* lora_dtype */
+  int32_t masters;       /* other than 0: the tensors have masters */
+  int32_t state_bits;    /* 32 or 8 */
+  int64_t state_numel;   /* lora_adamw_state_numel() of the tensors */
+  void *table;           /* device copy of the table */
+  int64_t table_bytes;   /* lora_adamw_table_bytes() of the tensors */
+  void *m;
+  void *v;
+  float *m_scale;        /* state_bits 8 only */
+  float *v_scale;
+  int32_t *step;         /* [n_tensors], 0 before a tensor's first step */
+} lora_adamw;
+
+int64_t lora_adamw_state_numel(const lora_adamw_tensor *tensors, int32_t n_tensors);
+int64_t lora_adamw_table_bytes(const lora_adamw_tensor *tensors, int32_t n_tensors);
+lora_status lora_adamw_table(const lora_adamw_tensor *tensors, int32_t n_tensors,
+                             int32_t param_dtype, int32_t grad_dtype, void *table);
+lora_status lora_adamw_step(const lora_adamw *opt, double lr, const float *lr_dev, double beta1,
+                            double beta2, double eps, double weight_decay,
+                            const float *grad_scale, const int32_t *active, uint32_t seed,
+                            void *stream);
+lora_status lora_adamw_read(const lora_adamw *opt, int32_t dtype, void *m_out, void *v_out,
+                            void *stream);
+
+/*
  * The whole layer in one call: lora_build_segments, lora_shrink and
  * lora_linear_fused together (adapter-batching page, sections "一个混合
  * Batch 的数学形式" and "Segmented Kernel 需要哪些 Metadata"; its section

@@ -16,6 +16,7 @@ Entry points carry the C names:
   ``lora_base_gemm_mxfp4``: MXFP4 operands)
 * ``lora_experts_sort(expert_ids, ex)``         (``_gather``, ``_combine``,
   ``_combine_backward``, ``_gemm_mxfp4w``: expert routing)
+* ``lora_adamw_step(opt, lr)``                  (``AdamW``, ``lora_adamw_read``)
 
 If the library is missing the import still succeeds, but every entry point
 raises ``RuntimeError``: there is no fallback path.
@@ -41,6 +42,7 @@ STATIC_MAX_H = 1 << 21
 LAYER_ONE_LAUNCH_ROWS = 512
 LAYER_SYNC_BYTES = 4096
 MAX_EXPERTS, MAX_TOP_K, MAX_CHOICES = 1024, 64, 1 << 30
+ADAMW_BLOCK = 256
 
 _c_int32_p = ctypes.POINTER(ctypes.c_int32)
 
@@ -92,6 +94,33 @@ class LoraExpertsC(ctypes.Structure):
     ]
 
 
+class LoraAdamwTensorC(ctypes.Structure):
+    _fields_ = [
+        ("param", ctypes.c_void_p),
+        ("grad", ctypes.c_void_p),
+        ("master", ctypes.c_void_p),
+        ("numel", ctypes.c_int64),
+    ]
+
+
+class LoraAdamwC(ctypes.Structure):
+    _fields_ = [
+        ("n_tensors", ctypes.c_int32),
+        ("param_dtype", ctypes.c_int32),
+        ("grad_dtype", ctypes.c_int32),
+        ("masters", ctypes.c_int32),
+        ("state_bits", ctypes.c_int32),
+        ("state_numel", ctypes.c_int64),
+        ("table", ctypes.c_void_p),
+        ("table_bytes", ctypes.c_int64),
+        ("m", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("m_scale", ctypes.c_void_p),
+        ("v_scale", ctypes.c_void_p),
+        ("step", ctypes.c_void_p),
+    ]
+
+
 class LoraError(RuntimeError):
     def __init__(self, code: int, msg: str):
         super().__init__(f"liblora status {code}: {msg}")
@@ -129,6 +158,11 @@ EXPORTS = (
     "lora_experts_combine",
     "lora_experts_combine_backward",
     "lora_experts_gemm_mxfp4w",
+    "lora_adamw_state_numel",
+    "lora_adamw_table_bytes",
+    "lora_adamw_table",
+    "lora_adamw_step",
+    "lora_adamw_read",
 )
 
 
@@ -202,6 +236,18 @@ def lib() -> ctypes.CDLL:
     L.lora_experts_gemm_mxfp4w.restype = i32
     L.lora_experts_gemm_mxfp4w.argtypes = [vp, i64, i32, EP, vp, i64, vp, i64, vp, i64, i32, i32,
                                            vp]
+    f64, u32 = ctypes.c_double, ctypes.c_uint32
+    AP = ctypes.POINTER(LoraAdamwC)
+    L.lora_adamw_state_numel.restype = i64
+    L.lora_adamw_state_numel.argtypes = [vp, i32]
+    L.lora_adamw_table_bytes.restype = i64
+    L.lora_adamw_table_bytes.argtypes = [vp, i32]
+    L.lora_adamw_table.restype = i32
+    L.lora_adamw_table.argtypes = [vp, i32, i32, i32, vp]
+    L.lora_adamw_step.restype = i32
+    L.lora_adamw_step.argtypes = [AP, f64, vp, f64, f64, f64, f64, vp, vp, u32, vp]
+    L.lora_adamw_read.restype = i32
+    L.lora_adamw_read.argtypes = [AP, i32, vp, vp, vp]
     if L.lora_abi_version() != ABI_VERSION:
         raise RuntimeError("liblora ABI version mismatch")
     _lib = L
@@ -883,3 +929,117 @@ def lora_experts_gemm_mxfp4w(X: torch.Tensor, ex: Experts, Wq: torch.Tensor,
     st = _launch_stream(stream, X, Wq, w_scale, Y, ex.expert_offsets)
     _check(lib().lora_experts_gemm_mxfp4w(_ptr(X), _ld(X), 1 if gathered else 0, ex.c, *w, _ptr(Y),
                                           _ld(Y), d_in, d_out, st))
+
+
+# ---------------------------------------------------------------------------
+# optimizer
+# ---------------------------------------------------------------------------
+class AdamW:
+    """The tensors of an optimizer step (lora_adamw_step) and their moments:
+    contiguous tensors and their gradients, of one dtype each (bf16 or float32),
+    all on one device.  The tensors are kept and updated in place; a step reads
+    the gradients' memory as it is then.
+
+    ``masters`` (bf16 tensors): True makes float32 copies of the tensors now, a
+    list gives them; they are what a step updates, and the tensors their
+    rounding.  ``bits``: 32, moments ``m`` and ``v`` float32; or 8, codes int8 and
+    uint8 with ``m_scale`` and ``v_scale``, one float32 per ADAMW_BLOCK elements
+    (include/lora.h has the format).  Tensor i's moments are elements [starts[i],
+    starts[i] + numel).  ``step`` int32 [n_tensors] counts each tensor's steps.
+    A checkpoint is these buffers and the masters."""
+
+    def __init__(self, params, grads, bits: int = 32, masters=None):
+        params, grads = list(params), list(grads)
+        if not params or len(params) != len(grads):
+            raise ValueError("one gradient for every tensor, at least one")
+        if bits not in (8, 32):
+            raise ValueError("bits: 8 or 32")
+        dev = params[0].device
+        if masters is True:
+            masters = [p.detach().float().contiguous() for p in params]
+        elif masters is not None and masters is not False:
+            masters = list(masters)
+            if len(masters) != len(params):
+                raise ValueError("one master for every tensor")
+        else:
+            masters = None
+        for i, (p, g) in enumerate(zip(params, grads)):
+            if p.shape != g.shape or p.device != dev or g.device != dev:
+                raise ValueError(f"tensor {i}: a gradient of its shape, on the first one's device")
+            if p.dtype != params[0].dtype or g.dtype != grads[0].dtype:
+                raise ValueError("the tensors must share a dtype, and the gradients one")
+            if not p.is_contiguous() or not g.is_contiguous():
+                raise ValueError(f"tensor {i}: contiguous tensors expected")
+        if masters is not None:
+            if params[0].dtype != torch.bfloat16:
+                raise ValueError("masters are for bf16 tensors")
+            for i, (p, w) in enumerate(zip(params, masters)):
+                if w.dtype != torch.float32 or w.shape != p.shape or w.device != dev \
+                        or not w.is_contiguous():
+                    raise ValueError(f"master {i}: contiguous float32 of the tensor's shape")
+        L = lib()
+        n = len(params)
+        host = (LoraAdamwTensorC * n)()
+        for i, (p, g) in enumerate(zip(params, grads)):
+            host[i] = LoraAdamwTensorC(_ptr(p), _ptr(g),
+                                       _ptr(masters[i]) if masters is not None else None,
+                                       p.numel())
+        total, size = L.lora_adamw_state_numel(host, n), L.lora_adamw_table_bytes(host, n)
+        if total < 0 or size < 0:
+            raise ValueError("too many tensors, or too many elements")
+        table = torch.zeros((size + 15) // 16 * 16, dtype=torch.uint8)
+        if table.data_ptr() % 16:
+            raise RuntimeError("host memory off 16 bytes")
+        p_code, g_code = _dtype_code(params[0].dtype), _dtype_code(grads[0].dtype)
+        _check(L.lora_adamw_table(host, n, p_code, g_code, table.data_ptr()))
+        self.params, self.grads, self.masters, self.bits = params, grads, masters, bits
+        self.starts, at = [], 0
+        for p in params:
+            self.starts.append(at)
+            at += -(-p.numel() // ADAMW_BLOCK) * ADAMW_BLOCK
+        self.numel = total
+        self.step = torch.zeros(n, dtype=torch.int32, device=dev)
+        eight = bits == 8
+        self.m = torch.zeros(total, dtype=torch.int8 if eight else torch.float32, device=dev)
+        self.v = torch.zeros(total, dtype=torch.uint8 if eight else torch.float32, device=dev)
+        f32 = dict(dtype=torch.float32, device=dev)
+        self.m_scale = torch.zeros(total // ADAMW_BLOCK, **f32) if eight else None
+        self.v_scale = torch.zeros(total // ADAMW_BLOCK, **f32) if eight else None
+        self._table = table.to(dev)
+        self._c = LoraAdamwC(n, p_code, g_code, 0 if masters is None else 1, bits, total,
+                             self._table.data_ptr(), size, _ptr(self.m), _ptr(self.v),
+                             _ptr(self.m_scale), _ptr(self.v_scale), self.step.data_ptr())
+        self.c = ctypes.byref(self._c)
+
+
+def lora_adamw_step(opt: AdamW, lr, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
+                    weight_decay: float = 0.01, grad_scale: Optional[torch.Tensor] = None,
+                    active: Optional[torch.Tensor] = None, seed: int = 0, stream=None) -> None:
+    """One AdamW step of every tensor of opt (decoupled weight decay).  lr: a
+    number, or a float32 device tensor of one element that is read when the step
+    runs (a captured step then follows a schedule).  grad_scale: float32 device
+    tensor of one element that multiplies every gradient (a clipping factor).
+    active: int32 device tensor [n_tensors]; tensors with 0 are left as they are,
+    their moments and step counts too.  seed: of the 8-bit moments' rounding."""
+    for t, what in ((lr if isinstance(lr, torch.Tensor) else None, "lr"),
+                    (grad_scale, "grad_scale")):
+        if t is not None and (t.dtype is not torch.float32 or t.numel() != 1):
+            raise ValueError(f"{what}: float32, one element")
+    if active is not None and (active.dtype is not torch.int32 or not active.is_contiguous()
+                               or active.shape != opt.step.shape):
+        raise ValueError("active: contiguous int32 [n_tensors]")
+    lr_dev = lr if isinstance(lr, torch.Tensor) else None
+    st = _launch_stream(stream, opt.step, lr_dev, grad_scale, active)
+    _check(lib().lora_adamw_step(opt.c, 0.0 if lr_dev is not None else lr, _ptr(lr_dev), beta1,
+                                 beta2, eps, weight_decay, _ptr(grad_scale), _ptr(active),
+                                 seed & 0xFFFFFFFF, st))
+
+
+def lora_adamw_read(opt: AdamW, m: torch.Tensor, v: torch.Tensor, stream=None) -> None:
+    """The values of 8-bit moments, into m and v (bf16 or float32, opt.numel
+    elements)."""
+    for t in (m, v):
+        if t.shape != (opt.numel,) or not t.is_contiguous() or t.dtype != m.dtype:
+            raise ValueError("m, v: contiguous [opt.numel], of one dtype")
+    st = _launch_stream(stream, opt.step, m, v)
+    _check(lib().lora_adamw_read(opt.c, _dtype_code(m.dtype), _ptr(m), _ptr(v), st))

@@ -166,6 +166,46 @@ hipError_t launch_experts_combine_backward(const void *dY, int64_t ldy, const vo
                                            int d, int dtype, void *dYs, int64_t ldds, float *dw,
                                            hipStream_t stream);
 
+// AdamW over many tensors (adamw.hip).  On the device: the tensors, the factors of a
+// step, and each chunk's tensor (a chunk is kAdamwChunk elements of one).
+constexpr int kAdamwChunk = 4096, kAdamwBlock = 256;
+// The table holds them in this order.
+struct AdamwTensor {
+  void *param;
+  const void *grad;
+  float *master;         // or null
+  int64_t numel;
+  int64_t start;         // of its moments, in elements: whole blocks
+  int64_t first_chunk;
+};
+struct AdamwFactors {
+  float rate, root, keep;
+  uint32_t key;
+  int32_t on;
+  int32_t pad[3];
+};
+constexpr int64_t kAdamwTensorBytes = sizeof(AdamwTensor) + sizeof(AdamwFactors);
+struct AdamwArgs {
+  int n_tensors, param_dtype, grad_dtype, bits;
+  bool master;
+  int64_t n_chunks;
+  const AdamwTensor *tensors;
+  const int32_t *chunk_tensor;
+  AdamwFactors *factors;
+  void *m, *v;
+  float *m_scale, *v_scale;
+  int32_t *step;
+  const int32_t *active;     // or null
+  const float *lr_dev, *grad_scale;   // or null
+  double lr, beta1, beta2, weight_decay;
+  float eps;
+  uint32_t seed;
+};
+hipError_t launch_adamw(const AdamwArgs &a, hipStream_t stream);
+hipError_t launch_adamw_read(const void *m, const void *v, const float *m_scale,
+                             const float *v_scale, int64_t total, int dtype, void *m_out,
+                             void *v_out, hipStream_t stream);
+
 // Inputs and outputs of the one-launch layer beyond the product's own
 // (layer.cuh): the per-row slot ids and the pool's shrink operands, H, the
 // sync buffer (or null) and the segment metadata it writes.
