@@ -345,6 +345,30 @@ lora_status lora_linear_fused(const void *X, int64_t ldx, const void *W, int64_t
                               const lora_pool *pool, void *Y, int64_t ldy, void *stream);
 
 /*
+ * The layer's gradients, for adapters in training on a frozen base weight: from
+ * dY, the gradient of Y = X W^T + s_a H B_a^T with H = X A_a^T, for every row i
+ * and every slot a that has rows of rank r > 0 in the batch,
+ *   dH[i][0:r] = dY[i] B_a                            fp32 [n][r_max], as H
+ *   dX[i]      = dY[i] W + s_a dH[i][0:r] A_a         pool dtype, one rounding
+ *   dA[a][k]   = s_a sum_{i in a} dH[i][k] X[i]       fp32 [n_slots][r_max][d_in]
+ *   dBt[a][k]  = s_a sum_{i in a} H[i][k] dY[i]       fp32 [n_slots][r_max][d_out]
+ * for k < r, sums in fp32 in a fixed order; with accumulate other than 0 the sums
+ * are added to dA and dBt.  Rank rows past r, slots without rows, and dH of rows
+ * without an adapter are left as they are.  (bf16 pools: H and dH enter dA's and
+ * dBt's products with 16 significant bits.)
+ * Wt is the base weight's transpose, [d_in][d_out]: laid out once, as the weight
+ * does not change.  H and seg are the forward pass's.  dX may be NULL (an input
+ * without gradient; Wt is then unused), and dA (X unused) or dBt (H unused).
+ * One projection, no DoRA (LORA_ERR_SHAPE for a stacked pool or one with
+ * dora_scale).  Other errors as lora_linear_fused.  n_rows == 0 is a no-op.
+ */
+lora_status lora_linear_backward(const void *dY, int64_t lddy, const void *Wt, int64_t ldwt,
+                                 const void *X, int64_t ldx, const float *H,
+                                 const lora_segments *seg, const lora_pool *pool, float *dH,
+                                 void *dX, int64_t lddx, float *dA, float *dBt,
+                                 int32_t accumulate, void *stream);
+
+/*
  * Quantized base weight (adapter-batching page, section "Quantized Base
  * Model 与 LoRA 的 Dtype 边界": the base weight may be INT4/INT8/FP8 while A
  * and B stay 16-bit; LoRA/QLoRA 多租户GPU推理服务化实战, section 1.2: the

@@ -11,6 +11,7 @@ Entry points carry the C names:
 * ``lora_expand(H, seg, pool, Y)``            (Y += ...)
 * ``lora_base_gemm(X, W, Y)``                 (Y = X W^T)
 * ``lora_linear_fused(X, W, H, seg, pool, Y)``  (Y = X W^T + LoRA)
+* ``lora_linear_backward(dY, Wt, X, H, seg, pool, dH, dX, dA, dBt)``  (gradients)
 * ``lora_mxfp4_quantize(X, Xq, x_scale)``      (and ``lora_mxfp4_dequantize``)
 * ``lora_base_gemm_mxfp4w(X, Wq, w_scale, Y)``  (``lora_linear_fused_mxfp4w``,
   ``lora_base_gemm_mxfp4``: MXFP4 operands)
@@ -158,6 +159,7 @@ EXPORTS = (
     "lora_experts_combine",
     "lora_experts_combine_backward",
     "lora_experts_gemm_mxfp4w",
+    "lora_linear_backward",
     "lora_adamw_state_numel",
     "lora_adamw_table_bytes",
     "lora_adamw_table",
@@ -236,6 +238,9 @@ def lib() -> ctypes.CDLL:
     L.lora_experts_gemm_mxfp4w.restype = i32
     L.lora_experts_gemm_mxfp4w.argtypes = [vp, i64, i32, EP, vp, i64, vp, i64, vp, i64, i32, i32,
                                            vp]
+    L.lora_linear_backward.restype = i32
+    L.lora_linear_backward.argtypes = [vp, i64, vp, i64, vp, i64, vp, SP, PP, vp, vp, i64, vp, vp,
+                                       i32, vp]
     f64, u32 = ctypes.c_double, ctypes.c_uint32
     AP = ctypes.POINTER(LoraAdamwC)
     L.lora_adamw_state_numel.restype = i64
@@ -929,6 +934,47 @@ def lora_experts_gemm_mxfp4w(X: torch.Tensor, ex: Experts, Wq: torch.Tensor,
     st = _launch_stream(stream, X, Wq, w_scale, Y, ex.expert_offsets)
     _check(lib().lora_experts_gemm_mxfp4w(_ptr(X), _ld(X), 1 if gathered else 0, ex.c, *w, _ptr(Y),
                                           _ld(Y), d_in, d_out, st))
+
+
+# ---------------------------------------------------------------------------
+# gradients of the layer
+# ---------------------------------------------------------------------------
+def lora_linear_backward(dY: torch.Tensor, Wt: Optional[torch.Tensor], X: Optional[torch.Tensor],
+                         H: Optional[torch.Tensor], seg: Segments, pool: Pool, dH: torch.Tensor,
+                         dX: Optional[torch.Tensor] = None, dA: Optional[torch.Tensor] = None,
+                         dBt: Optional[torch.Tensor] = None, accumulate: bool = False,
+                         stream=None) -> None:
+    """Gradients of lora_linear_fused on a frozen base weight: dH = dY B_a (like
+    H, float32 [n, r_max]), dX = dY W + s_a dH A_a, and, for the slots with rows in
+    the batch, dA = s_a dH^T X and dBt = s_a H^T dY, float32 of A's and Bt's shapes;
+    accumulate adds to dA and dBt.  Wt is the transposed base weight [d_in, d_out],
+    laid out once; H and seg are the forward pass's.  None leaves dX, dA or dBt out
+    (Wt, X or H may then be None too)."""
+    n, r = seg.n_rows, pool.r_max
+    if pool.n_proj > 1 or pool.dora_scale is not None:
+        raise ValueError("a pool of one projection and without DoRA")
+    for t, want, what in ((dY, (n, pool.d_out), "dY [n, d_out]"),
+                          (Wt if dX is not None else None, (pool.d_in, pool.d_out),
+                           "Wt [d_in, d_out]"),
+                          (X if dA is not None else None, (n, pool.d_in), "X [n, d_in]"),
+                          (dX, (n, pool.d_in), "dX [n, d_in]")):
+        if t is not None and (t.dtype != pool.dtype or tuple(t.shape) != want):
+            raise ValueError(f"{what} of the pool dtype")
+    if (dX is not None and Wt is None) or (dA is not None and X is None) \
+            or (dBt is not None and H is None):
+        raise ValueError("dX needs Wt, dA needs X, dBt needs H")
+    for t, want, what in ((dH, (n, r), "dH [n, r_max]"),
+                          (H if dBt is not None else None, (n, r), "H [n, r_max]"),
+                          (dA, tuple(pool.A.shape), "dA [n_slots, r_max, d_in]"),
+                          (dBt, tuple(pool.Bt.shape), "dBt [n_slots, r_max, d_out]")):
+        if t is not None and (t.dtype != torch.float32 or tuple(t.shape) != want
+                              or not t.is_contiguous()):
+            raise ValueError(f"{what}: contiguous float32")
+    st = _launch_stream(stream, dY, Wt, X, H, dH, dX, dA, dBt, pool.A, pool.Bt, seg.row_segment)
+    _check(lib().lora_linear_backward(
+        _ptr(dY), _ld(dY), _ptr(Wt), 0 if Wt is None else _ld(Wt), _ptr(X),
+        0 if X is None else _ld(X), _ptr(H), seg.c, pool.c, _ptr(dH), _ptr(dX),
+        0 if dX is None else _ld(dX), _ptr(dA), _ptr(dBt), 1 if accumulate else 0, st))
 
 
 # ---------------------------------------------------------------------------

@@ -94,6 +94,18 @@ lora::PoolView pool_view(const lora_pool *p) {
   return v;
 }
 
+// The pool of the gradients: dY takes X's place, so A and Bt change places.
+lora::PoolView transposed(const lora::PoolView &p) {
+  lora::PoolView v = p;
+  v.d_in = p.d_out;
+  v.d_out = p.d_in;
+  v.A = p.Bt;
+  v.Bt = p.A;
+  v.B = nullptr;
+  for (int q = 1; q <= lora::kMaxProj; ++q) v.proj.col_off[q] = v.d_out;
+  return v;
+}
+
 // FP8 weight: E4M3 codes [d_out][ldw] (16-byte aligned rows, d_in % 16 == 0)
 // and one float32 scale per output row.
 lora_status check_fp8_weight(const void *Wq, int64_t ldw, const float *w_scale, int32_t d_in,
@@ -202,6 +214,45 @@ lora_status lora_expand(const float *H, const lora_segments *seg, const lora_poo
   if (!aligned16(H)) return LORA_ERR_ALIGN;
   return hip_status(lora::launch_expand(H, seg_view(seg), pool_view(pool), Y, ldy,
                                         static_cast<hipStream_t>(stream)));
+}
+
+lora_status lora_linear_backward(const void *dY, int64_t lddy, const void *Wt, int64_t ldwt,
+                                 const void *X, int64_t ldx, const float *H,
+                                 const lora_segments *seg, const lora_pool *pool, float *dH,
+                                 void *dX, int64_t lddx, float *dA, float *dBt,
+                                 int32_t accumulate, void *stream) {
+  lora_status st = check_pool(pool);
+  if (st != LORA_OK) return st;
+  if (pool->n_proj >= 2 || pool->dora_scale) return LORA_ERR_SHAPE;
+  st = check_segments(seg, pool);
+  if (st != LORA_OK) return st;
+  const int32_t n = seg->n_rows;
+  st = check_matrix(dY, lddy, pool->d_out, n);
+  if (st != LORA_OK) return st;
+  if (dX) {
+    st = check_matrix(Wt, ldwt, pool->d_out, pool->d_in);
+    if (st != LORA_OK) return st;
+    st = check_matrix(dX, lddx, pool->d_in, n);
+    if (st != LORA_OK) return st;
+  }
+  if (dA) {
+    st = check_matrix(X, ldx, pool->d_in, n);
+    if (st != LORA_OK) return st;
+    if (!aligned16(dA)) return LORA_ERR_ALIGN;
+  }
+  if (n == 0) return LORA_OK;
+  if (!dH || (dBt && !H)) return LORA_ERR_NULL;
+  if (!aligned16(dH) || (dBt && (!aligned16(H) || !aligned16(dBt)))) return LORA_ERR_ALIGN;
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  const lora::SegView sv = seg_view(seg);
+  const lora::PoolView pv = pool_view(pool), tv = transposed(pv);
+  hipError_t e = lora::launch_shrink(dY, lddy, sv, tv, dH, s);
+  if (e == hipSuccess)
+    e = lora::launch_adapter_grads(X, ldx, dH, dA, dY, lddy, H, dBt, sv, pv, accumulate != 0, s);
+  if (e == hipSuccess && dX)
+    e = lora::launch_gemm(dY, lddy, Wt, ldwt, dX, lddx, n, pool->d_out, pool->d_in, pool->dtype, dH,
+                          &sv, &tv, s);
+  return hip_status(e);
 }
 
 lora_status lora_pool_pack_slot(const lora_pool *pool, int32_t slot, int32_t rank, double alpha,

@@ -96,6 +96,13 @@ hipError_t launch_build_shrink(const BuildArgs &a, const void *X, int64_t ldx,
 hipError_t launch_expand(const float *H, const SegView &seg, const PoolView &pool, void *Y,
                          int64_t ldy, hipStream_t stream);
 
+// dA[slot] (+)= s dH^T X and dBt[slot] (+)= s H^T dY over each segment's rows (either
+// output may be null).
+hipError_t launch_adapter_grads(const void *X, int64_t ldx, const float *dH, float *dA,
+                                const void *dY, int64_t lddy, const float *H, float *dBt,
+                                const SegView &seg, const PoolView &pool, bool accumulate,
+                                hipStream_t stream);
+
 // Adapter weights into a slot (one source per projection), then the slot's
 // rank and scale alpha / rank.  b_rank_rows: B sources are [rank][ldb]
 // (B^T) instead of [d_out_q][ldb].
