@@ -556,6 +556,32 @@ lora_status lora_experts_gemm_mxfp4w(const void *X, int64_t ldx, int32_t gathere
                                      int32_t d_in, int32_t d_out, void *stream);
 
 /*
+ * The experts' products on bf16 weights, for every sorted row p of expert e:
+ *   lora_experts_gemm            Y[p]  = X[row] W_e^T
+ *   lora_experts_gemm_backward   dXs[p] = dY[p] W_e,   dW_e = sum_p dY[p]^T X[row]
+ * with row as in lora_experts_gemm_mxfp4w (gathered != 0: sorted_choice[p] /
+ * top_k).  W [n_experts][d_out][ldw] and dW [n_experts][d_out][lddw] hold the
+ * experts' matrices one after the other; X, W, Y, dY and dXs are bf16, dW is of
+ * dw_dtype (bf16 or fp32).  Sums are fp32 with one rounding.  With accumulate other
+ * than 0 dW's old value is added before it; otherwise an expert without rows gets
+ * zeros.  Y, dY and dXs have n_tokens * top_k rows; rows of Y and dXs past
+ * expert_offsets[n_experts] are left as they were, and those of dY (and of X in
+ * sorted order) are not used.  dXs is in sorted order for gathered X too: the
+ * tokens' gradient is its lora_experts_combine with weights NULL.
+ * dXs or dW may be NULL to leave it out, not both (LORA_ERR_NULL); W may be NULL
+ * without dXs, and X without dW.  d_in and d_out are positive multiples of 8
+ * (LORA_ERR_SHAPE / _ALIGN); other errors as lora_experts_gemm_mxfp4w.
+ */
+lora_status lora_experts_gemm(const void *X, int64_t ldx, int32_t gathered,
+                              const lora_experts *ex, const void *W, int64_t ldw, void *Y,
+                              int64_t ldy, int32_t d_in, int32_t d_out, void *stream);
+lora_status lora_experts_gemm_backward(const void *dY, int64_t lddy, const void *X, int64_t ldx,
+                                       int32_t gathered, const lora_experts *ex, const void *W,
+                                       int64_t ldw, void *dXs, int64_t lddxs, void *dW,
+                                       int64_t lddw, int32_t dw_dtype, int32_t accumulate,
+                                       int32_t d_in, int32_t d_out, void *stream);
+
+/*
  * AdamW over many tensors at once (decoupled weight decay), for adapters and
  * experts in training: per element, with t the tensor's own step count,
  *   m = beta1 m + (1 - beta1) g,   v = beta2 v + (1 - beta2) g^2,

@@ -16,7 +16,7 @@ Entry points carry the C names:
 * ``lora_base_gemm_mxfp4w(X, Wq, w_scale, Y)``  (``lora_linear_fused_mxfp4w``,
   ``lora_base_gemm_mxfp4``: MXFP4 operands)
 * ``lora_experts_sort(expert_ids, ex)``         (``_gather``, ``_combine``,
-  ``_combine_backward``, ``_gemm_mxfp4w``: expert routing)
+  ``_combine_backward``, ``_gemm``, ``_gemm_backward``, ``_gemm_mxfp4w``: experts)
 * ``lora_adamw_step(opt, lr)``                  (``AdamW``, ``lora_adamw_read``)
 
 If the library is missing the import still succeeds, but every entry point
@@ -160,6 +160,8 @@ EXPORTS = (
     "lora_experts_combine_backward",
     "lora_experts_gemm_mxfp4w",
     "lora_linear_backward",
+    "lora_experts_gemm",
+    "lora_experts_gemm_backward",
     "lora_adamw_state_numel",
     "lora_adamw_table_bytes",
     "lora_adamw_table",
@@ -241,6 +243,11 @@ def lib() -> ctypes.CDLL:
     L.lora_linear_backward.restype = i32
     L.lora_linear_backward.argtypes = [vp, i64, vp, i64, vp, i64, vp, SP, PP, vp, vp, i64, vp, vp,
                                        i32, vp]
+    L.lora_experts_gemm.restype = i32
+    L.lora_experts_gemm.argtypes = [vp, i64, i32, EP, vp, i64, vp, i64, i32, i32, vp]
+    L.lora_experts_gemm_backward.restype = i32
+    L.lora_experts_gemm_backward.argtypes = [vp, i64, vp, i64, i32, EP, vp, i64, vp, i64, vp, i64,
+                                             i32, i32, i32, i32, vp]
     f64, u32 = ctypes.c_double, ctypes.c_uint32
     AP = ctypes.POINTER(LoraAdamwC)
     L.lora_adamw_state_numel.restype = i64
@@ -913,6 +920,65 @@ def lora_experts_combine_backward(dY: torch.Tensor, Ys: Optional[torch.Tensor],
         _ptr(dY), _ld(dY), _ptr(Ys), 0 if Ys is None else _ld(Ys), _ptr(weights), ex.c, d,
         _dtype_code(dY.dtype), _ptr(dYs), 0 if dYs is None else _ld(dYs), _ptr(d_weights),
         st))
+
+
+def _expert_matrices(ex: Experts, t: torch.Tensor, d_in: int, d_out: int, what: str) -> int:
+    """Elements a row of the experts' matrices t [n_experts, d_out, d_in], checked."""
+    if t.shape != (ex.n_experts, d_out, d_in):
+        raise ValueError(f"{what} [n_experts, d_out, d_in]")
+    e, ld, one = t.stride()
+    if one != 1 or (ex.n_experts > 1 and e != d_out * ld):
+        raise ValueError(f"{what}: row-major matrices, one after the other")
+    return ld
+
+
+def lora_experts_gemm(X: torch.Tensor, ex: Experts, W: torch.Tensor, Y: torch.Tensor,
+                      gathered: bool = True, stream=None) -> None:
+    """The experts' products Y[p] = X[row of p] W[e]^T over every expert's sorted
+    rows, bf16, with W [n_experts, d_out, d_in].  gathered: X holds token rows, read
+    through sorted_choice; otherwise X is in sorted order already."""
+    if not (X.dtype == W.dtype == Y.dtype == torch.bfloat16):
+        raise ValueError("X, W and Y must be bf16")
+    d_in, d_out = X.shape[-1], Y.shape[-1]
+    ldw = _expert_matrices(ex, W, d_in, d_out, "W")
+    choices = ex.n_tokens * ex.top_k
+    if X.shape != (ex.n_tokens if gathered else choices, d_in) or Y.shape != (choices, d_out):
+        raise ValueError("shapes: X [rows, d_in], Y [n_tokens * top_k, d_out]")
+    st = _launch_stream(stream, X, W, Y, ex.expert_offsets)
+    _check(lib().lora_experts_gemm(_ptr(X), _ld(X), 1 if gathered else 0, ex.c, _ptr(W), ldw, _ptr(Y),
+                                   _ld(Y), d_in, d_out, st))
+
+
+def lora_experts_gemm_backward(dY: torch.Tensor, X: Optional[torch.Tensor], ex: Experts,
+                               W: Optional[torch.Tensor], dXs: Optional[torch.Tensor],
+                               dW: Optional[torch.Tensor], gathered: bool = True,
+                               accumulate: bool = False, stream=None) -> None:
+    """Gradients of lora_experts_gemm from dY [n_tokens * top_k, d_out]: dXs[p] =
+    dY[p] W[e], in sorted order (a gathered X's gradient is its lora_experts_combine
+    with weights None), and dW[e] = sum dY[p]^T X[row of p], bf16 or float32, which
+    accumulate adds to.  None leaves dXs (and W) or dW (and X) out."""
+    if dXs is None and dW is None:
+        raise ValueError("dXs or dW")
+    if (dXs is not None and W is None) or (dW is not None and X is None):
+        raise ValueError("dXs needs W, dW needs X")
+    X, W = (X if dW is not None else None), (W if dXs is not None else None)
+    for t in (dY, X, W, dXs):
+        if t is not None and t.dtype != torch.bfloat16:
+            raise ValueError("dY, X, W and dXs must be bf16")
+    d_out, d_in = dY.shape[-1], (dXs if dXs is not None else dW).shape[-1]
+    choices = ex.n_tokens * ex.top_k
+    rows = ex.n_tokens if gathered else choices
+    if dY.shape != (choices, d_out) or (X is not None and X.shape != (rows, d_in)) \
+            or (dXs is not None and dXs.shape != (choices, d_in)):
+        raise ValueError("shapes: dY [n_tokens * top_k, d_out], X [rows, d_in], "
+                         "dXs [n_tokens * top_k, d_in]")
+    ldw = 0 if W is None else _expert_matrices(ex, W, d_in, d_out, "W")
+    lddw = 0 if dW is None else _expert_matrices(ex, dW, d_in, d_out, "dW")
+    st = _launch_stream(stream, dY, X, W, dXs, dW, ex.expert_offsets)
+    _check(lib().lora_experts_gemm_backward(
+        _ptr(dY), _ld(dY), _ptr(X), 0 if X is None else _ld(X), 1 if gathered else 0, ex.c, _ptr(W),
+        ldw, _ptr(dXs), 0 if dXs is None else _ld(dXs), _ptr(dW), lddw,
+        0 if dW is None else _dtype_code(dW.dtype), 1 if accumulate else 0, d_in, d_out, st))
 
 
 def lora_experts_gemm_mxfp4w(X: torch.Tensor, ex: Experts, Wq: torch.Tensor,

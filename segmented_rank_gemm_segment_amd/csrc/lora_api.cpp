@@ -118,6 +118,17 @@ lora_status check_fp8_weight(const void *Wq, int64_t ldw, const float *w_scale, 
   return LORA_OK;
 }
 
+lora_status check_expert_product(int32_t d_in, int32_t d_out) {
+  if (d_in <= 0 || d_out <= 0) return LORA_ERR_SHAPE;
+  return d_in % 8 || d_out % 8 ? LORA_ERR_ALIGN : LORA_OK;
+}
+
+// Weights (or their gradients) `stride` elements from an expert's to the next one's.
+lora::ExpertView expert_view(const lora_experts *ex, int32_t gathered, int64_t stride) {
+  return lora::ExpertView{ex->n_tokens * ex->top_k, ex->top_k, ex->n_experts, ex->expert_offsets,
+                          gathered ? ex->sorted_choice : nullptr, stride, 0};
+}
+
 lora_status hip_status(hipError_t e) { return e == hipSuccess ? LORA_OK : LORA_ERR_HIP; }
 
 }  // namespace
@@ -690,6 +701,61 @@ lora_status lora_experts_gemm_mxfp4w(const void *X, int64_t ldx, int32_t gathere
                             (int64_t)d_out * ldws};
   return hip_status(lora::launch_experts_gemm_mx(X, ldx, ev, Wq, ldw, mx, Y, ldy, d_in, d_out,
                                                  static_cast<hipStream_t>(stream)));
+}
+
+lora_status lora_experts_gemm(const void *X, int64_t ldx, int32_t gathered,
+                              const lora_experts *ex, const void *W, int64_t ldw, void *Y,
+                              int64_t ldy, int32_t d_in, int32_t d_out, void *stream) {
+  lora_status st = check_experts(ex);
+  if (st != LORA_OK) return st;
+  st = check_expert_product(d_in, d_out);
+  if (st != LORA_OK) return st;
+  st = check_matrix(W, ldw, d_in, d_out);
+  if (st != LORA_OK) return st;
+  st = check_matrix(X, ldx, d_in, ex->n_tokens);
+  if (st != LORA_OK) return st;
+  st = check_matrix(Y, ldy, d_out, ex->n_tokens);
+  if (st != LORA_OK || ex->n_tokens == 0) return st;
+  return hip_status(lora::launch_experts_gemm(X, ldx, expert_view(ex, gathered, d_out * ldw), W, ldw,
+                                              Y, ldy, d_in, d_out,
+                                              static_cast<hipStream_t>(stream)));
+}
+
+lora_status lora_experts_gemm_backward(const void *dY, int64_t lddy, const void *X, int64_t ldx,
+                                       int32_t gathered, const lora_experts *ex, const void *W,
+                                       int64_t ldw, void *dXs, int64_t lddxs, void *dW,
+                                       int64_t lddw, int32_t dw_dtype, int32_t accumulate,
+                                       int32_t d_in, int32_t d_out, void *stream) {
+  lora_status st = check_experts(ex);
+  if (st != LORA_OK) return st;
+  st = check_expert_product(d_in, d_out);
+  if (st != LORA_OK) return st;
+  if (!dXs && !dW) return LORA_ERR_NULL;
+  if (dW && !valid_dtype(dw_dtype)) return LORA_ERR_DTYPE;
+  st = check_matrix(dY, lddy, d_out, ex->n_tokens);
+  if (st != LORA_OK) return st;
+  if (dXs) {
+    st = check_matrix(W, ldw, d_in, d_out);
+    if (st != LORA_OK) return st;
+    st = check_matrix(dXs, lddxs, d_in, ex->n_tokens);
+    if (st != LORA_OK) return st;
+  }
+  if (dW) {
+    st = check_matrix(dW, lddw, d_in, d_out);
+    if (st != LORA_OK) return st;
+    st = check_matrix(X, ldx, d_in, ex->n_tokens);
+    if (st != LORA_OK) return st;
+  }
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  hipError_t e = hipSuccess;
+  // (without tokens there are no rows to write, but weights' gradients of zeros)
+  if (dXs && ex->n_tokens > 0)
+    e = lora::launch_experts_gemm_rows(dY, lddy, expert_view(ex, 0, d_out * ldw), W, ldw, dXs, lddxs,
+                                       d_out, d_in, s);
+  if (dW && e == hipSuccess)
+    e = lora::launch_experts_gemm_weights(dY, lddy, X, ldx, expert_view(ex, gathered, d_out * lddw), dW,
+                                          lddw, dw_dtype, accumulate != 0, d_out, d_in, s);
+  return hip_status(e);
 }
 
 lora_status lora_linear_fused_static(const int32_t *row_slot, const void *X, int64_t ldx,

@@ -148,6 +148,18 @@ hipError_t launch_experts_gemm_mx(const void *X, int64_t ldx, const ExpertView &
                                   int64_t ldw, const MxScales &mx, void *Y, int64_t ldy, int K,
                                   int N, hipStream_t stream);
 
+// The experts' products on bf16 weights [n_experts][N or K][ldw], w_stride elements
+// apart: Y[p] = X[row of p] W_e^T (K = d_in, N = d_out), dX[p] = dY[p] W_e (K = d_out,
+// N = d_in), and dW_e (+)= sum_p dY[p]^T X[row of p] (M = d_out, N = d_in).
+hipError_t launch_experts_gemm(const void *X, int64_t ldx, const ExpertView &ex, const void *W,
+                               int64_t ldw, void *Y, int64_t ldy, int K, int N, hipStream_t stream);
+hipError_t launch_experts_gemm_rows(const void *dY, int64_t lddy, const ExpertView &ex,
+                                    const void *W, int64_t ldw, void *dX, int64_t lddx, int K,
+                                    int N, hipStream_t stream);
+hipError_t launch_experts_gemm_weights(const void *dY, int64_t lddy, const void *X, int64_t ldx,
+                                       const ExpertView &ex, void *dW, int64_t lddw, int dtype,
+                                       bool accumulate, int M, int N, hipStream_t stream);
+
 // MXFP4 codes and scales (ldq and lds bytes a row) of rows of d values, and back.
 hipError_t launch_mx_quantize(const void *X, int64_t ldx, int n, int d, int dtype, void *q,
                               int64_t ldq, void *s, int64_t lds, hipStream_t stream);
