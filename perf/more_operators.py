@@ -262,8 +262,12 @@ def prepare(case, seed):
         if case["op"] == "adapters":
             s["pool"] = srg.Pool(s["A"], s["Bt"], s["rank"], ALPHA)
             s["seg"] = srg.Segments(case["n"], case["slots"], DEV)
+            if case["acc"]:
+                s["sums"] = {k: torch.empty_like(s[k]) for k in ("dA", "dBt")}
         elif case["op"] == "experts":
             s["ex"] = srg.Experts(case["n"], case["top_k"], case["experts"], DEV)
+            if case["back"] and case["acc"]:
+                s["sums"] = {"dW": torch.empty_like(s["dW"])}
         else:
             def parts(buf):
                 return [buf[a:a + n] for a, n in zip(s["starts"], s["sizes"])]
@@ -458,14 +462,21 @@ def _plain_adamw(s):
 # ---------------------------------------------------------------------------
 # one pass
 # ---------------------------------------------------------------------------
+def _into(s, name):
+    """The buffer of a gradient.  One that is added to starts each pass from the
+    earlier part's gradient, which the pass leaves as it is."""
+    return s["sums"][name].copy_(s[name]) if s["acc"] else s[name]
+
+
 def _own(s):
     import segmented_rank_gemm_segment_amd as srg
     op = s["op"]
     if op == "adapters":
+        dA, dBt = _into(s, "dA"), _into(s, "dBt")
         srg.lora_build_segments(s["slot"], s["pool"], s["seg"])
         srg.lora_linear_backward(s["dY"], s.get("Wt"), s["X"], s["H"], s["seg"], s["pool"],
-                                 s["dH"], s.get("dX"), s["dA"], s["dBt"], accumulate=s["acc"])
-        out = {"dH": s["dH"], "dA": s["dA"], "dBt": s["dBt"]}
+                                 s["dH"], s.get("dX"), dA, dBt, accumulate=s["acc"])
+        out = {"dH": s["dH"], "dA": dA, "dBt": dBt}
         if s["dx"]:
             out["dX"] = s["dX"]
         return out
@@ -475,9 +486,10 @@ def _own(s):
         if not s["back"]:
             srg.lora_experts_gemm(s["X"], ex, s["W"], s["Y"], gathered=s["gathered"])
             return {"offsets": ex.expert_offsets, "Y": s["Y"]}
-        srg.lora_experts_gemm_backward(s["dY"], s["X"], ex, s["W"], s["dXs"], s["dW"],
+        dW = _into(s, "dW")
+        srg.lora_experts_gemm_backward(s["dY"], s["X"], ex, s["W"], s["dXs"], dW,
                                        gathered=s["gathered"], accumulate=s["acc"])
-        return {"offsets": ex.expert_offsets, "dXs": s["dXs"], "dW": s["dW"]}
+        return {"offsets": ex.expert_offsets, "dXs": s["dXs"], "dW": dW}
     opt = s["opt"]
     srg.lora_adamw_step(opt, LR, BETA1, BETA2, EPS, DECAY, active=s["active"], seed=SEED)
     out = {"p": s["p"], "step": opt.step}
