@@ -354,8 +354,7 @@ lora_status lora_linear_fused(const void *X, int64_t ldx, const void *W, int64_t
  *   dBt[a][k]  = s_a sum_{i in a} H[i][k] dY[i]       fp32 [n_slots][r_max][d_out]
  * for k < r, sums in fp32 in a fixed order; with accumulate other than 0 the sums
  * are added to dA and dBt.  Rank rows past r, slots without rows, and dH of rows
- * without an adapter are left as they are.  (bf16 pools: H and dH enter dA's and
- * dBt's products with 16 significant bits.)
+ * without an adapter are left as they are. 
  * Wt is the base weight's transpose, [d_in][d_out]: laid out once, as the weight
  * does not change.  H and seg are the forward pass's.  dX may be NULL (an input
  * without gradient; Wt is then unused), and dA (X unused) or dBt (H unused).

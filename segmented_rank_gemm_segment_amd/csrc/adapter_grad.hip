@@ -15,8 +15,9 @@
 // holds 256 columns, and in its accumulators a lane has 8 neighbouring columns of a
 // rank row, stored as 32 bytes.
 //
-// V is fp32 and is split into a bf16 and the bf16 of what is left, 16 significant
-// bits; both are multiplied.  fp32 pools go through the fp32 matrix instruction.
+// V is fp32 and is split into three bf16, each the rounding of what the ones before
+// leave, which hold its 24 significant bits; each is multiplied (with two, 16 bits, the
+// gradients were 2.4e-6 off where fp32 sums are 3e-7).  fp32 pools go through the fp32 matrix instruction.
 //
 // A segment of up to kRows rows is one step: each wave of the workgroup takes other
 // columns.  In a longer one the four waves take every fourth step of the same columns
@@ -128,19 +129,19 @@ __global__ __launch_bounds__(kWaves *kWave, RB == 1 ? 2 : 1) void adapter_grad_k
 #pragma unroll
       for (int b = 0; b < RB; ++b) {
         if (b * 32 >= r) break;
-        u32x4 hi, lo;
 #pragma unroll
-        for (int p = 0; p < 4; ++p) {
-          const float x = s.v[b][2 * p], y = s.v[b][2 * p + 1];
-          hi[p] = pack_bf16x2(x, y);
-          lo[p] = pack_bf16x2(x - bf16_lo(hi[p]), y - bf16_hi(hi[p]));
+        for (int part = 0; part < 3; ++part) {
+          u32x4 x;
+#pragma unroll
+          for (int p = 0; p < 4; ++p) {
+            x[p] = pack_bf16x2(s.v[b][2 * p], s.v[b][2 * p + 1]);
+            s.v[b][2 * p] -= bf16_lo(x[p]);         // exact: what is left for the next part
+            s.v[b][2 * p + 1] -= bf16_hi(x[p]);
+          }
+#pragma unroll
+          for (int j = 0; j < VEC; ++j)
+            acc[b][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(x), col8[j], acc[b][j], 0, 0, 0);
         }
-#pragma unroll
-        for (int j = 0; j < VEC; ++j)
-          acc[b][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(hi), col8[j], acc[b][j], 0, 0, 0);
-#pragma unroll
-        for (int j = 0; j < VEC; ++j)
-          acc[b][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(lo), col8[j], acc[b][j], 0, 0, 0);
       }
     } else {
 #pragma unroll
