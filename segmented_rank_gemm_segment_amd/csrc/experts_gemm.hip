@@ -15,6 +15,8 @@
 //
 // Workgroups are persistent and each XCD walks its own part of the tiles: the loads
 // of a tile's first stages go out under the products of the one before.
+#include <type_traits>
+
 #include "lds_dma.cuh"
 #include "lora_device.cuh"
 #include "lora_kernels.h"
@@ -68,22 +70,23 @@ struct Operand {
   __device__ static __forceinline__ int chunk(int wid, int i, int l) {
     return ((l % LPR) ^ swz(row(wid, i, l))) * 8;
   }
-  // Where lane l reads in a stage: fragment i holds rows or columns [i0 + 32 i, +32) of
-  // the operand, its sub-step kk 16 k.  Along K fragments are 32 rows apart and sub-steps
-  // two XORed chunks; else a fragment's columns are XORed and sub-steps are 16 rows apart.
-  template <int F> struct Reader {
+  // Where lane l reads in a stage: of W waves, wave w's fragment i holds rows or columns
+  // 32 (w F + i) and on of the operand, its sub-step kk 16 k.  Along K sub-steps are two
+  // XORed chunks; else a fragment's columns are XORed and sub-steps are 16 rows apart.
+  template <int W> struct Reader {
+    static constexpr int F = B / 32 / W;
     static constexpr int ROWS = ALONG_K ? 1 : F, SUBS = ALONG_K ? 4 : 1;
     int at[ROWS], sub[SUBS];
-    __device__ __forceinline__ void init(int i0, int l) {
+    __device__ __forceinline__ void init(int w, int l) {
       if constexpr (ALONG_K) {
-        at[0] = (i0 + (l & 31)) * RB;
+        at[0] = (w * F * 32 + (l & 31)) * RB;
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) sub[kk] = ((kk * 2 + (l >> 5)) ^ swz(l & 31)) * 16;
       } else {
         const int t = l & 15, k = (l >> 5) * 8 + (t >> 2);
 #pragma unroll
         for (int i = 0; i < F; ++i)
-          at[i] = k * RB + (((i0 + i * 32) / 8 + ((l >> 4) & 1) * 2 + ((t & 3) >> 1)) ^ swz(k)) * 16 + (t & 1) * 8;
+          at[i] = k * RB + (((w * F + i) * 4 + ((l >> 4) & 1) * 2 + ((t & 3) >> 1)) ^ swz(k)) * 16 + (t & 1) * 8;
       }
     }
     __device__ __forceinline__ mfma_bf16x8 read(const unsigned char *st, int i, int kk) const {
@@ -99,14 +102,15 @@ struct Operand {
 template <int FORM, int BM, int BN, int WM, int WN, int PER_CU, bool TAIL, bool F32OUT>
 __global__ __launch_bounds__(WM *WN *kWave, WM *WN *PER_CU / 4) void experts_gemm_kernel(ExpertGemmArgs g) {
   constexpr int NW = WM * WN, T = NW * kWave;
-  constexpr int TM = BM / WM, TN = BN / WN, FM = TM / 32, FN = TN / 32;
+  constexpr int FM = BM / WM / 32, FN = BN / WN / 32;
   using OP = Operand<BM, FORM != kWeights, NW>;
   using OQ = Operand<BN, FORM == kForward, NW>;
   constexpr int STAGE = OP::BYTES + OQ::BYTES;
-  constexpr int TAB = 4 * (LORA_MAX_EXPERTS + 1);
-  static_assert((2 * STAGE + TAB) * PER_CU <= 160 * 1024, "LDS");
+  constexpr int TAB = (4 * (LORA_MAX_EXPERTS + 1) + 15) / 16 * 16;
+  constexpr int SMEM = 2 * STAGE + TAB + NW * 2048;
+  static_assert(SMEM * PER_CU <= 160 * 1024, "LDS");
   static_assert(FORM == kWeights || !F32OUT, "rows are bf16");
-  __shared__ __align__(16) unsigned char smem[2 * STAGE + TAB];
+  __shared__ __align__(16) unsigned char smem[SMEM];
   int *const tab = reinterpret_cast<int *>(smem + 2 * STAGE);
 
   const int tid = threadIdx.x, l = tid & (kWave - 1);
@@ -190,8 +194,9 @@ __global__ __launch_bounds__(WM *WN *kWave, WM *WN *PER_CU / 4) void experts_gem
       x.e = uniform(t / tiles_w);
       tile_at(t - x.e * tiles_w, tiles_w / tiles_n, tiles_n, mi, ni);
     } else {
-      tile_at(t, all, tiles_n, mi, ni);
-      x.e = find(uniform(mi));
+      x.e = find(uniform(t / tiles_n));
+      const int first = uniform(tab[x.e]);
+      tile_at(t - first * tiles_n, uniform(tab[x.e + 1]) - first, tiles_n, mi, ni);
     }
     mi = uniform(mi);
     x.r0 = uniform(g.off[x.e]);
@@ -203,7 +208,7 @@ __global__ __launch_bounds__(WM *WN *kWave, WM *WN *PER_CU / 4) void experts_gem
       x.k_end = x.r1 - x.r0;
       x.stages = max(1, (x.k_end + 63) / 64);       // (no rows: a stage of zeros)
     } else {
-      x.m0 = x.r0 + (mi - uniform(tab[x.e])) * BM;
+      x.m0 = x.r0 + mi * BM;
       x.m_end = x.r1;
       x.k_end = g.K;
       x.stages = (g.K + 63) / 64;
@@ -353,10 +358,10 @@ __global__ __launch_bounds__(WM *WN *kWave, WM *WN *PER_CU / 4) void experts_gem
     advance();
   };
 
-  typename OP::template Reader<FM> pr;
-  typename OQ::template Reader<FN> qr;
-  pr.init(wm * TM, l);
-  qr.init(wn * TN, l);
+  typename OP::template Reader<WM> pr;
+  typename OQ::template Reader<WN> qr;
+  pr.init(wm, l);
+  qr.init(wn, l);
 
   f32x16 acc[FN][FM];
   mfma_bf16x8 pf[2][FM], qf[2][FN];
@@ -387,7 +392,7 @@ __global__ __launch_bounds__(WM *WN *kWave, WM *WN *PER_CU / 4) void experts_gem
   aim(t);
   issue();
   Tile x = tile_of(t);                              // the tile being computed
-  int kt = 0, b = 0;
+  int b = 0;
   vm_wait<0>();                                     // the first stage has landed
   if (TAIL && x.k_end < 64) zero_tail(x, 0, 0);
   lgkm_barrier();
@@ -396,92 +401,107 @@ __global__ __launch_bounds__(WM *WN *kWave, WM *WN *PER_CU / 4) void experts_gem
   for (int q = 0; q < FM + FN; ++q) read(0, q, smem, 0);
   zero_acc();
   constexpr int NM = FM * FN, NR = FM + FN, NL = OP::I + OQ::I;
+  // Sub-step kk's products with the reads of the next one's fragments from st, and the
+  // loads of the next stage but one where LOAD.
+  auto sub_step = [&](auto load, int kk, const unsigned char *st) __attribute__((always_inline)) {
+    constexpr bool LOAD = decltype(load)::value;
+    constexpr int STEPS = NM > NR ? (NM > NL || !LOAD ? NM : NL) : (NR > NL || !LOAD ? NR : NL);
+#pragma unroll
+    for (int q = 0; q < STEPS; ++q) {
+      if (q < NM)
+        acc[q / FM][q % FM] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+            qf[kk & 1][q / FM], pf[kk & 1][q % FM], acc[q / FM][q % FM], 0, 0, 0);
+      if (q < NR) read((kk + 1) & 1, q, st, (kk + 1) & 3);
+      if constexpr (LOAD) {
+        if (q < OP::I) issue_p(q);
+        else if (q < NL) issue_q(q - OP::I);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  int kt = 0;
   while (true) {
     const unsigned char *st = smem + b * STAGE;
 #pragma unroll
-    for (int kk = 0; kk < 3; ++kk)
-#pragma unroll
-      for (int q = 0; q < (NM > NR ? NM : NR); ++q) {
-        if (q < NM)
-          acc[q / FM][q % FM] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-              qf[kk & 1][q / FM], pf[kk & 1][q % FM], acc[q / FM][q % FM], 0, 0, 0);
-        if (q < NR) read((kk + 1) & 1, q, st, kk + 1);
-        __builtin_amdgcn_sched_barrier(0);
-      }
+    for (int kk = 0; kk < 3; ++kk) sub_step(std::false_type{}, kk, st);
     const bool last = kt + 1 == x.stages;
     const Tile done = x;
     if (last && t + stride < t_end) x = tile_of(t + stride);
-    const int kn = last ? 0 : kt + 1;               // the next stage, of x
+    kt = last ? 0 : kt + 1;                         // the next stage, of x
     pin();
     vm_wait<0>();                                   // it has landed
-    if (TAIL && (kn + 1) * 64 > x.k_end) zero_tail(x, kn, b ^ 1);
+    if (TAIL && (kt + 1) * 64 > x.k_end) zero_tail(x, kt, b ^ 1);
     pin();
     lgkm_barrier();                                 // it is there, and this one has been read
-    const unsigned char *sn = smem + (b ^ 1) * STAGE;
-#pragma unroll
-    for (int q = 0; q < (NM > NR ? (NM > NL ? NM : NL) : (NR > NL ? NR : NL)); ++q) {
-      if (q < NM)
-        acc[q / FM][q % FM] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-            qf[1][q / FM], pf[1][q % FM], acc[q / FM][q % FM], 0, 0, 0);
-      if (q < NR) read(0, q, sn, 0);
-      if (q < OP::I) issue_p(q);
-      else if (q < NL) issue_q(q - OP::I);
-      __builtin_amdgcn_sched_barrier(0);
-    }
+    sub_step(std::true_type{}, 3, smem + (b ^ 1) * STAGE);
     pin();
     advance();
     b ^= 1;
-    if (!last) {
-      ++kt;
-      continue;
-    }
-    kt = 0;
-    // lane l has row wm TM + 32 i + l % 32 of the tile and, of each 32 columns,
-    // [8 v + 4 (l / 32), +4) in accumulator entries [4 v, 4 v + 4)
+    if (!last) continue;
+
+    // Lane l has row l % 32 of a fragment and, of its 32 columns, [8 v + 4 (l / 32), +4) in
+    // accumulator entries [4 v, 4 v + 4).  The fragments leave by way of 2 KB of LDS a
+    // wave, 64 bytes of 32 rows at a time, so that four lanes write 64 bytes of a row
+    // (16 bytes of a row a lane: 64 x 1024 rows, 2048 -> 1536 in 378 us where it is now
+    // OUTUS; without any stores it would be 330).
+    unsigned char *const out = smem + 2 * STAGE + TAB + wid * 2048;
+    const int wr = (l & 31) * 64, ws = (l >> 2) & 3;          // the lane's row, its chunks' XOR
+    const int rr = l >> 2, rc = ((l & 3) ^ (rr >> 2 & 3)) * 16;   // the row and chunk it stores
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
-      const int row = done.m0 + wm * TM + i * 32 + (l & 31);
-      const int64_t at = (FORM == kWeights ? done.e * g.w_stride : 0) + (int64_t)row * g.ldo;
 #pragma unroll
       for (int j = 0; j < FN; ++j) {
         const f32x16 c = acc[j][i];
-        if constexpr (F32OUT) {
+        const int col0 = done.n0 + (wn * FN + j) * 32;
+        const int row0 = done.m0 + (wm * FM + i) * 32;
+        const int64_t at = FORM == kWeights ? done.e * g.w_stride : 0;
+        if (!F32OUT && !(FORM == kWeights && g.accumulate)) {
 #pragma unroll
-          for (int v = 0; v < 4; ++v) {
-            const int col = done.n0 + wn * TN + j * 32 + v * 8 + (l >> 5) * 4;
-            if (row >= done.m_end || col >= N) continue;
-            float *const y = static_cast<float *>(g.out) + at + col;
-            float o[4] = {c[4 * v], c[4 * v + 1], c[4 * v + 2], c[4 * v + 3]};
-            if (g.accumulate) {
-              float old[4];
-              Elem<float>::unpack(ldg16(y), old);
+          for (int p = 0; p < 2; ++p) {
+            // lower lanes' second quad against upper lanes' first: 8 columns each
+            const uint32_t lo0 = pack_bf16x2(c[8 * p], c[8 * p + 1]), lo1 = pack_bf16x2(c[8 * p + 2], c[8 * p + 3]);
+            const uint32_t hi0 = pack_bf16x2(c[8 * p + 4], c[8 * p + 5]), hi1 = pack_bf16x2(c[8 * p + 6], c[8 * p + 7]);
+            const auto s0 = __builtin_amdgcn_permlane32_swap(lo0, hi0, false, false);
+            const auto s1 = __builtin_amdgcn_permlane32_swap(lo1, hi1, false, false);
+            *reinterpret_cast<u32x4 *>(out + wr + (((p * 2 + (l >> 5)) ^ ws) * 16)) = u32x4{s0[0], s1[0], s0[1], s1[1]};
+          }
+          u32x4 o[2];
 #pragma unroll
-              for (int q = 0; q < 4; ++q) o[q] += old[q];
-            }
-            stg16(y, Elem<float>::pack(o));
+          for (int p = 0; p < 2; ++p)
+            o[p] = *reinterpret_cast<const u32x4 *>(out + (rr + p * 16) * 64 + rc);
+#pragma unroll
+          for (int p = 0; p < 2; ++p) {
+            const int row = row0 + rr + p * 16, col = col0 + (l & 3) * 8;
+            if (row < done.m_end && col < N)                  // N % 8 == 0: all 8 columns or none
+              *reinterpret_cast<u32x4 *>(static_cast<bf16_t *>(g.out) + at + (int64_t)row * g.ldo + col) = o[p];
           }
         } else {
 #pragma unroll
-          for (int p = 0; p < 2; ++p) {
-            const int col = done.n0 + wn * TN + j * 32 + p * 16 + (l >> 5) * 8;
-            const bool in = row < done.m_end && col < N;      // N % 8 == 0: all 8 columns or none
-            bf16_t *const y = static_cast<bf16_t *>(g.out) + at + col;
-            // lower lanes' second quad against upper lanes' first: 8 columns each
-            float o[8];
+          for (int p = 0; p < 2; ++p) {                       // 16 columns in fp32
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const auto s = __builtin_amdgcn_permlane32_swap(
-                  __float_as_uint(c[8 * p + q]), __float_as_uint(c[8 * p + 4 + q]), false, false);
-              o[q] = __uint_as_float(s[0]);
-              o[4 + q] = __uint_as_float(s[1]);
+            for (int v = 0; v < 2; ++v) {
+              const int a = 8 * p + 4 * v;
+              *reinterpret_cast<f32x4 *>(out + wr + (((v * 2 + (l >> 5)) ^ ws) * 16)) = f32x4{c[a], c[a + 1], c[a + 2], c[a + 3]};
             }
-            if (FORM == kWeights && g.accumulate && in) {
-              float old[8];
-              Elem<bf16_t>::unpack(ldg16(y), old);
+            f32x4 o[2];
 #pragma unroll
-              for (int q = 0; q < 8; ++q) o[q] += old[q];
+            for (int q = 0; q < 2; ++q)
+              o[q] = *reinterpret_cast<const f32x4 *>(out + (rr + q * 16) * 64 + rc);
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              const int row = row0 + rr + q * 16, col = col0 + p * 16 + (l & 3) * 4;
+              if (row >= done.m_end || col >= N) continue;
+              if constexpr (F32OUT) {
+                f32x4 *const y = reinterpret_cast<f32x4 *>(static_cast<float *>(g.out) + at + (int64_t)row * g.ldo + col);
+                if (g.accumulate) o[q] += *y;
+                *y = o[q];
+              } else {
+                uint2 *const y = reinterpret_cast<uint2 *>(static_cast<bf16_t *>(g.out) + at + (int64_t)row * g.ldo + col);
+                const uint2 old = *y;
+                *y = make_uint2(pack_bf16x2(o[q][0] + bf16_lo(old.x), o[q][1] + bf16_hi(old.x)),
+                                pack_bf16x2(o[q][2] + bf16_lo(old.y), o[q][3] + bf16_hi(old.y)));
+              }
             }
-            if (in) stg16(y, Elem<bf16_t>::pack(o));
           }
         }
       }
