@@ -14,14 +14,16 @@
 // the last sub-step's products, under which the stage after the next is loaded.
 //
 // Long segments, 256 x 256 tiles: a stage is 64 KB a CU, 128 flops a byte.  16384 rows, 4096
-// -> 14336 in 1455 us (1.32 PFLOP/s; a library's product reaches 1.36 there): its loads
+// -> 14336 in 1435 us (1.34 PFLOP/s; a library's product reaches 1.36 there): its loads
 // alone take 1140 and its products alone, whose power brings the clock down to about 1.5
-// GHz, 1230.  64 experts of 1024 rows, 2048 -> 1536: 376 us (1.10 PFLOP/s); the loads alone
+// GHz, 1230.  64 experts of 1024 rows, 2048 -> 1536: 368 us (1.12 PFLOP/s); the loads alone
 // 326 (10 TB/s from the L2s), the products 280, and 330 without the stores of 200 MB.
 // L2 prefetch of the following stage, a line a lane, took 15% more time; branches that
-// leave out fragments past an expert's last row took more than they saved.
-// Short segments, 32 x 128 tiles, three workgroups a CU: bound by W's bytes.  64 x 8
-// choices on 128 experts of 2048 -> 1536 in 141 us, 5.7 TB/s.
+// leave out fragments past an expert's last row took more than they saved.  (Issue priority
+// past the barrier: 2%.)
+// Short segments: 128 x 128 tiles, two workgroups a CU, or the kernel for few rows below
+// (tile_choice.h), bound by W's bytes.  64 x 8 choices on 128 experts of 2048 -> 1536 in 144
+// to 156 us, 5.2 to 5.6 TB/s; one token's 8 choices in 13.6, half of a copy's rate.
 #include <type_traits>
 
 #include "experts_tiles.cuh"
@@ -234,23 +236,27 @@ __global__ __launch_bounds__(WM *WN *kWave, WM *WN *PER_CU / 4) void experts_gem
 #pragma unroll
   for (int q = 0; q < NR; ++q) read(0, q, smem, 0);
   zero_acc();
+  Tile nx = tile_of(t);
   int kt = 0, b = 0;
   while (true) {
     const unsigned char *st = smem + b * STAGE;
 #pragma unroll
     for (int kk = 0; kk < 3; ++kk) sub_step(std::false_type{}, kk, st);
     const bool last = kt + 1 == stages;
+    const Tile x = nx;
+    if (last && t + stride < t_end) nx = tile_of(t + stride);
     kt = last ? 0 : kt + 1;                         // the next stage
     pin();
     vm_wait<0>();                                   // it has landed
     if (TAIL && kt + 1 == stages) zero_tail(kt, b ^ 1);
     lgkm_barrier();                                 // it is there, and this one has been read
+    __builtin_amdgcn_s_setprio(1);
     sub_step(std::true_type{}, 3, smem + (b ^ 1) * STAGE);
+    __builtin_amdgcn_s_setprio(0);
     pin();
     advance();
     b ^= 1;
     if (!last) continue;
-    const Tile x = tile_of(t);
 #pragma unroll
     for (int i = 0; i < FM; ++i)
 #pragma unroll
@@ -268,6 +274,143 @@ __global__ __launch_bounds__(WM *WN *kWave, WM *WN *PER_CU / 4) void experts_gem
   vm_wait<0>();                                     // no load outlives the workgroup's LDS
 }
 
+// A batch of few rows has few tiles, and a CU that streams a tile's W by itself waits for
+// memory most of the time: 32 x BN tiles whose K goes round over the workgroup's waves in
+// stages of 64, each wave with two buffers of its own.  A wave waits for all of its loads,
+// sends out its next stage's and multiplies the one that has landed; the waves' sums are
+// added through LDS in their order.
+constexpr int kFewWaves = 4;
+template <int FORM, int BN, int PER_CU, bool TAIL>
+__global__ __launch_bounds__(kFewWaves *kWave, PER_CU) void experts_few_kernel(ExpertGemmArgs g) {
+  constexpr int BM = 32, FN = BN / 32, T = kFewWaves * kWave;
+  using OP = StageLoads<BM, true, 1>;
+  using OQ = StageLoads<BN, FORM == kForward, 1>;
+  constexpr int STAGE = OP::BYTES + OQ::BYTES;
+  constexpr int RING = kFewWaves * 2 * STAGE;
+  static_assert((RING + kExpertTab) * PER_CU <= 160 * 1024, "LDS");
+  static_assert(kFewWaves * FN * 16 * kWave * 4 + kFewWaves * 2048 <= RING && FN <= kFewWaves, "sums");
+  __shared__ __align__(16) unsigned char smem[RING + kExpertTab];
+  int *const tab = reinterpret_cast<int *>(smem + RING);
+  const int l = threadIdx.x & (kWave - 1), w = scalar_int(threadIdx.x / kWave);
+  const int E = g.n_experts, N = g.N, K = g.K;
+  const int tiles_n = (N + BN - 1) / BN, stages = (K + 63) / 64;
+  expert_table<T>(E, tab, reinterpret_cast<int *>(smem),
+                  [&](int e) { return (g.off[e + 1] - g.off[e] + BM - 1) / BM; });
+  const int tiles = scalar_int(tab[E]) * tiles_n;
+  unsigned char *const mine = smem + w * 2 * STAGE;
+  const uint32_t dst = scalar_int(lds_offset(mine));
+  FragmentReader<BM, true, 1> pr;
+  FragmentReader<BN, FORM == kForward, 1> qr;
+  pr.init(0, l);
+  qr.init(0, l);
+
+  for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
+    const int e = expert_find(tab, E, scalar_int(t / tiles_n));
+    const int first = scalar_int(tab[e]) * tiles_n;
+    const int m0 = scalar_int(g.off[e]) + scalar_int((t - first) / tiles_n) * BM;
+    const int n0 = scalar_int((t - first) % tiles_n) * BN, m_end = scalar_int(g.off[e + 1]);
+    // where past an end something valid is read instead, as in the larger tiles
+    const bf16_t *const we = g.Q + e * g.w_stride;
+    const unsigned char *const qbase = scalar_ptr(FORM == kForward ? we + (int64_t)n0 * g.ldq : we + n0);
+    const unsigned char *prow[OP::I];
+    uint32_t qoff[OQ::I];
+#pragma unroll
+    for (int i = 0; i < OP::I; ++i) {
+      const int p = min(m0 + OP::row(0, i, l), m_end - 1);
+      const int row = FORM == kForward && g.sorted ? token_of(g, g.sorted[p]) : p;
+      prow[i] = reinterpret_cast<const unsigned char *>(g.P + (int64_t)row * g.ldp + OP::chunk(0, i, l));
+    }
+#pragma unroll
+    for (int i = 0; i < OQ::I; ++i) {
+      const int c = OQ::chunk(0, i, l), r = OQ::row(0, i, l);
+      if constexpr (FORM == kForward)
+        qoff[i] = ((uint32_t)min(r, N - 1 - n0) * (uint32_t)g.ldq + (uint32_t)c) * 2u;
+      else
+        qoff[i] = ((uint32_t)r * (uint32_t)g.ldq + (uint32_t)(n0 + c < N ? c : 0)) * 2u;
+    }
+    auto issue = [&](int s, int b) __attribute__((always_inline)) {
+      const uint32_t d = scalar_int(dst + b * STAGE);
+      const unsigned char *const q = scalar_ptr(qbase + (int64_t)s * (FORM == kForward ? 128 : 128 * g.ldq));
+#pragma unroll
+      for (int i = 0; i < OP::I; ++i) {
+        const int c = OP::chunk(0, i, l);
+        dma16(d, i * 1024, prow[i] + (TAIL && s * 64 + c >= K ? s * 128 - c * 2 : s * 128));
+      }
+#pragma unroll
+      for (int i = 0; i < OQ::I; ++i) {
+        const int c = OQ::chunk(0, i, l), r = OQ::row(0, i, l);
+        const uint32_t back = !TAIL                ? 0u
+                              : FORM == kForward   ? (s * 64 + c >= K ? c * 2u : 0u)
+                              : s * 64 + r >= K    ? (uint32_t)r * (uint32_t)g.ldq * 2u
+                                                   : 0u;
+        dma16_s(d, OP::BYTES + i * 1024, qoff[i] - back, q);
+      }
+    };
+    f32x16 acc[FN];
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) acc[j][v] = 0.f;
+    int b = 0;
+    if (w < stages) issue(w, 0);
+    for (int s = w; s < stages; s += kFewWaves) {
+      vm_wait<0>();                                 // stage s has landed
+      unsigned char *const st = mine + b * STAGE;
+      if (TAIL && s + 1 == stages) {
+        const u32x4 z = {0, 0, 0, 0};
+#pragma unroll
+        for (int i = 0; i < OP::I; ++i)
+          if (s * 64 + OP::chunk(0, i, l) >= K) *reinterpret_cast<u32x4 *>(st + i * 1024 + l * 16) = z;
+#pragma unroll
+        for (int i = 0; i < OQ::I; ++i)
+          if (s * 64 + (FORM == kForward ? OQ::chunk(0, i, l) : OQ::row(0, i, l)) >= K)
+            *reinterpret_cast<u32x4 *>(st + OP::BYTES + i * 1024 + l * 16) = z;
+      }
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the other buffer has been read
+      if (s + kFewWaves < stages) issue(s + kFewWaves, b ^ 1);
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk) {
+        const mfma_bf16x8 p = pr.read(st, 0, kk);
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+          acc[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(qr.read(st + OP::BYTES, j, kk), p, acc[j], 0, 0, 0);
+      }
+      b ^= 1;
+    }
+    __syncthreads();                                // the rings are free
+    f32x4 *const sums = reinterpret_cast<f32x4 *>(smem);
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+#pragma unroll
+      for (int v = 0; v < 4; ++v)
+        sums[((w * FN + j) * 4 + v) * kWave + l] = f32x4{acc[j][4 * v], acc[j][4 * v + 1], acc[j][4 * v + 2], acc[j][4 * v + 3]};
+    __syncthreads();
+    if (w < FN) {
+      f32x16 c;
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        f32x4 x = sums[(w * 4 + v) * kWave + l];
+#pragma unroll
+        for (int o = 1; o < kFewWaves; ++o) x += sums[((o * FN + w) * 4 + v) * kWave + l];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) c[4 * v + q] = x[q];
+      }
+      store_fragment<false, false>(smem + kFewWaves * FN * 16 * kWave * 4 + w * 2048, c, l,
+                                   static_cast<bf16_t *>(g.out) + (int64_t)m0 * g.ldo + n0 + w * 32, g.ldo,
+                                   m_end - m0, N - n0 - w * 32, false);
+    }
+    __syncthreads();                                // and again
+  }
+}
+
+template <int FORM, int BN, int PER_CU> void launch_few(const ExpertGemmArgs &g, hipStream_t stream) {
+  const dim3 grid(kCUs * PER_CU), block(kFewWaves * kWave);
+  if (g.K % 64 == 0)
+    hipLaunchKernelGGL((experts_few_kernel<FORM, BN, PER_CU, false>), grid, block, 0, stream, g);
+  else
+    hipLaunchKernelGGL((experts_few_kernel<FORM, BN, PER_CU, true>), grid, block, 0, stream, g);
+}
+
 template <int FORM, int BM, int BN, int WM, int WN, int PER_CU>
 void launch_tiles(const ExpertGemmArgs &g, hipStream_t stream) {
   const dim3 grid(kCUs * PER_CU), block(WM * WN * kWave);
@@ -277,13 +420,12 @@ void launch_tiles(const ExpertGemmArgs &g, hipStream_t stream) {
     hipLaunchKernelGGL((experts_gemm_kernel<FORM, BM, BN, WM, WN, PER_CU, true>), grid, block, 0, stream, g);
 }
 
-// Mean rows of an expert from which the 256 x 256 tiles are taken.
-constexpr int kLargeRows = 64;
 template <int FORM> hipError_t launch_rows(const ExpertGemmArgs &g, hipStream_t stream) {
-  if (g.n_choices / g.n_experts < kLargeRows)
-    launch_tiles<FORM, 32, 128, 1, 4, 3>(g, stream);
-  else
-    launch_tiles<FORM, 256, 256, 2, 4, 1>(g, stream);
+  switch (experts_kernel_of(g.n_choices, g.n_experts, g.K, g.N, FORM == kForward)) {
+    case kExpertsFew: launch_few<FORM, 64, 1>(g, stream); break;
+    case kExpertsMid: launch_tiles<FORM, 128, 128, 2, 2, 2>(g, stream); break;
+    default: launch_tiles<FORM, 256, 256, 2, 4, 1>(g, stream);
+  }
   return hipGetLastError();
 }
 

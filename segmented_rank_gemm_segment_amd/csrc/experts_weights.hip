@@ -2,17 +2,24 @@
 //
 //   dW_e[j][c] (+)= sum_p dY[p][j] X[row(p)][c]
 //
-// on 256 x 256 tiles (j x c) of a persistent workgroup, the expert's rows being K.  Both
-// operands' memory runs along the outputs: a row of dY and one of X are a k each, staged
-// and read by the LDS transpose read (experts_tiles.cuh).
+// on 256 x 256 tiles (j x c) of a persistent workgroup, the expert's rows being K, in stages
+// of 64 and two LDS buffers.  Both operands' memory runs along the outputs: a row of dY and
+// one of X are a k each, staged and read by the LDS transpose read (experts_tiles.cuh).
 //
-// K goes in stages of 32 rows through a ring of four LDS buffers.  Two waves own a buffer
-// and alone fill it, with whole 512-byte pieces of rows: a wave has one stage in flight
-// and, before the stage is read, waits for all of its loads; no wait depends on the order
-// in which loads complete, and a stage has the time of three to arrive.
+// Waits and barriers as in the products that write rows (experts_gemm.hip).  A stage's loads
+// have other rows than the last one's, so their addresses take more arithmetic; it stands
+// between the products of the first sub-steps (16384 rows, 14336 x 4096, 1904 us with it
+// among the last sub-step's loads, 2030 after them, 1720 so).  Loads by two owner waves of a
+// ring of four stages of 32, each in one go, took 3300: the others wait for the owners.
 //
 // An expert's tiles cost its stages and kTileCost more; each XCD takes an eighth of the
 // cost, and its CUs an expert's tiles together, which share the operands in its L2.
+//
+// Bound by the loads (1380 of the 1720 us alone) and the products (1340 alone, at the clock
+// that their power leaves), 1.12 PFLOP/s; an expert's few stages add the waits at tiles'
+// ends: 64 experts of 1024 rows, 2048 -> 1536, in 414 us in sorted order, 445 with X's rows
+// gathered, 515 with uneven experts (some CUs have a tile more of the long ones).  Few rows:
+// the stores, 128 experts of 1 row, 175 us of 156 at a copy's rate.
 #include <type_traits>
 
 #include "experts_tiles.cuh"
@@ -24,19 +31,21 @@ constexpr int kKS = 64, kRing = 2;          // k of a stage, buffers
 constexpr int kTileCost = 2;                // of a tile's start and stores, in stages
 
 // GATHER: X's rows by way of sorted_choice.
-template <int BM, int BN, int WM, int WN, bool F32OUT, bool GATHER>
-__global__ __launch_bounds__(WM *WN *kWave, WM *WN / 4) void experts_weights_kernel(ExpertGemmArgs g) {
+template <int BM, int BN, int WM, int WN, int PER_CU, bool F32OUT, bool GATHER>
+__global__ __launch_bounds__(WM *WN *kWave, WM *WN *PER_CU / 4) void experts_weights_kernel(ExpertGemmArgs g) {
   constexpr int NW = WM * WN, T = NW * kWave;
   constexpr int FM = BM / WM / 32, FN = BN / WN / 32;
   constexpr int PB = BM * kKS * 2, QB = BN * kKS * 2, STAGE = PB + QB;
   constexpr int I = PB / 1024 / NW;         // a wave's loads of an operand and stage
-  static_assert(BM == 256 && BN == 256 && NW == 8, "two rows a load");
+  constexpr int LPR = BM * 2 / 16, RPI = 64 / LPR;          // lanes a row, rows a load
+  constexpr int NC = 4 / RPI;               // loads of a wave that differ in their chunks
+  static_assert(BM == BN && RPI <= 4, "the operands' loads are alike");
   constexpr int SMEM = kRing * STAGE + kExpertTab + NW * 2048;
-  static_assert(SMEM <= 160 * 1024, "LDS");
+  static_assert(SMEM * PER_CU <= 160 * 1024, "LDS");
   __shared__ __align__(16) unsigned char smem[SMEM];
   int *const tab = reinterpret_cast<int *>(smem + kRing * STAGE);
 
-  const int tid = threadIdx.x, l = tid & (kWave - 1), h = l >> 5;
+  const int tid = threadIdx.x, l = tid & (kWave - 1), h = l / LPR;    // the lane's row of a load
   const int wid = scalar_int(tid / kWave);
   const int wm = wid / WN, wn = wid % WN;
   const int E = g.n_experts, M = g.M, N = g.N;
@@ -75,13 +84,13 @@ __global__ __launch_bounds__(WM *WN *kWave, WM *WN / 4) void experts_weights_ker
     return x;
   };
 
-  // This wave's loads, I instructions of two rows for each operand and stage.  Rows past the
+  // This wave's loads, I instructions of RPI rows for each operand and stage.  Rows past the
   // last one are zeroed in LDS before use and read from a valid row here; an expert without
   // rows reads the start of the output, which is there even where a batch without tokens has
   // no rows at all.  Columns past the last one are not stored.
   const uint32_t sbase = lds_offset(smem);
   const uint32_t dst = scalar_int(sbase + wid * I * 1024);
-  auto local_row = [&](int i, int h) __attribute__((always_inline)) { return (wid * I + i) * 2 + h; };
+  auto local_row = [&](int i, int h) __attribute__((always_inline)) { return (wid * I + i) * RPI + h; };
   Tile li;                                          // the tile being loaded
   int k_i = 0, b_i = 0, t_i = t;                    // its next stage, the buffer for it
   int f_r0, f_left;                                 // the stage after that one: first row, rows from there
@@ -89,7 +98,7 @@ __global__ __launch_bounds__(WM *WN *kWave, WM *WN / 4) void experts_weights_ker
   const uint32_t ldp2 = (uint32_t)(g.ldp * 2), ldq2 = (uint32_t)(g.ldq * 2);
   const int64_t pstep = kKS * 2 * g.ldp;
   const uint32_t hoff = h * ldp2;
-  uint32_t pc[2], qc[2];                            // bytes of the lane's chunk, even and odd loads
+  uint32_t pc[NC], qc[NC];                          // bytes of the lane's chunk of a load
   // Addresses are made, and the following stage's rows looked up, between the products of
   // the first two sub-steps: a wave that does it elsewhere keeps the matrix cores waiting.
   uint32_t poff[I];
@@ -97,9 +106,9 @@ __global__ __launch_bounds__(WM *WN *kWave, WM *WN / 4) void experts_weights_ker
   int qrow[I];                                      // the next stage's rows, or their choices
   auto ready_one = [&](int i) __attribute__((always_inline)) {
     const int left = li.rows - k_i * kKS;
-    poff[i] = (local_row(i, h) < left ? hoff + (uint32_t)(wid * I + i) * 2u * ldp2 : 0u) + pc[i & 1];
+    poff[i] = (local_row(i, h) < left ? hoff + (uint32_t)(wid * I + i) * RPI * ldp2 : 0u) + pc[i % NC];
     const int row = GATHER ? token_of(g, qrow[i]) : qrow[i];
-    qaddr[i] = qbase + (uint64_t)(uint32_t)row * ldq2 + qc[i & 1];
+    qaddr[i] = qbase + (uint64_t)(uint32_t)row * ldq2 + qc[i % NC];
   };
   auto fetch_one = [&](int i) __attribute__((always_inline)) {
     const bool in = local_row(i, h) < f_left;
@@ -118,8 +127,8 @@ __global__ __launch_bounds__(WM *WN *kWave, WM *WN / 4) void experts_weights_ker
     pbase = scalar_ptr(none ? o : g.P + (int64_t)li.r0 * g.ldp + li.m0);
     qbase = scalar_ptr(none ? o : g.Q + li.n0);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int c = ((ln & 31) ^ chunk_xor<BM, false>(local_row(i, ln >> 5))) * 8;
+    for (int i = 0; i < NC; ++i) {
+      const int c = ((ln % LPR) ^ chunk_xor<BM, false>(local_row(i, ln / LPR))) * 8;
       pc[i] = !none && li.m0 + c < M ? c * 2u : 0u;
       qc[i] = !none && li.n0 + c < N ? c * 2u : 0u;
     }
@@ -201,10 +210,10 @@ __global__ __launch_bounds__(WM *WN *kWave, WM *WN / 4) void experts_weights_ker
   auto sub_step = [&](auto k, const unsigned char *st) __attribute__((always_inline)) {
     constexpr int kk = decltype(k)::value;
     constexpr bool LOAD = kk == SUBS - 1;
-    static_assert(I <= NM && 2 * I <= NM && NR <= NM, "one of each beside a product");
+    static_assert(NR <= NM && I <= NM, "one of each beside a product");
 #pragma unroll
-    for (int q = 0; q < NM; ++q) {
-      acc[q / FM][q % FM] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+    for (int q = 0; q < (LOAD && 2 * I > NM ? 2 * I : NM); ++q) {
+      if (q < NM) acc[q / FM][q % FM] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
           qf[kk & 1][q / FM], pf[kk & 1][q % FM], acc[q / FM][q % FM], 0, 0, 0);
       if (q < NR) read((kk + 1) & 1, q, st, (kk + 1) % SUBS);
       if (kk == 0 && q < I) ready_one(q);
@@ -254,7 +263,9 @@ __global__ __launch_bounds__(WM *WN *kWave, WM *WN / 4) void experts_weights_ker
     settle();
     if ((kt + 1) * kKS > x.rows) zero_tail(x.rows - kt * kKS, b ^ 1);
     lgkm_barrier();                                 // it is there, and this one has been read
+    __builtin_amdgcn_s_setprio(1);
     sub_step(std::integral_constant<int, 3>{}, smem + (b ^ 1) * STAGE);
+    __builtin_amdgcn_s_setprio(0);
     pin();
     advance();
     b ^= 1;
@@ -285,8 +296,17 @@ __global__ __launch_bounds__(WM *WN *kWave, WM *WN / 4) void experts_weights_ker
 }
 
 template <bool F32OUT, bool GATHER> void launch_weights(const ExpertGemmArgs &g, hipStream_t stream) {
-  hipLaunchKernelGGL((experts_weights_kernel<256, 256, 2, 4, F32OUT, GATHER>), dim3(kCUs), dim3(512), 0,
-                     stream, g);
+  // As long as the CUs do not all get one of the large tiles, tiles of 128 x 128, two
+  // workgroups a CU (large / 128, us: 8 experts of 64 rows, 1032 x 520, 16 / 13, of 1024 rows
+  // 67 / 50; 2 of 256 rows, 1024 x 1024, 18 / 11; but 8 of 256, 4096 x 14336, 410 / 493, 128
+  // of 64, 2048 x 1536, 232 / 304).
+  const int64_t tiles = (int64_t)((g.M + 255) / 256) * ((g.N + 255) / 256) * g.n_experts;
+  if (tiles > kCUs)
+    hipLaunchKernelGGL((experts_weights_kernel<256, 256, 2, 4, 1, F32OUT, GATHER>), dim3(kCUs), dim3(512),
+                       0, stream, g);
+  else
+    hipLaunchKernelGGL((experts_weights_kernel<128, 128, 2, 2, 2, F32OUT, GATHER>), dim3(kCUs * 2),
+                       dim3(256), 0, stream, g);
 }
 
 }  // namespace

@@ -144,4 +144,38 @@ inline bool mx_wide_scales(int K, int64_t ldws, int64_t ldxs = 0) {
   return K % 512 == 0 && ldws % 16 == 0 && ldxs % 16 == 0;
 }
 
+// The experts' products on bf16 weights (experts_gemm.hip): 32 x 64 tiles whose K goes
+// round over a workgroup's waves, 128 x 128, or 256 x 256.
+enum ExpertsKernel { kExpertsFew, kExpertsMid, kExpertsLarge };
+inline double expert_tiles(int n_choices, int n_experts, int bm, int tiles_n) {
+  // every expert in use (at most one a choice) has half a tile more than its rows fill
+  const double used = n_choices < n_experts ? n_choices : n_experts, m = n_choices / used / bm + 0.5;
+  return used * (m < 1 ? 1 : m) * tiles_n;
+}
+// The cheapest, a kernel's rounds over the CUs (which hold one workgroup of the first and
+// last, two of the other) times a tile's microseconds, of a start and its 64s of K.  In us
+// (few / mid / large), few rows on weights that come from memory:
+//   1 x 8 choices of 128 experts, 2048 -> 1536: 13.6 / 32 / 48, and the rows' gradient 12.3 /
+//     22 / 37; 1 x 2 of 8, 4096 -> 14336: 48 / 70 and 70 / 184
+//   4 x 8 of 128, 2048 -> 1536: 42 / 46 and 44 / 37; 64 x 8: 157 / 156 and 171 / 144
+//   30 x 4 of 32, 1024 -> 1024: 16.7 / 20.1 and 16.1 / 17.5; 200 x 4: 21 / 20.5 and 22 / 19.4
+// and many (uneven ones, mid / large): 128 experts of 2048 -> 1536, 96 rows each 195 / 228 and
+//   203 / 210, 160 rows 252 / 246 and 233 / 231, 256 rows 322 / 304 and 310 / 285; 64 of 4096
+//   -> 4096, 96 rows 454 / 559 and 471 / 545, 192 rows 688 / 617 and 663 / 597; 8 of 4096 ->
+//   14336, 128 rows 247 / 302 and 275 / 334, 256 rows 356 / 334 and 439 / 356.
+// (Where memory is what they wait for, the first two are level: the first counts two thirds
+// of its own time in a forward product, four fifths in a gradient, whose W it reads in half
+// cache lines.)
+inline ExpertsKernel experts_kernel_of(int n_choices, int n_experts, int K, int N, bool forward) {
+  const double stages = (K + 63) / 64;
+  auto rounds = [](double tiles, int at_once) { return tiles <= at_once ? 1.0 : tiles / at_once; };
+  const double few = (forward ? 2.7 + 0.21 * stages : 3.3 + 0.26 * stages) *
+                     rounds(expert_tiles(n_choices, n_experts, 32, (N + 63) / 64), kCUs);
+  const double mid = (4 + 0.85 * stages) *
+                     rounds(expert_tiles(n_choices, n_experts, 128, (N + 127) / 128), 2 * kCUs);
+  const double large = (6 + 1.3 * stages) *
+                       rounds(expert_tiles(n_choices, n_experts, 256, (N + 255) / 256), kCUs);
+  return few < mid && few < large ? kExpertsFew : mid <= large ? kExpertsMid : kExpertsLarge;
+}
+
 }  // namespace lora

@@ -102,6 +102,12 @@ SHAPES = [
     (2000, 5, 37, "skewed", 128, 136, True, 0),
     (1500, 8, 1024, "skewed", 64, 72, True, 0),
     (1024, 1, 2, "one", 512, 256, True, 8),
+    (40, 4, 16, "skewed", 1032, 2056, True, 0),
+    (260, 8, 16, "bad", 264, 1544, True, 8),
+    (1100, 4, 8, "uniform", 520, 1032, False, 0),
+    (3000, 2, 12, "bad", 320, 776, True, 0),
+    (6000, 4, 8, "skewed", 584, 2056, True, 8),
+    (7000, 4, 8, "bad", 2048, 1024, False, 0),
 ]
 
 
