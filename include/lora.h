@@ -354,7 +354,7 @@ lora_status lora_linear_fused(const void *X, int64_t ldx, const void *W, int64_t
  *   dBt[a][k]  = s_a sum_{i in a} H[i][k] dY[i]       fp32 [n_slots][r_max][d_out]
  * for k < r, sums in fp32 in a fixed order; with accumulate other than 0 the sums
  * are added to dA and dBt.  Rank rows past r, slots without rows, and dH of rows
- * without an adapter are left as they are. 
+ * without an adapter are left as they are.
  * Wt is the base weight's transpose, [d_in][d_out]: laid out once, as the weight
  * does not change.  H and seg are the forward pass's.  dX may be NULL (an input
  * without gradient; Wt is then unused), and dA (X unused) or dBt (H unused).
@@ -617,9 +617,10 @@ lora_status lora_experts_gemm_backward(const void *dY, int64_t lddy, const void 
  * 0 (an adapter with no rows in the batch) is left as it is, its moments and step
  * count too.  lr is read from lr_dev (device fp32) where that is not NULL;
  * grad_scale, NULL or device fp32: multiplies every gradient.  Errors: sizes, lr
- * not finite, beta outside [0, 1), eps <= 0, weight_decay not finite or negative (LORA_ERR_SHAPE),
- * state_bits other than 8 or 32 (LORA_ERR_DTYPE), NULL, alignment of 16 bytes (4
- * for step, active, lr_dev and grad_scale).
+ * not finite, beta outside [0, 1), eps as a float below 2^-126 or not finite,
+ * weight_decay not finite or negative (LORA_ERR_SHAPE), state_bits other than 8 or
+ * 32 (LORA_ERR_DTYPE), NULL, alignment of 16 bytes (4 for step, active, lr_dev and
+ * grad_scale).
  *
  * lora_adamw_read: the values of 8-bit moments as `dtype`, into m_out and v_out
  * [state_numel] (LORA_ERR_DTYPE for 32-bit moments, which are values already).

@@ -5,7 +5,12 @@
 //   w = (1 - lr wd) w - lr / (1 - b1^t) m / (sqrt(v) / sqrt(1 - b2^t) + eps),
 //
 // with t the tensor's own step count.  Bound by memory: each of w, m and v is read
-// and written once and g read once.
+// and written once and g read once.  Measured: 201 M bf16 elements with fp32 masters and
+// moments (28 bytes an element) 1052 us, 5.4 TB/s, what a copy of 1 GiB reaches (5.2);
+// 176 M with 8-bit moments (10 bytes) 414 us, 4.3 TB/s, where the codes' arithmetic
+// shows; 8.4 M of 16.8 M taking part 62 us, 4.1 TB/s; 18 k elements of 9 tensors 14 us,
+// two launches' latency.  The factors are a launch of their own: formed by every
+// workgroup, their 64-bit powers would stand before each chunk's arithmetic.
 //
 // 8-bit moments: blocks of 256 consecutive elements share a float32 scale, their
 // largest magnitude.  A first moment's code c (-127..127) stands for
@@ -15,6 +20,8 @@
 // nearest code would hold it where it is; a value between two codes takes the upper
 // one with the probability that makes the expectation the value itself.  A second
 // moment above 0 takes code 1 at least: a quotient by a zero root would be huge.
+#include <type_traits>
+
 #include "lora_device.cuh"
 #include "lora_kernels.h"
 #include "tile_choice.h"
@@ -54,27 +61,30 @@ __global__ __launch_bounds__(256) void adamw_factors_kernel(AdamwArgs a) {
   a.factors[i] = f;
 }
 
-template <typename T> __device__ __forceinline__ void load8(const T *p, float (&x)[kVec]);
-template <> __device__ __forceinline__ void load8<float>(const float *p, float (&x)[kVec]) {
-  Elem<float>::unpack(ldg16(p), x);
-  Elem<float>::unpack(ldg16(p + 4), x + 4);
-}
-template <> __device__ __forceinline__ void load8<bf16_t>(const bf16_t *p, float (&x)[kVec]) {
-  Elem<bf16_t>::unpack(ldg16(p), x);
-}
-template <typename T> __device__ __forceinline__ void store8(T *p, const float (&x)[kVec]);
-template <> __device__ __forceinline__ void store8<float>(float *p, const float (&x)[kVec]) {
-  stg16(p, Elem<float>::pack(x));
-  stg16(p + 4, Elem<float>::pack(x + 4));
-}
-template <> __device__ __forceinline__ void store8<bf16_t>(bf16_t *p, const float (&x)[kVec]) {
-  stg16(p, Elem<bf16_t>::pack(x));
-}
-// The first `count` of 8 elements (a tensor's last ones).
-template <typename T>
-__device__ __forceinline__ void load_some(const T *p, int count, float (&x)[kVec]) {
+// 8 elements as they are loaded.
+template <typename T> struct Raw {
+  static constexpr int N = kVec / Elem<T>::kVec;
+  uint4 q[N];
+  __device__ __forceinline__ void load(const T *p) {
 #pragma unroll
-  for (int e = 0; e < kVec; ++e) x[e] = e < count ? Elem<T>::load1(p + e) : 0.f;
+    for (int i = 0; i < N; ++i) q[i] = ldg16(p + i * Elem<T>::kVec);
+  }
+  // the first `count` of them (a tensor's last ones), zeros behind
+  __device__ __forceinline__ void load_some(const T *p, int count) {
+    float x[kVec];
+#pragma unroll
+    for (int e = 0; e < kVec; ++e) x[e] = e < count ? Elem<T>::load1(p + e) : 0.f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) q[i] = Elem<T>::pack(x + i * Elem<T>::kVec);
+  }
+  __device__ __forceinline__ void values(float (&x)[kVec]) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i) Elem<T>::unpack(q[i], x + i * Elem<T>::kVec);
+  }
+};
+template <typename T> __device__ __forceinline__ void store8(T *p, const float (&x)[kVec]) {
+#pragma unroll
+  for (int i = 0; i < kVec; i += Elem<T>::kVec) stg16(p + i, Elem<T>::pack(x + i));
 }
 template <typename T>
 __device__ __forceinline__ void store_some(T *p, int count, const float (&x)[kVec]) {
@@ -120,21 +130,22 @@ __device__ __forceinline__ float inverse(float scale) {
   return scale > 0.f ? 1.f / scale : 0.f;             // (NaN: 0, and codes of 0)
 }
 
-// The codes of first moments: z = 127^2 |x| / scale lies between c^2 and (c + 1)^2,
-// and u (2 c + 1) < z - c^2 takes the upper one.
+// The codes of first moments: z = 127^2 |x| / scale lies between c^2 and (c + 1)^2, and
+// u (2 c + 1) < z - c^2 takes the upper one; u comes in 2^-16ths.  An error of the root
+// changes c beside a whole number only, where the other c with the other share is the same.
 __device__ __forceinline__ uint2 codes_m(const float (&x)[kVec], float scale,
                                          const float (&u)[kVec]) {
   const float inv = inverse(scale) * 16129.f;
   uint32_t q[2] = {0u, 0u};
 #pragma unroll
   for (int e = 0; e < kVec; ++e) {
-    const float z = inv > 0.f ? fabsf(x[e]) * inv : 0.f;
+    const float z = fabsf(x[e]) * inv;
     float c = floorf(__builtin_amdgcn_sqrtf(z));
-    c += u[e] * (2.f * c + 1.f) < fmaf(-c, c, z) ? 1.f : 0.f;
-    const int i = (int)fminf(c, 127.f);
-    q[e / 4] |= (uint32_t)((x[e] < 0.f ? -i : i) & 0xff) << (8 * (e & 3));
+    c += u[e] * fmaf(c, 0x1p-15f, 0x1p-16f) < fmaf(-c, c, z) ? 1.f : 0.f;
+    // a byte of c + 128, rounded (exact) and held to 1..255, less 128 by its upper bit
+    q[e / 4] = __builtin_amdgcn_cvt_pk_u8_f32(copysignf(fminf(c, 127.f), x[e]) + 128.f, e & 3, q[e / 4]);
   }
-  return make_uint2(q[0], q[1]);
+  return inv > 0.f ? make_uint2(q[0] ^ 0x80808080u, q[1] ^ 0x80808080u) : make_uint2(0u, 0u);
 }
 // Of second moments: z = 255^4 x / scale between c^4 and (c + 1)^4, which are
 // (2 c + 1) (2 c^2 + 2 c + 1) apart.
@@ -144,14 +155,14 @@ __device__ __forceinline__ uint2 codes_v(const float (&x)[kVec], float scale,
   uint32_t q[2] = {0u, 0u};
 #pragma unroll
   for (int e = 0; e < kVec; ++e) {
-    const float z = inv > 0.f ? x[e] * inv : 0.f;
+    const float z = x[e] * inv;
     float c = floorf(__builtin_amdgcn_sqrtf(__builtin_amdgcn_sqrtf(z)));
-    const float c2 = c * c, gap = (2.f * c + 1.f) * (2.f * c2 + 2.f * c + 1.f);
-    c += u[e] * gap < fmaf(-c2, c2, z) ? 1.f : 0.f;
-    const int i = (int)fminf(fmaxf(c, z > 0.f ? 1.f : 0.f), 255.f);
-    q[e / 4] |= (uint32_t)i << (8 * (e & 3));
+    const float c2 = c * c, t = c + c + 1.f;
+    c += u[e] * fmaf(c, 0x1p-15f, 0x1p-16f) * fmaf(c2, 2.f, t) < fmaf(-c2, c2, z) ? 1.f : 0.f;
+    c = fmaxf(c, z > 0.f ? 1.f : 0.f);
+    q[e / 4] = __builtin_amdgcn_cvt_pk_u8_f32(c, e & 3, q[e / 4]);        // (held to 255)
   }
-  return make_uint2(q[0], q[1]);
+  return inv > 0.f ? make_uint2(q[0], q[1]) : make_uint2(0u, 0u);
 }
 
 // A workgroup takes chunks of kAdamwChunk elements of one tensor.  P, G: the tensors'
@@ -165,37 +176,63 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(AdamwArgs a) {
   for (int64_t chunk = blockIdx.x; chunk < a.n_chunks; chunk += gridDim.x) {
     const int ti = a.chunk_tensor[chunk];
     const AdamwFactors f = a.factors[ti];
+    const AdamwTensor t = a.tensors[ti];            // (both at once)
     if (!f.on) continue;
-    const AdamwTensor t = a.tensors[ti];
     const int64_t base = (chunk - t.first_chunk) * kAdamwChunk;
     const uint32_t mkey = mix32(f.key + (uint32_t)(base >> 33));
+    // Every step's loads go out before the first step's arithmetic.  A block's lanes stay
+    // together: lanes past the tensor's end, in its last block, hold zeros, and the
+    // moments' buffers hold whole blocks.
+    using W = typename std::conditional<MASTER, float, P>::type;
+    Raw<G> graw[kSteps];
+    Raw<W> wraw[kSteps];
+    Raw<float> mraw[EIGHT ? 1 : kSteps], vraw[EIGHT ? 1 : kSteps];
+    uint2 mq[EIGHT ? kSteps : 1], vq[EIGHT ? kSteps : 1];
+    float ms[EIGHT ? kSteps : 1], vs[EIGHT ? kSteps : 1];
+    const int64_t in_tensor = t.numel - base;
+    const int n = in_tensor < kAdamwChunk ? (int)in_tensor : kAdamwChunk;      // of the chunk
+    const G *const gp = static_cast<const G *>(t.grad) + base;
+    P *const pp = static_cast<P *>(t.param) + base;
+    W *const wp = MASTER ? reinterpret_cast<W *>(t.master) + base : reinterpret_cast<W *>(pp);
+    const int64_t st = t.start + base;
+    float *const mf = static_cast<float *>(a.m) + st, *const vf = static_cast<float *>(a.v) + st;
+    int8_t *const mc = static_cast<int8_t *>(a.m) + st;
+    uint8_t *const vc = static_cast<uint8_t *>(a.v) + st;
+    float *const msp = a.m_scale + st / kAdamwBlock, *const vsp = a.v_scale + st / kAdamwBlock;
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) {
-      const int64_t e0 = base + s * kStep + threadIdx.x * kVec;
-      // (a block's lanes stay together: lanes past the tensor's end hold zeros)
-      if (base + s * kStep + (int64_t)(threadIdx.x & ~31) * kVec >= t.numel) continue;
-      const int left = (int)min((int64_t)kVec, t.numel - e0);      // may be 0 or less
-      const bool whole = left == kVec;
-      P *const pp = static_cast<P *>(t.param) + e0;
-      const G *const gp = static_cast<const G *>(t.grad) + e0;
-      float *const wp = MASTER ? t.master + e0 : nullptr;
-      const int64_t st = t.start + e0;
-      float g[kVec], w[kVec], m[kVec], v[kVec];
-      if (whole) {
-        load8(gp, g);
-        if constexpr (MASTER) load8(wp, w); else load8(pp, w);
+      const int e0 = s * kStep + (int)threadIdx.x * kVec;
+      if ((e0 & ~(kAdamwBlock - 1)) >= n) continue;
+      if (e0 + kVec <= n) {
+        graw[s].load(gp + e0);
+        wraw[s].load(wp + e0);
       } else {
-        load_some(gp, left, g);
-        if constexpr (MASTER) load_some(wp, left, w); else load_some(pp, left, w);
+        graw[s].load_some(gp + e0, n - e0);
+        wraw[s].load_some(wp + e0, n - e0);
       }
-      // (the moments' buffers hold whole blocks)
       if constexpr (EIGHT) {
-        const int64_t blk = st / kAdamwBlock;
-        values_m(*reinterpret_cast<const uint2 *>(static_cast<int8_t *>(a.m) + st), a.m_scale[blk], m);
-        values_v(*reinterpret_cast<const uint2 *>(static_cast<uint8_t *>(a.v) + st), a.v_scale[blk], v);
+        mq[s] = *reinterpret_cast<const uint2 *>(mc + e0);
+        vq[s] = *reinterpret_cast<const uint2 *>(vc + e0);
+        ms[s] = msp[e0 / kAdamwBlock];
+        vs[s] = vsp[e0 / kAdamwBlock];
       } else {
-        load8(static_cast<const float *>(a.m) + st, m);
-        load8(static_cast<const float *>(a.v) + st, v);
+        mraw[s].load(mf + e0);
+        vraw[s].load(vf + e0);
+      }
+    }
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+      const int e0 = s * kStep + (int)threadIdx.x * kVec;
+      if ((e0 & ~(kAdamwBlock - 1)) >= n) continue;
+      float g[kVec], w[kVec], m[kVec], v[kVec];
+      graw[s].values(g);
+      wraw[s].values(w);
+      if constexpr (EIGHT) {
+        values_m(mq[s], ms[s], m);
+        values_v(vq[s], vs[s], v);
+      } else {
+        mraw[s].values(m);
+        vraw[s].values(v);
       }
       uint32_t mtop = 0u, vtop = 0u;
 #pragma unroll
@@ -203,37 +240,40 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(AdamwArgs a) {
         const float ge = g[e] * gs;
         m[e] = fmaf(m[e], b1, ge * c1);
         v[e] = fmaf(v[e], b2, ge * ge * c2);
-        w[e] = w[e] * f.keep - f.rate * (m[e] / (sqrtf(v[e]) * f.root + a.eps));
+        // (the instructions' root and reciprocal, within one unit in the last place; a v
+        // below 2^-126 counts as zero here, beside eps that is 2^-126 at least)
+        const float den = fmaf(__builtin_amdgcn_sqrtf(v[e]), f.root, a.eps);
+        w[e] = fmaf(w[e], f.keep, -f.rate * (m[e] * __builtin_amdgcn_rcpf(den)));
         if constexpr (EIGHT) {
           mtop = max(mtop, __float_as_uint(fabsf(m[e])));
           vtop = max(vtop, __float_as_uint(fabsf(v[e])));
         }
       }
-      if (whole) {
-        if constexpr (MASTER) store8(wp, w);
-        store8(pp, w);
+      if (e0 + kVec <= n) {
+        if constexpr (MASTER) store8(wp + e0, w);
+        store8(pp + e0, w);
       } else {
-        if constexpr (MASTER) store_some(wp, left, w);
-        store_some(pp, left, w);
+        if constexpr (MASTER) store_some(wp + e0, n - e0, w);
+        store_some(pp + e0, n - e0, w);
       }
       if constexpr (EIGHT) {
-        const float ms = block_scale(block_max(mtop)), vs = block_scale(block_max(vtop));
+        const float mscale = block_scale(block_max(mtop)), vscale = block_scale(block_max(vtop));
         float u[kVec];
 #pragma unroll
         for (int e = 0; e < kVec; e += 2) {
-          const uint32_t h = mix32((uint32_t)((uint64_t)(e0 + e) >> 1) ^ mkey);
-          u[e] = (float)(h & 0xffffu) * 0x1p-16f;
-          u[e + 1] = (float)(h >> 16) * 0x1p-16f;
+          const uint32_t h = mix32((uint32_t)((uint64_t)(base + e0 + e) >> 1) ^ mkey);
+          u[e] = (float)(h & 0xffffu);
+          u[e + 1] = (float)(h >> 16);
         }
-        *reinterpret_cast<uint2 *>(static_cast<int8_t *>(a.m) + st) = codes_m(m, ms, u);
-        *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(a.v) + st) = codes_v(v, vs, u);
+        *reinterpret_cast<uint2 *>(mc + e0) = codes_m(m, mscale, u);
+        *reinterpret_cast<uint2 *>(vc + e0) = codes_v(v, vscale, u);
         if ((threadIdx.x & 31) == 0) {
-          a.m_scale[st / kAdamwBlock] = ms;
-          a.v_scale[st / kAdamwBlock] = vs;
+          msp[e0 / kAdamwBlock] = mscale;
+          vsp[e0 / kAdamwBlock] = vscale;
         }
       } else {
-        store8(static_cast<float *>(a.m) + st, m);
-        store8(static_cast<float *>(a.v) + st, v);
+        store8(mf + e0, m);
+        store8(vf + e0, v);
       }
     }
   }
@@ -255,7 +295,11 @@ __global__ __launch_bounds__(kThreads) void adamw_read_kernel(const int8_t *m, c
   }
 }
 
-constexpr int kGroups = kCUs * 8;      // workgroups of a launch at most
+// One workgroup a chunk (the bound keeps a grid's threads below 2^32): the next chunk's
+// loads go out while this one's stores are on their way, which a loop over chunks in
+// 8 or 16 workgroups a CU does less well (the first figures above 1119 us, 428 and 67).
+constexpr int64_t kStepGroups = 1 << 22;
+constexpr int kReadGroups = kCUs * 8;
 
 template <typename P, typename G, bool MASTER>
 void launch_by_bits(const AdamwArgs &a, dim3 grid, hipStream_t s) {
@@ -275,7 +319,7 @@ void launch_by_grad(const AdamwArgs &a, dim3 grid, hipStream_t s) {
 hipError_t launch_adamw(const AdamwArgs &a, hipStream_t stream) {
   hipLaunchKernelGGL(adamw_factors_kernel, dim3((a.n_tensors + 255) / 256), dim3(256), 0, stream, a);
   if (a.n_chunks > 0) {
-    const dim3 grid((unsigned)(a.n_chunks < kGroups ? a.n_chunks : kGroups));
+    const dim3 grid((unsigned)(a.n_chunks < kStepGroups ? a.n_chunks : kStepGroups));
     if (a.param_dtype == LORA_F32) launch_by_grad<float, false>(a, grid, stream);
     else if (a.master) launch_by_grad<bf16_t, true>(a, grid, stream);
     else launch_by_grad<bf16_t, false>(a, grid, stream);
@@ -287,7 +331,7 @@ hipError_t launch_adamw_read(const void *m, const void *v, const float *m_scale,
                              const float *v_scale, int64_t total, int dtype, void *m_out,
                              void *v_out, hipStream_t stream) {
   const int64_t groups = (total + kStep - 1) / kStep;
-  const dim3 grid((unsigned)(groups < kGroups ? groups : kGroups));
+  const dim3 grid((unsigned)(groups < kReadGroups ? groups : kReadGroups));
   const int8_t *mc = static_cast<const int8_t *>(m);
   const uint8_t *vc = static_cast<const uint8_t *>(v);
   if (dtype == LORA_BF16)

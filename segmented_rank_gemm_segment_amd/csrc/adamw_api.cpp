@@ -17,6 +17,8 @@ using lora::kAdamwChunk;
 using lora::kAdamwTensorBytes;
 static_assert(LORA_ADAMW_BLOCK == kAdamwBlock, "block");
 
+constexpr float kMinEps = 0x1p-126f;      // the smallest normal: a quotient stays finite
+
 bool aligned(const void *p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
 bool valid_dtype(int32_t d) { return d == LORA_F32 || d == LORA_BF16; }
 
@@ -130,7 +132,8 @@ lora_status lora_adamw_step(const lora_adamw *opt, double lr, const float *lr_de
   if (st != LORA_OK) return st;
   // (comparisons that a NaN fails)
   if (!std::isfinite(lr) || !(beta1 >= 0.0 && beta1 < 1.0) || !(beta2 >= 0.0 && beta2 < 1.0) ||
-      !(eps > 0.0 && std::isfinite(eps)) || !(weight_decay >= 0.0 && std::isfinite(weight_decay)))
+      !((float)eps >= kMinEps && std::isfinite((float)eps)) ||
+      !(weight_decay >= 0.0 && std::isfinite(weight_decay)))
     return LORA_ERR_SHAPE;
   if (!aligned(lr_dev, 4) || !aligned(grad_scale, 4) || !aligned(active, 4)) return LORA_ERR_ALIGN;
   lora::AdamwArgs a{};
