@@ -440,6 +440,13 @@ class Pool:
         self.generation[slot] += 1
         return self.generation[slot]
 
+    def write_b(self, stream=None) -> None:
+        """B from Bt's values again (lora_pool_write_b): after Bt was written in
+        place, by an optimizer step for one.  Nothing to do without ``natural_b``."""
+        if self.B is not None:
+            st = _launch_stream(stream, self.B, self.Bt)
+            _check(lib().lora_pool_write_b(self.c, st))
+
     def dora_prepare(self, slot: int, W: torch.Tensor, magnitude: Optional[torch.Tensor] = None,
                      stream=None) -> None:
         """DoRA column factors of ``slot`` from its current weights and the
@@ -974,11 +981,12 @@ def lora_experts_gemm_backward(dY: torch.Tensor, X: Optional[torch.Tensor], ex: 
                          "dXs [n_tokens * top_k, d_in]")
     ldw = 0 if W is None else _expert_matrices(ex, W, d_in, d_out, "W")
     lddw = 0 if dW is None else _expert_matrices(ex, dW, d_in, d_out, "dW")
+    dw_code = LORA_BF16 if dW is None else _dtype_code(dW.dtype)
     st = _launch_stream(stream, dY, X, W, dXs, dW, ex.expert_offsets)
     _check(lib().lora_experts_gemm_backward(
         _ptr(dY), _ld(dY), _ptr(X), 0 if X is None else _ld(X), 1 if gathered else 0, ex.c, _ptr(W),
         ldw, _ptr(dXs), 0 if dXs is None else _ld(dXs), _ptr(dW), lddw,
-        0 if dW is None else _dtype_code(dW.dtype), 1 if accumulate else 0, d_in, d_out, st))
+        dw_code, 1 if accumulate else 0, d_in, d_out, st))
 
 
 def lora_experts_gemm_mxfp4w(X: torch.Tensor, ex: Experts, Wq: torch.Tensor,
@@ -1058,7 +1066,9 @@ class AdamW:
     uint8 with ``m_scale`` and ``v_scale``, one float32 per ADAMW_BLOCK elements
     (include/lora.h has the format).  Tensor i's moments are elements [starts[i],
     starts[i] + numel).  ``step`` int32 [n_tensors] counts each tensor's steps.
-    A checkpoint is these buffers and the masters."""
+    A checkpoint is these buffers and the masters.  The buffers are filled on the
+    current stream; a step on another one has to wait for it.  A pool's B follows
+    its Bt with Pool.write_b."""
 
     def __init__(self, params, grads, bits: int = 32, masters=None):
         params, grads = list(params), list(grads)
@@ -1153,5 +1163,6 @@ def lora_adamw_read(opt: AdamW, m: torch.Tensor, v: torch.Tensor, stream=None) -
     for t in (m, v):
         if t.shape != (opt.numel,) or not t.is_contiguous() or t.dtype != m.dtype:
             raise ValueError("m, v: contiguous [opt.numel], of one dtype")
+    code = _dtype_code(m.dtype)
     st = _launch_stream(stream, opt.step, m, v)
-    _check(lib().lora_adamw_read(opt.c, _dtype_code(m.dtype), _ptr(m), _ptr(v), st))
+    _check(lib().lora_adamw_read(opt.c, code, _ptr(m), _ptr(v), st))
