@@ -595,8 +595,8 @@ lora_status lora_experts_gemm_backward(const void *dY, int64_t lddy, const void 
  * scale (c / 255)^4.  A value between two codes takes the upper one with the
  * probability that makes the expectation the value itself, by a hash of (seed, t,
  * tensor, element): the same call gives the same codes.  A v above 0 takes code 1
- * at least.  A block whose largest is below 2^-100 becomes zeros; one with an
- * infinity or NaN gets a NaN scale and codes 0.
+ * at least, one below 2^-126 code 1.  A block whose largest is below 2^-100 becomes
+ * zeros; one with an infinity or NaN gets a NaN scale and codes 0.
  *
  * Tensor i's moments start at element start(i), the sum of the earlier tensors'
  * numel, each rounded up to whole blocks; m and v hold lora_adamw_state_numel
@@ -609,8 +609,8 @@ lora_status lora_experts_gemm_backward(const void *dY, int64_t lddy, const void 
  * tensors, a tensor or master that overlaps another one or a gradient
  * (LORA_ERR_SHAPE), an unknown dtype (LORA_ERR_DTYPE), a pointer off 16 bytes
  * (LORA_ERR_ALIGN).  The caller copies it to the device once and keeps it with the
- * rest of the lora_adamw; a part of it is written by every step, so steps
- * on one lora_adamw (replays of graphs among them) have to be ordered.
+ * rest of the lora_adamw.  Steps on one lora_adamw (replays of graphs among
+ * them) have to be ordered.
  * The sizes functions return -1 for sizes out of range.
  *
  * lora_adamw_step: active, NULL or device int32 [n_tensors]: a tensor whose entry is

@@ -7,10 +7,10 @@
 // with t the tensor's own step count.  Bound by memory: each of w, m and v is read
 // and written once and g read once.  Measured: 201 M bf16 elements with fp32 masters and
 // moments (28 bytes an element) 1052 us, 5.4 TB/s, what a copy of 1 GiB reaches (5.2);
-// 176 M with 8-bit moments (10 bytes) 414 us, 4.3 TB/s, where the codes' arithmetic
-// shows; 8.4 M of 16.8 M taking part 62 us, 4.1 TB/s; 18 k elements of 9 tensors 14 us,
-// two launches' latency.  The factors are a launch of their own: formed by every
-// workgroup, their 64-bit powers would stand before each chunk's arithmetic.
+// 176 M with 8-bit moments (10 bytes) 400 us, 4.4 TB/s, where the codes' arithmetic
+// shows; 8.4 M of 16.8 M taking part 58 us, 4.3 TB/s; 18 k elements of 9 tensors 9 to
+// 13 us, the launches' latency.  The factors of a tensor are formed by each of its
+// workgroups: a launch of its own before this one took 3 to 5 us, which this hides.
 //
 // 8-bit moments: blocks of 256 consecutive elements share a float32 scale, their
 // largest magnitude.  A first moment's code c (-127..127) stands for
@@ -43,22 +43,30 @@ __host__ __device__ inline uint32_t mix32(uint32_t x) {
   return x ^ (x >> 16);
 }
 
-// Each tensor's step count and the factors of this step.  The bias corrections are
-// formed in 64 bits: 1 - b2^t of the first steps is a small difference.
-__global__ __launch_bounds__(256) void adamw_factors_kernel(AdamwArgs a) {
-  const int i = blockIdx.x * 256 + threadIdx.x;
-  if (i >= a.n_tensors) return;
-  const bool on = !a.active || a.active[i] != 0;
-  int t = a.step[i];
-  if (on) a.step[i] = ++t;
-  const double lr = a.lr_dev ? (double)*a.lr_dev : a.lr;
-  AdamwFactors f;
-  f.on = on;
-  f.rate = (float)(lr / (1.0 - pow(a.beta1, (double)t)));
-  f.root = (float)(1.0 / sqrt(1.0 - pow(a.beta2, (double)t)));
-  f.keep = (float)(1.0 - lr * a.weight_decay);
-  f.key = mix32(mix32(a.seed ^ ((uint32_t)t * 0x9E3779B1u)) + (uint32_t)i);
-  a.factors[i] = f;
+// The factors of a tensor's step, by two lanes.  The bias corrections are formed in 64
+// bits, as 1 - b^t of the first steps is a small difference, and b^t by squaring: at
+// most 62 products, so within 2^-46 of it.
+struct Factors {
+  float rate, root, keep;
+  uint32_t key;
+};
+__device__ inline double power(double b, int t) {
+  double p = 1.0;
+  for (; t > 0; t >>= 1, b *= b)
+    if (t & 1) p *= b;
+  return p;
+}
+__device__ inline void write_factors(const AdamwArgs &a, int tensor, int lane, Factors &f) {
+  const int t = a.step[tensor] + 1;
+  const float left = (float)(1.0 - power(lane ? a.beta2 : a.beta1, t));
+  if (lane) {
+    f.root = 1.f / sqrtf(left);
+    f.key = mix32(mix32(a.seed ^ ((uint32_t)t * 0x9E3779B1u)) + (uint32_t)tensor);
+  } else {
+    const double lr = a.lr_dev ? (double)*a.lr_dev : a.lr;
+    f.rate = (float)lr / left;
+    f.keep = (float)(1.0 - lr * a.weight_decay);
+  }
 }
 
 // 8 elements as they are loaded.
@@ -96,29 +104,36 @@ __device__ __forceinline__ void store_some(T *p, int count, const float (&x)[kVe
 __device__ __forceinline__ uint32_t byte_of(const uint2 &q, int e) {
   return ((e < 4 ? q.x : q.y) >> (8 * (e & 3))) & 0xffu;
 }
-__device__ __forceinline__ void values_m(const uint2 &q, float scale, float (&x)[kVec]) {
-  const float s = scale * (1.f / 16129.f);
+// c |c| and c^4 of the codes: the moments are these times the unit scales below.
+constexpr float kUnitM = 1.f / 16129.f, kUnitV = 1.f / 4228250625.f;
+__device__ __forceinline__ void powers_m(const uint2 &q, float (&x)[kVec]) {
 #pragma unroll
   for (int e = 0; e < kVec; ++e) {
     const float c = (float)(int8_t)byte_of(q, e);
-    x[e] = s * (c * fabsf(c));
+    x[e] = c * fabsf(c);
   }
 }
-__device__ __forceinline__ void values_v(const uint2 &q, float scale, float (&x)[kVec]) {
-  const float s = scale * (1.f / 4228250625.f);
+__device__ __forceinline__ void powers_v(const uint2 &q, float (&x)[kVec]) {
 #pragma unroll
   for (int e = 0; e < kVec; ++e) {
     const float c = (float)byte_of(q, e), c2 = c * c;
-    x[e] = s * (c2 * c2);
+    x[e] = c2 * c2;
   }
 }
 
 // The largest of the 32 lanes that hold a block, as the bits of a float that is not
-// negative (NaN above infinity above all numbers).
+// negative (NaN above infinity above all numbers): within quads, then mirrored halves
+// and rows of 16, then the two rows.
+template <int CTRL> __device__ __forceinline__ uint32_t max_dpp(uint32_t b) {
+  return max(b, (uint32_t)__builtin_amdgcn_update_dpp((int)b, (int)b, CTRL, 0xf, 0xf, false));
+}
 __device__ __forceinline__ uint32_t block_max(uint32_t b) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) b = max(b, (uint32_t)__shfl_xor((int)b, o));
-  return b;
+  b = max_dpp<0xb1>(b);         // quad_perm 1, 0, 3, 2
+  b = max_dpp<0x4e>(b);         // quad_perm 2, 3, 0, 1
+  b = max_dpp<0x141>(b);        // row_half_mirror
+  b = max_dpp<0x140>(b);        // row_mirror
+  const auto rows = __builtin_amdgcn_permlane16_swap(b, b, false, false);
+  return max((uint32_t)rows[0], (uint32_t)rows[1]);
 }
 // The scale of a block from its largest magnitude.  Below 2^-100 the block is kept as
 // zeros (its reciprocal would pass the range); an infinity or NaN makes it NaN.
@@ -133,33 +148,35 @@ __device__ __forceinline__ float inverse(float scale) {
 // The codes of first moments: z = 127^2 |x| / scale lies between c^2 and (c + 1)^2, and
 // u (2 c + 1) < z - c^2 takes the upper one; u comes in 2^-16ths.  An error of the root
 // changes c beside a whole number only, where the other c with the other share is the same.
+// 127^2 is taken four steps lower, which z cannot pass then and c not 127.
+constexpr float kBelowM = 16129.f * (1.f - 0x1p-22f);
 __device__ __forceinline__ uint2 codes_m(const float (&x)[kVec], float scale,
                                          const float (&u)[kVec]) {
-  const float inv = inverse(scale) * 16129.f;
+  const float inv = inverse(scale) * kBelowM;
   uint32_t q[2] = {0u, 0u};
 #pragma unroll
   for (int e = 0; e < kVec; ++e) {
     const float z = fabsf(x[e]) * inv;
     float c = floorf(__builtin_amdgcn_sqrtf(z));
     c += u[e] * fmaf(c, 0x1p-15f, 0x1p-16f) < fmaf(-c, c, z) ? 1.f : 0.f;
-    // a byte of c + 128, rounded (exact) and held to 1..255, less 128 by its upper bit
-    q[e / 4] = __builtin_amdgcn_cvt_pk_u8_f32(copysignf(fminf(c, 127.f), x[e]) + 128.f, e & 3, q[e / 4]);
+    // a byte of c + 128, rounded (exact), less 128 by its upper bit
+    q[e / 4] = __builtin_amdgcn_cvt_pk_u8_f32(copysignf(c, x[e]) + 128.f, e & 3, q[e / 4]);
   }
   return inv > 0.f ? make_uint2(q[0] ^ 0x80808080u, q[1] ^ 0x80808080u) : make_uint2(0u, 0u);
 }
 // Of second moments: z = 255^4 x / scale between c^4 and (c + 1)^4, which are
-// (2 c + 1) (2 c^2 + 2 c + 1) apart.
-__device__ __forceinline__ uint2 codes_v(const float (&x)[kVec], float scale,
-                                         const float (&u)[kVec]) {
-  const float inv = inverse(scale) * 4228250625.f;
+// (2 c + 1) (2 c^2 + 2 c + 1) apart.  root: of x, which the update needs too.
+__device__ __forceinline__ uint2 codes_v(const float (&x)[kVec], const float (&root)[kVec],
+                                         float scale, const float (&u)[kVec]) {
+  const float inv = inverse(scale) * 4228250625.f, rinv = __builtin_amdgcn_sqrtf(inv);
   uint32_t q[2] = {0u, 0u};
 #pragma unroll
   for (int e = 0; e < kVec; ++e) {
     const float z = x[e] * inv;
-    float c = floorf(__builtin_amdgcn_sqrtf(__builtin_amdgcn_sqrtf(z)));
+    float c = floorf(__builtin_amdgcn_sqrtf(root[e] * rinv));
     const float c2 = c * c, t = c + c + 1.f;
     c += u[e] * fmaf(c, 0x1p-15f, 0x1p-16f) * fmaf(c2, 2.f, t) < fmaf(-c2, c2, z) ? 1.f : 0.f;
-    c = fmaxf(c, z > 0.f ? 1.f : 0.f);
+    c = fmaxf(c, __builtin_amdgcn_fmed3f(z * 0x1p126f, 0.f, 1.f));        // (1 if z > 0)
     q[e / 4] = __builtin_amdgcn_cvt_pk_u8_f32(c, e & 3, q[e / 4]);        // (held to 255)
   }
   return inv > 0.f ? make_uint2(q[0], q[1]) : make_uint2(0u, 0u);
@@ -167,19 +184,20 @@ __device__ __forceinline__ uint2 codes_v(const float (&x)[kVec], float scale,
 
 // A workgroup takes chunks of kAdamwChunk elements of one tensor.  P, G: the tensors'
 // and gradients' types; MASTER: an fp32 copy of each tensor is what is updated, and
-// the tensor its rounding; EIGHT: 8-bit moments.
+// the tensor its rounding; EIGHT: 8-bit moments.  Every workgroup forms the factors
+// itself, while its loads are on their way.
 template <typename P, typename G, bool MASTER, bool EIGHT>
 __global__ __launch_bounds__(kThreads) void adamw_kernel(AdamwArgs a) {
   const float gs = a.grad_scale ? *a.grad_scale : 1.f;
   const float b1 = (float)a.beta1, b2 = (float)a.beta2;
   const float c1 = (float)(1.0 - a.beta1), c2 = (float)(1.0 - a.beta2);
+  __shared__ Factors shared[2];
+  int turn = 0;
   for (int64_t chunk = blockIdx.x; chunk < a.n_chunks; chunk += gridDim.x) {
     const int ti = a.chunk_tensor[chunk];
-    const AdamwFactors f = a.factors[ti];
-    const AdamwTensor t = a.tensors[ti];            // (both at once)
-    if (!f.on) continue;
+    if (a.active && a.active[ti] == 0) continue;
+    const AdamwTensor t = a.tensors[ti];
     const int64_t base = (chunk - t.first_chunk) * kAdamwChunk;
-    const uint32_t mkey = mix32(f.key + (uint32_t)(base >> 33));
     // Every step's loads go out before the first step's arithmetic.  A block's lanes stay
     // together: lanes past the tensor's end, in its last block, hold zeros, and the
     // moments' buffers hold whole blocks.
@@ -220,16 +238,24 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(AdamwArgs a) {
         vraw[s].load(vf + e0);
       }
     }
+    if (threadIdx.x < 2) write_factors(a, ti, threadIdx.x, shared[turn]);
+    __syncthreads();
+    const Factors f = shared[turn];
+    turn ^= 1;         // (the next barrier lies between this chunk's reads and the write after)
+    const uint32_t mkey = mix32(f.key + (uint32_t)(base >> 33)), pair = (uint32_t)(base >> 1);
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) {
       const int e0 = s * kStep + (int)threadIdx.x * kVec;
       if ((e0 & ~(kAdamwBlock - 1)) >= n) continue;
-      float g[kVec], w[kVec], m[kVec], v[kVec];
+      float g[kVec], w[kVec], m[kVec], v[kVec], root[kVec];
+      float mb = b1, vb = b2;                         // the old moments' factors
       graw[s].values(g);
       wraw[s].values(w);
       if constexpr (EIGHT) {
-        values_m(mq[s], ms[s], m);
-        values_v(vq[s], vs[s], v);
+        powers_m(mq[s], m);
+        powers_v(vq[s], v);
+        mb *= ms[s] * kUnitM;
+        vb *= vs[s] * kUnitV;
       } else {
         mraw[s].values(m);
         vraw[s].values(v);
@@ -238,11 +264,12 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(AdamwArgs a) {
 #pragma unroll
       for (int e = 0; e < kVec; ++e) {
         const float ge = g[e] * gs;
-        m[e] = fmaf(m[e], b1, ge * c1);
-        v[e] = fmaf(v[e], b2, ge * ge * c2);
+        m[e] = fmaf(m[e], mb, ge * c1);
+        v[e] = fmaf(v[e], vb, ge * ge * c2);
+        root[e] = __builtin_amdgcn_sqrtf(v[e]);
         // (the instructions' root and reciprocal, within one unit in the last place; a v
         // below 2^-126 counts as zero here, beside eps that is 2^-126 at least)
-        const float den = fmaf(__builtin_amdgcn_sqrtf(v[e]), f.root, a.eps);
+        const float den = fmaf(root[e], f.root, a.eps);
         w[e] = fmaf(w[e], f.keep, -f.rate * (m[e] * __builtin_amdgcn_rcpf(den)));
         if constexpr (EIGHT) {
           mtop = max(mtop, __float_as_uint(fabsf(m[e])));
@@ -261,12 +288,12 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(AdamwArgs a) {
         float u[kVec];
 #pragma unroll
         for (int e = 0; e < kVec; e += 2) {
-          const uint32_t h = mix32((uint32_t)((uint64_t)(base + e0 + e) >> 1) ^ mkey);
+          const uint32_t h = mix32((pair + (uint32_t)(e0 + e) / 2) ^ mkey);
           u[e] = (float)(h & 0xffffu);
           u[e + 1] = (float)(h >> 16);
         }
         *reinterpret_cast<uint2 *>(mc + e0) = codes_m(m, mscale, u);
-        *reinterpret_cast<uint2 *>(vc + e0) = codes_v(v, vscale, u);
+        *reinterpret_cast<uint2 *>(vc + e0) = codes_v(v, root, vscale, u);
         if ((threadIdx.x & 31) == 0) {
           msp[e0 / kAdamwBlock] = mscale;
           vsp[e0 / kAdamwBlock] = vscale;
@@ -279,6 +306,16 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(AdamwArgs a) {
   }
 }
 
+// The steps are counted when all of the step's workgroups have read the counts: a launch
+// of 2 us.  (Its last workgroup could do it, found by a counter for each tensor, but the
+// workgroups' additions to the counters took 1.1 and 1.9 ms more in the first two
+// figures above.)
+__global__ __launch_bounds__(kThreads) void adamw_count_kernel(int32_t *step, const int32_t *active,
+                                                               int n) {
+  const int i = blockIdx.x * kThreads + threadIdx.x;
+  if (i < n && (!active || active[i] != 0)) step[i] += 1;
+}
+
 // The values of 8-bit moments.
 template <typename T>
 __global__ __launch_bounds__(kThreads) void adamw_read_kernel(const int8_t *m, const uint8_t *v,
@@ -288,8 +325,14 @@ __global__ __launch_bounds__(kThreads) void adamw_read_kernel(const int8_t *m, c
   for (int64_t e = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * kVec; e < total;
        e += (int64_t)gridDim.x * kStep) {
     float x[kVec], y[kVec];
-    values_m(*reinterpret_cast<const uint2 *>(m + e), m_scale[e / kAdamwBlock], x);
-    values_v(*reinterpret_cast<const uint2 *>(v + e), v_scale[e / kAdamwBlock], y);
+    powers_m(*reinterpret_cast<const uint2 *>(m + e), x);
+    powers_v(*reinterpret_cast<const uint2 *>(v + e), y);
+    const float ms = m_scale[e / kAdamwBlock] * kUnitM, vs = v_scale[e / kAdamwBlock] * kUnitV;
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) {
+      x[i] *= ms;
+      y[i] *= vs;
+    }
     store8(m_out + e, x);
     store8(v_out + e, y);
   }
@@ -297,7 +340,7 @@ __global__ __launch_bounds__(kThreads) void adamw_read_kernel(const int8_t *m, c
 
 // One workgroup a chunk (the bound keeps a grid's threads below 2^32): the next chunk's
 // loads go out while this one's stores are on their way, which a loop over chunks in
-// 8 or 16 workgroups a CU does less well (the first figures above 1119 us, 428 and 67).
+// 8 or 16 workgroups a CU does less well (1119 us, 428 and 67 for 1050, 414 and 62 when it was tried).
 constexpr int64_t kStepGroups = 1 << 22;
 constexpr int kReadGroups = kCUs * 8;
 
@@ -317,13 +360,14 @@ void launch_by_grad(const AdamwArgs &a, dim3 grid, hipStream_t s) {
 }  // namespace
 
 hipError_t launch_adamw(const AdamwArgs &a, hipStream_t stream) {
-  hipLaunchKernelGGL(adamw_factors_kernel, dim3((a.n_tensors + 255) / 256), dim3(256), 0, stream, a);
   if (a.n_chunks > 0) {
     const dim3 grid((unsigned)(a.n_chunks < kStepGroups ? a.n_chunks : kStepGroups));
     if (a.param_dtype == LORA_F32) launch_by_grad<float, false>(a, grid, stream);
     else if (a.master) launch_by_grad<bf16_t, true>(a, grid, stream);
     else launch_by_grad<bf16_t, false>(a, grid, stream);
   }
+  hipLaunchKernelGGL(adamw_count_kernel, dim3((a.n_tensors + kThreads - 1) / kThreads),
+                     dim3(kThreads), 0, stream, a.step, a.active, a.n_tensors);
   return hipGetLastError();
 }
 

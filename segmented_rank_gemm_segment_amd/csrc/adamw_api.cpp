@@ -111,13 +111,11 @@ lora_status lora_adamw_table(const lora_adamw_tensor *tensors, int32_t n_tensors
     if (written) end_written = std::max(end_written, r[i].end);
   }
   AdamwTensor *const out = static_cast<AdamwTensor *>(table);
-  lora::AdamwFactors *const f = reinterpret_cast<lora::AdamwFactors *>(out + n_tensors);
-  int32_t *const map = reinterpret_cast<int32_t *>(f + n_tensors);
+  int32_t *const map = reinterpret_cast<int32_t *>(out + n_tensors);
   int64_t start = 0, chunk = 0;
   for (int32_t i = 0; i < n_tensors; ++i) {
     const lora_adamw_tensor &t = tensors[i];
     out[i] = AdamwTensor{t.param, t.grad, t.master, t.numel, start, chunk};
-    f[i] = lora::AdamwFactors{};
     start += (t.numel + kAdamwBlock - 1) / kAdamwBlock * kAdamwBlock;
     for (int64_t c = chunks_of(t.numel); c > 0; --c) map[chunk++] = i;
   }
@@ -144,9 +142,7 @@ lora_status lora_adamw_step(const lora_adamw *opt, double lr, const float *lr_de
   a.master = opt->masters != 0;
   a.n_chunks = (opt->table_bytes - opt->n_tensors * kAdamwTensorBytes) / 4;
   a.tensors = static_cast<const AdamwTensor *>(opt->table);
-  a.factors = reinterpret_cast<lora::AdamwFactors *>(static_cast<AdamwTensor *>(opt->table) +
-                                                     opt->n_tensors);
-  a.chunk_tensor = reinterpret_cast<const int32_t *>(a.factors + opt->n_tensors);
+  a.chunk_tensor = reinterpret_cast<const int32_t *>(a.tensors + opt->n_tensors);
   a.m = opt->m;
   a.v = opt->v;
   a.m_scale = opt->m_scale;

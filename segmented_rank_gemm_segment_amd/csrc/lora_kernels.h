@@ -185,10 +185,9 @@ hipError_t launch_experts_combine_backward(const void *dY, int64_t ldy, const vo
                                            int d, int dtype, void *dYs, int64_t ldds, float *dw,
                                            hipStream_t stream);
 
-// AdamW over many tensors (adamw.hip).  On the device: the tensors, the factors of a
-// step, and each chunk's tensor (a chunk is kAdamwChunk elements of one).
+// AdamW over many tensors (adamw.hip).  On the device: the tensors, and each chunk's
+// tensor (a chunk is kAdamwChunk elements of one).
 constexpr int kAdamwChunk = 4096, kAdamwBlock = 256;
-// The table holds them in this order.
 struct AdamwTensor {
   void *param;
   const void *grad;
@@ -197,20 +196,13 @@ struct AdamwTensor {
   int64_t start;         // of its moments, in elements: whole blocks
   int64_t first_chunk;
 };
-struct AdamwFactors {
-  float rate, root, keep;
-  uint32_t key;
-  int32_t on;
-  int32_t pad[3];
-};
-constexpr int64_t kAdamwTensorBytes = sizeof(AdamwTensor) + sizeof(AdamwFactors);
+constexpr int64_t kAdamwTensorBytes = sizeof(AdamwTensor);
 struct AdamwArgs {
   int n_tensors, param_dtype, grad_dtype, bits;
   bool master;
   int64_t n_chunks;
   const AdamwTensor *tensors;
   const int32_t *chunk_tensor;
-  AdamwFactors *factors;
   void *m, *v;
   float *m_scale, *v_scale;
   int32_t *step;
