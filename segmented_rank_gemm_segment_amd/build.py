@@ -22,7 +22,7 @@ LIB = os.path.join(PKG, "liblora.so")
 
 SOURCES = ["build_segments.hip", "shrink_expand.hip", "gemm.hip", "gemm_mx.hip", "mx_product.hip",
            "pack_slot.hip", "dora.hip", "static_scratch.hip", "mxfp4.hip", "experts.hip",
-           "experts_gemm.hip", "experts_weights.hip", "adapter_grad.hip", "adamw.hip",
+           "experts_gemm.hip", "experts_weights.hip", "adapter_dh.hip", "adapter_grad.hip", "adamw.hip",
            "lora_api.cpp", "adamw_api.cpp"]
 ARCH = os.environ.get("LORA_OFFLOAD_ARCH", "gfx950")
 

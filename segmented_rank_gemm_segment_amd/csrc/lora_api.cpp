@@ -257,7 +257,7 @@ lora_status lora_linear_backward(const void *dY, int64_t lddy, const void *Wt, i
   const hipStream_t s = static_cast<hipStream_t>(stream);
   const lora::SegView sv = seg_view(seg);
   const lora::PoolView pv = pool_view(pool), tv = transposed(pv);
-  hipError_t e = lora::launch_shrink(dY, lddy, sv, tv, dH, s);
+  hipError_t e = lora::launch_adapter_dh(dY, lddy, sv, pv, dH, s);
   if (e == hipSuccess)
     e = lora::launch_adapter_grads(X, ldx, dH, dA, dY, lddy, H, dBt, sv, pv, accumulate != 0, s);
   if (e == hipSuccess && dX)

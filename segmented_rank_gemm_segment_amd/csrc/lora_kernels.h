@@ -96,6 +96,10 @@ hipError_t launch_build_shrink(const BuildArgs &a, const void *X, int64_t ldx,
 hipError_t launch_expand(const float *H, const SegView &seg, const PoolView &pool, void *Y,
                          int64_t ldy, hipStream_t stream);
 
+// dH = dY B of every row's own adapter (adapter_dh.hip).
+hipError_t launch_adapter_dh(const void *dY, int64_t lddy, const SegView &seg, const PoolView &pool,
+                             float *dH, hipStream_t stream);
+
 // dA[slot] (+)= s dH^T X and dBt[slot] (+)= s H^T dY over each segment's rows (either
 // output may be null).
 hipError_t launch_adapter_grads(const void *X, int64_t ldx, const float *dH, float *dA,

@@ -231,3 +231,19 @@ def test_against_differences():
         (up, e1), (down, e2) = loss(c.A, c.Bt + D), loss(c.A, c.Bt - D)
         dot = np.sum(f64(c.dBt) * f64(D))
         assert abs(up - down - 2 * dot) <= e1 + e2 + 1e-4 * np.sum(np.abs(f64(c.dBt) * f64(D)))
+
+
+# rows and ranks of every workgroup shape of dH's kernel, rows that are no multiple of its blocks
+DH_CASES = [(1000, 16), (3301, 16), (1801, 32), (3301, 32), (1100, 64), (5003, 64), (16403, 64)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d_out", [8, 264, 2056])
+@pytest.mark.parametrize("n,r_max", DH_CASES)
+def test_dh_of_long_batches(n, r_max, d_out, dtype):
+    lengths = [n // 2, n // 4, 1, 17, 33, 64, 65, n // 16]
+    lengths.append(n - sum(lengths) - 2)
+    c = Case(seed=14, lengths=lengths, d_in=8, d_out=d_out, r_max=r_max, dtype=dtype, base=2, pad=8)
+    old = c.dA.clone(), c.dBt.clone()
+    c.call(dX=False, dA=False, dBt=False)
+    c.check(*old, dX=False, dA=False, dBt=False)
