@@ -6,7 +6,9 @@
 // two products of the same form, out = s V^T U over the segment's rows, both in one
 // launch.  Bound by memory: U is read once and the gradients written once, and what
 // is multiplied per byte of U, up to 64 ranks, is below what the matrix cores do
-// meanwhile.
+// meanwhile.  Measured: 16,943 rows of 8 slots, 4096 -> 14336, ranks 8 to 64, 157 to 165
+// us (625 MB of X and dY, 3.9 TB/s); 2303 rows of 37 slots, 8192 -> 1024, ranks 8 to 32,
+// added to what is there, 27 us (42 MB read and twice 27 MB of gradients, 3.6 TB/s).
 //
 // Segments of more than kShortRows rows go through the matrix cores.  The reduction runs
 // over rows, so both operands want 8 rows of one column in a lane.  A lane loads VEC
@@ -24,7 +26,9 @@
 //
 // Shorter segments, a decode batch's or many tenants' few rows each, are bound by the
 // writes: each thread keeps its columns of all rows in registers and forms one rank row
-// after the other.
+// after the other (128 segments of two rows, 4096 -> 4096, ranks 8 and 16, 14 us for 45
+// MB).  Each of the two launches leaves the other's segments alone, 2 to 4 us where that
+// is all of them.
 #include "lds_dma.cuh"
 #include "lora_device.cuh"
 #include "lora_kernels.h"

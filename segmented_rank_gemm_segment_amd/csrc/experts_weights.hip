@@ -13,12 +13,14 @@
 // ring of four stages of 32, each in one go, took 3300: the others wait for the owners.
 //
 // An expert's tiles cost its stages and kTileCost more; each XCD takes an eighth of the
-// cost, and its CUs an expert's tiles together, which share the operands in its L2.
+// cost, and its CUs an expert's tiles together, which share the operands in its L2.  (Every
+// CU the same number of each expert's tiles, longest first, and what is left back and forth
+// between the CUs, so that all end together: 5% more time, as the CUs share what binds them.)
 //
 // Bound by the loads (1380 of the 1720 us alone) and the products (1340 alone, at the clock
 // that their power leaves), 1.12 PFLOP/s; an expert's few stages add the waits at tiles'
 // ends: 64 experts of 1024 rows, 2048 -> 1536, in 414 us in sorted order, 445 with X's rows
-// gathered, 515 with uneven experts (some CUs have a tile more of the long ones).  Few rows:
+// gathered, 515 with uneven experts.  Few rows:
 // the stores, 128 experts of 1 row, 175 us of 156 at a copy's rate.
 #include <type_traits>
 

@@ -146,6 +146,20 @@ def test_parts(dX, dA, dBt):
     assert dBt or torch.equal(c.dBt, old[1])
 
 
+@pytest.mark.parametrize("policy", ["two_buckets", "padded"])
+@pytest.mark.parametrize("name", ["ranks", "f32"])
+def test_rank_policies(name, policy):
+    """What lies past a row's rank, in H, dH, A and Bt, is not used as a number."""
+    c = Case(**CASES[name])
+    for a, k in enumerate(c.rank.tolist()):
+        c.A[a, k:] = float("nan")
+        c.Bt[a, k:] = float("nan")
+    c.pool.set_policy(policy)
+    old = c.dA.clone(), c.dBt.clone()
+    c.call()
+    c.check(*old)
+
+
 def test_bad_slots_and_no_rows():
     c = Case(**CASES["ranks"])
     c.slot[::7] = 1000                                   # demoted to base-only
