@@ -595,8 +595,8 @@ lora_status lora_experts_gemm_backward(const void *dY, int64_t lddy, const void 
  * scale (c / 255)^4.  A value between two codes takes the upper one with the
  * probability that makes the expectation the value itself, by a hash of (seed, t,
  * tensor, element): the same call gives the same codes.  A v above 0 takes code 1
- * at least, one below 2^-126 code 1.  A block whose largest is below 2^-100 becomes
- * zeros; one with an infinity or NaN gets a NaN scale and codes 0.
+ * at least.  A block whose largest is below 2^-100 becomes zeros; one with a NaN or
+ * an infinity, an m of 2^126 or a v of 2^118 and more, gets a NaN scale and codes 0.
  *
  * Tensor i's moments start at element start(i), the sum of the earlier tensors'
  * numel, each rounded up to whole blocks; m and v hold lora_adamw_state_numel

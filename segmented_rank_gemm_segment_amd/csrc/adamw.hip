@@ -7,7 +7,7 @@
 // with t the tensor's own step count.  Bound by memory: each of w, m and v is read
 // and written once and g read once.  Measured: 201 M bf16 elements with fp32 masters and
 // moments (28 bytes an element) 1052 us, 5.4 TB/s, what a copy of 1 GiB reaches (5.2);
-// 176 M with 8-bit moments (10 bytes) 400 us, 4.4 TB/s, where the codes' arithmetic
+// 176 M with 8-bit moments (10 bytes) 405 us, 4.3 TB/s, where the codes' arithmetic
 // shows; 8.4 M of 16.8 M taking part 58 us, 4.3 TB/s; 18 k elements of 9 tensors 9 to
 // 13 us, the launches' latency.  The factors of a tensor are formed by each of its
 // workgroups: a launch of its own before this one took 3 to 5 us, which this hides.
@@ -104,8 +104,12 @@ __device__ __forceinline__ void store_some(T *p, int count, const float (&x)[kVe
 __device__ __forceinline__ uint32_t byte_of(const uint2 &q, int e) {
   return ((e < 4 ? q.x : q.y) >> (8 * (e & 3))) & 0xffu;
 }
-// c |c| and c^4 of the codes: the moments are these times the unit scales below.
-constexpr float kUnitM = 1.f / 16129.f, kUnitV = 1.f / 4228250625.f;
+// c |c| and c^4 of the codes: the moments are these times the unit scales below.  Second
+// moments are formed 2^8 times as large, kLift, beside 8-bit codes: the unit of a scale near
+// 2^-100 is then a normal number, its reciprocal's 255^4 in range, and the root of what is
+// at least a code's 2^-2 no zero.
+constexpr float kLift = 256.f;
+constexpr float kUnitM = 1.f / 16129.f, kUnitV = kLift / 4228250625.f;
 __device__ __forceinline__ void powers_m(const uint2 &q, float (&x)[kVec]) {
 #pragma unroll
   for (int e = 0; e < kVec; ++e) {
@@ -135,11 +139,12 @@ __device__ __forceinline__ uint32_t block_max(uint32_t b) {
   const auto rows = __builtin_amdgcn_permlane16_swap(b, b, false, false);
   return max((uint32_t)rows[0], (uint32_t)rows[1]);
 }
-// The scale of a block from its largest magnitude.  Below 2^-100 the block is kept as
-// zeros (its reciprocal would pass the range); an infinity or NaN makes it NaN.
-constexpr uint32_t kTiny = (127u - 100u) << 23, kInf = 0x7f800000u;
-__device__ __forceinline__ float block_scale(uint32_t top) {
-  return __uint_as_float(top < kTiny ? 0u : top >= kInf ? 0x7fc00000u : top);
+// The scale of a block from its largest magnitude.  Below `tiny` the block is kept as
+// zeros (its reciprocal would pass the range); 2^126 or more (whose reciprocal is no normal
+// number), an infinity or NaN make it NaN.
+constexpr uint32_t kTiny = (127u - 100u) << 23, kTinyV = kTiny + (8u << 23), kHuge = (127u + 126u) << 23;
+__device__ __forceinline__ float block_scale(uint32_t top, uint32_t tiny) {
+  return __uint_as_float(top < tiny ? 0u : top >= kHuge ? 0x7fc00000u : top);
 }
 __device__ __forceinline__ float inverse(float scale) {
   return scale > 0.f ? 1.f / scale : 0.f;             // (NaN: 0, and codes of 0)
@@ -190,7 +195,7 @@ template <typename P, typename G, bool MASTER, bool EIGHT>
 __global__ __launch_bounds__(kThreads) void adamw_kernel(AdamwArgs a) {
   const float gs = a.grad_scale ? *a.grad_scale : 1.f;
   const float b1 = (float)a.beta1, b2 = (float)a.beta2;
-  const float c1 = (float)(1.0 - a.beta1), c2 = (float)(1.0 - a.beta2);
+  const float c1 = (float)(1.0 - a.beta1), c2 = (float)(1.0 - a.beta2) * (EIGHT ? kLift : 1.f);
   __shared__ Factors shared[2];
   int turn = 0;
   for (int64_t chunk = blockIdx.x; chunk < a.n_chunks; chunk += gridDim.x) {
@@ -240,7 +245,8 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(AdamwArgs a) {
     }
     if (threadIdx.x < 2) write_factors(a, ti, threadIdx.x, shared[turn]);
     __syncthreads();
-    const Factors f = shared[turn];
+    Factors f = shared[turn];
+    if (EIGHT) f.root *= 1.f / 16.f;                // (of kLift)
     turn ^= 1;         // (the next barrier lies between this chunk's reads and the write after)
     const uint32_t mkey = mix32(f.key + (uint32_t)(base >> 33)), pair = (uint32_t)(base >> 1);
 #pragma unroll
@@ -267,8 +273,8 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(AdamwArgs a) {
         m[e] = fmaf(m[e], mb, ge * c1);
         v[e] = fmaf(v[e], vb, ge * ge * c2);
         root[e] = __builtin_amdgcn_sqrtf(v[e]);
-        // (the instructions' root and reciprocal, within one unit in the last place; a v
-        // below 2^-126 counts as zero here, beside eps that is 2^-126 at least)
+        // (the instructions' root and reciprocal, within one unit in the last place; the root
+        // of what is below 2^-126 is zero, beside eps that is 2^-126 at least)
         const float den = fmaf(root[e], f.root, a.eps);
         w[e] = fmaf(w[e], f.keep, -f.rate * (m[e] * __builtin_amdgcn_rcpf(den)));
         if constexpr (EIGHT) {
@@ -284,7 +290,8 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(AdamwArgs a) {
         store_some(pp + e0, n - e0, w);
       }
       if constexpr (EIGHT) {
-        const float mscale = block_scale(block_max(mtop)), vscale = block_scale(block_max(vtop));
+        const float mscale = block_scale(block_max(mtop), kTiny);
+        const float vscale = block_scale(block_max(vtop), kTinyV);
         float u[kVec];
 #pragma unroll
         for (int e = 0; e < kVec; e += 2) {
@@ -296,7 +303,7 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(AdamwArgs a) {
         *reinterpret_cast<uint2 *>(vc + e0) = codes_v(v, root, vscale, u);
         if ((threadIdx.x & 31) == 0) {
           msp[e0 / kAdamwBlock] = mscale;
-          vsp[e0 / kAdamwBlock] = vscale;
+          vsp[e0 / kAdamwBlock] = vscale * (1.f / kLift);
         }
       } else {
         store8(mf + e0, m);
@@ -331,7 +338,7 @@ __global__ __launch_bounds__(kThreads) void adamw_read_kernel(const int8_t *m, c
 #pragma unroll
     for (int i = 0; i < kVec; ++i) {
       x[i] *= ms;
-      y[i] *= vs;
+      y[i] = y[i] * (1.f / kLift) * vs;
     }
     store8(m_out + e, x);
     store8(v_out + e, y);

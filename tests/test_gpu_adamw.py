@@ -201,6 +201,48 @@ def test_small_blocks_become_zeros():
     assert torch.isfinite(opt.params[0]).all()
 
 
+def test_steps_of_small_scales():
+    """Second moments whose scales are just above 2^-100, where a code's unit, 255^-4 of
+    it, is below the smallest normal number."""
+    opt, gen = setup(13, [(2048,), (300,)], bits=8)
+    for step in range(3):
+        for g in opt.grads:
+            g.copy_((torch.rand(g.shape, generator=gen) + 0.5) * 2.0 ** -44)
+        before = snapshot(opt)
+        srg.lora_adamw_step(opt, 1e-2, seed=step)
+        assert (opt.v_scale > 0).all() and (opt.v_scale < 2.0 ** -94).all()
+        check(opt, before, 1e-2, seed=step)
+    m, v = torch.empty(opt.numel, device=DEV), torch.empty(opt.numel, device=DEV)
+    srg.lora_adamw_read(opt, m, v)
+    want = ref.value_v(opt.v.cpu().numpy(), opt.v_scale.cpu().numpy())
+    assert (np.abs(f64(v) - want) <= 4 * U * want + 2.0 ** -149).all()
+
+
+def test_largest_blocks():
+    """Moments up to their documented bounds keep codes in range; past them the scale is NaN."""
+    opt, _ = setup(14, [(256,), (256,), (256,)], bits=8)
+    kw = dict(beta1=0.0, beta2=0.999)                    # m = g, v = 0.001 g^2
+    sign = torch.where(torch.arange(256, device=DEV) % 2 == 0, 1.0, -1.0)
+    opt.grads[0].copy_(sign * 2.0 ** 63)                 # v just below 2^118 ...
+    opt.grads[1].copy_(sign * 2.0 ** 63.99)              # ... and above
+    opt.grads[2].copy_(sign * 2.0 ** 40)
+    srg.lora_adamw_step(opt, 1e-2, **kw)
+    assert torch.isfinite(opt.m_scale).all()
+    assert torch.isfinite(opt.v_scale[[0, 2]]).all() and torch.isnan(opt.v_scale[1])
+    assert (opt.m.abs() == 127).all() and torch.equal(opt.m[:256].sign().float(), sign)
+    assert (opt.v[:256] == 255).all() and not opt.v[256:512].any()
+    opt.m_scale[2] = 2.0 ** 126                          # m = 0.9 of 2^126, then 1.1
+    opt.v.zero_()
+    opt.v_scale.zero_()
+    for g in opt.grads:
+        g.zero_()
+    srg.lora_adamw_step(opt, 1e-2, beta1=0.9)
+    assert torch.isfinite(opt.m_scale).all() and (opt.m[512:].abs() == 127).all()
+    opt.m_scale[2] = 2.0 ** 126 * 1.2
+    srg.lora_adamw_step(opt, 1e-2, beta1=0.9)
+    assert torch.isnan(opt.m_scale[2]) and not opt.m[512:].any()
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_read(dtype):
     opt, _ = setup(7, SIZES, bits=8)
