@@ -146,23 +146,25 @@ constexpr uint32_t kTiny = (127u - 100u) << 23, kTinyV = kTiny + (8u << 23), kHu
 __device__ __forceinline__ float block_scale(uint32_t top, uint32_t tiny) {
   return __uint_as_float(top < tiny ? 0u : top >= kHuge ? 0x7fc00000u : top);
 }
-__device__ __forceinline__ float inverse(float scale) {
-  return scale > 0.f ? 1.f / scale : 0.f;             // (NaN: 0, and codes of 0)
+// (one division, so that z below has two roundings: a share of the codes' distance that is
+// off by them takes the other code that often)
+__device__ __forceinline__ float over_scale(float top, float scale) {
+  return scale > 0.f ? top / scale : 0.f;             // (NaN: 0, and codes of 0)
 }
 
 // The codes of first moments: z = 127^2 |x| / scale lies between c^2 and (c + 1)^2, and
 // u (2 c + 1) < z - c^2 takes the upper one; u comes in 2^-16ths.  An error of the root
 // changes c beside a whole number only, where the other c with the other share is the same.
-// 127^2 is taken four steps lower, which z cannot pass then and c not 127.
-constexpr float kBelowM = 16129.f * (1.f - 0x1p-22f);
+// c is 126 at most and the upper one 127, which the block's largest takes whatever u is: its
+// z - 126^2 is 253 within the 2^-9 of z's roundings, and 253 u at most 253 (1 - 2^-16).
 __device__ __forceinline__ uint2 codes_m(const float (&x)[kVec], float scale,
                                          const float (&u)[kVec]) {
-  const float inv = inverse(scale) * kBelowM;
+  const float inv = over_scale(16129.f, scale);
   uint32_t q[2] = {0u, 0u};
 #pragma unroll
   for (int e = 0; e < kVec; ++e) {
     const float z = fabsf(x[e]) * inv;
-    float c = floorf(__builtin_amdgcn_sqrtf(z));
+    float c = fminf(floorf(__builtin_amdgcn_sqrtf(z)), 126.f);
     c += u[e] * fmaf(c, 0x1p-15f, 0x1p-16f) < fmaf(-c, c, z) ? 1.f : 0.f;
     // a byte of c + 128, rounded (exact), less 128 by its upper bit
     q[e / 4] = __builtin_amdgcn_cvt_pk_u8_f32(copysignf(c, x[e]) + 128.f, e & 3, q[e / 4]);
@@ -173,7 +175,7 @@ __device__ __forceinline__ uint2 codes_m(const float (&x)[kVec], float scale,
 // (2 c + 1) (2 c^2 + 2 c + 1) apart.  root: of x, which the update needs too.
 __device__ __forceinline__ uint2 codes_v(const float (&x)[kVec], const float (&root)[kVec],
                                          float scale, const float (&u)[kVec]) {
-  const float inv = inverse(scale) * 4228250625.f, rinv = __builtin_amdgcn_sqrtf(inv);
+  const float inv = over_scale(4228250625.f, scale), rinv = __builtin_amdgcn_sqrtf(inv);
   uint32_t q[2] = {0u, 0u};
 #pragma unroll
   for (int e = 0; e < kVec; ++e) {
