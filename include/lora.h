@@ -617,10 +617,11 @@ lora_status lora_experts_gemm_backward(const void *dY, int64_t lddy, const void 
  * 0 (an adapter with no rows in the batch) is left as it is, its moments and step
  * count too.  lr is read from lr_dev (device fp32) where that is not NULL;
  * grad_scale, NULL or device fp32: multiplies every gradient.  Errors: sizes, lr
- * not finite, beta outside [0, 1), eps as a float below 2^-126 or not finite,
- * weight_decay not finite or negative (LORA_ERR_SHAPE), state_bits other than 8 or
- * 32 (LORA_ERR_DTYPE), NULL, alignment of 16 bytes (4 for step, active, lr_dev and
- * grad_scale).
+ * not finite, beta outside [0, 1), eps as a float below 2^-126 (beside 8-bit moments
+ * 2^-40: blocks of v below 2^-100 are zeros, and their roots must not count) or not
+ * finite, weight_decay not finite or negative (LORA_ERR_SHAPE), state_bits other than
+ * 8 or 32 (LORA_ERR_DTYPE), NULL, alignment of 16 bytes (4 for step, active, lr_dev
+ * and grad_scale).
  *
  * lora_adamw_read: the values of 8-bit moments as `dtype`, into m_out and v_out
  * [state_numel] (LORA_ERR_DTYPE for 32-bit moments, which are values already).

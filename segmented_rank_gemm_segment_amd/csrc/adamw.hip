@@ -189,6 +189,15 @@ __device__ __forceinline__ uint2 codes_v(const float (&x)[kVec], const float (&r
   return inv > 0.f ? make_uint2(q[0], q[1]) : make_uint2(0u, 0u);
 }
 
+// The root by the instruction, within one unit in the last place, which takes what is below
+// 2^-126 for zero.  The root of that is up to 2^-63: small numbers are taken 2^64 times as
+// large.  Not beside 8-bit codes, whose eps is 2^-40 at least and v 2^8 times as large.
+template <bool EIGHT> __device__ __forceinline__ float root_of(float v) {
+  if constexpr (EIGHT) return __builtin_amdgcn_sqrtf(v);
+  const bool small = v < 0x1p-64f;
+  return __builtin_amdgcn_sqrtf(v * (small ? 0x1p64f : 1.f)) * (small ? 0x1p-32f : 1.f);
+}
+
 // A workgroup takes chunks of kAdamwChunk elements of one tensor.  P, G: the tensors'
 // and gradients' types; MASTER: an fp32 copy of each tensor is what is updated, and
 // the tensor its rounding; EIGHT: 8-bit moments.  Every workgroup forms the factors
@@ -274,9 +283,9 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(AdamwArgs a) {
         const float ge = g[e] * gs;
         m[e] = fmaf(m[e], mb, ge * c1);
         v[e] = fmaf(v[e], vb, ge * ge * c2);
-        root[e] = __builtin_amdgcn_sqrtf(v[e]);
-        // (the instructions' root and reciprocal, within one unit in the last place; the root
-        // of what is below 2^-126 is zero, beside eps that is 2^-126 at least)
+        root[e] = root_of<EIGHT>(v[e]);
+        // (the instruction's reciprocal, within one unit in the last place, of what is no less
+        // than eps and so a normal number)
         const float den = fmaf(root[e], f.root, a.eps);
         w[e] = fmaf(w[e], f.keep, -f.rate * (m[e] * __builtin_amdgcn_rcpf(den)));
         if constexpr (EIGHT) {

@@ -17,7 +17,11 @@ using lora::kAdamwChunk;
 using lora::kAdamwTensorBytes;
 static_assert(LORA_ADAMW_BLOCK == kAdamwBlock, "block");
 
-constexpr float kMinEps = 0x1p-126f;      // the smallest normal: a quotient stays finite
+// The smallest eps: the smallest normal number, whose reciprocal is finite.  8-bit second
+// moments whose blocks are below 2^-100 become zeros, roots of up to 2^-50 that bias corrections
+// of the first steps raise to 2^-45: nothing beside an eps of 2^-40, all there is beside a
+// smaller one.
+constexpr float kMinEps = 0x1p-126f, kMinEps8 = 0x1p-40f;
 
 bool aligned(const void *p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
 bool valid_dtype(int32_t d) { return d == LORA_F32 || d == LORA_BF16; }
@@ -130,7 +134,7 @@ lora_status lora_adamw_step(const lora_adamw *opt, double lr, const float *lr_de
   if (st != LORA_OK) return st;
   // (comparisons that a NaN fails)
   if (!std::isfinite(lr) || !(beta1 >= 0.0 && beta1 < 1.0) || !(beta2 >= 0.0 && beta2 < 1.0) ||
-      !((float)eps >= kMinEps && std::isfinite((float)eps)) ||
+      !((float)eps >= (opt->state_bits == 8 ? kMinEps8 : kMinEps) && std::isfinite((float)eps)) ||
       !(weight_decay >= 0.0 && std::isfinite(weight_decay)))
     return LORA_ERR_SHAPE;
   if (!aligned(lr_dev, 4) || !aligned(grad_scale, 4) || !aligned(active, 4)) return LORA_ERR_ALIGN;

@@ -1,4 +1,5 @@
-"""AdamW at the ends of its ranges: codes next to the border between two of them.
+"""AdamW at the ends of its ranges: codes next to the border between two of them, second
+moments below the normal numbers, the smallest eps.
 
 A code's place.  On a first step m' = c1 g and v' = c2 g^2 are one and two fp32 roundings,
 which are repeated here, so only what the codes add is left: z = L / top x (the division and
@@ -41,3 +42,51 @@ def test_codes_beside_a_border():
         up, down = np.count_nonzero(diff > 0), np.count_nonzero(diff < 0)
         # five standard deviations of a fair coin's
         assert abs(up - down) <= 5 * np.sqrt(up + down) + 1, (what, up, down)
+
+
+U, HALF_STEP = 2.0 ** -24, 2.0 ** -150     # of fp32: relative, and of its subnormal numbers
+
+
+@pytest.mark.parametrize("eps", [1e-20, 1e-25, 1e-30, 2.0 ** -126])
+def test_second_moments_below_the_normal_numbers(eps):
+    """Gradients of 1e-20 to 1e-17, whose second moments are subnormal, beside an eps that
+    does not hide their roots.
+
+    v' is off by eight roundings u of it and by half a subnormal step, h, for each of
+    g^2 (then times 0.001), its product and the sum: dv <= 8 u v + 2.001 h.  Its root is off
+    by dv / sqrt(v) at most, and the update by that against the denominator that is left.
+    m' and w' round as usual (five u and three u of their terms, sixteen u of the update)."""
+    n, lr, b1, b2, wd = 4099, 1e-2, 0.9, 0.999, 0.01
+    gen = torch.Generator().manual_seed(22)
+    w = (torch.randn(n, generator=gen) * 0.1).to(DEV)
+    g = torch.zeros(n, device=DEV)
+    opt = srg.AdamW([w], [g])
+    for t in (1, 2, 3):
+        size = 10.0 ** (-20 + 3 * torch.rand(n, generator=gen, dtype=torch.float64))
+        g.copy_((size * torch.where(torch.rand(n, generator=gen) < 0.5, -1, 1)).float())
+        f64 = lambda x: x[:n].double().cpu().numpy()
+        w0, g0, m0, v0 = f64(w), f64(g), f64(opt.m), f64(opt.v)
+        srg.lora_adamw_step(opt, lr, b1, b2, eps, wd)
+        want, m, v, up = ref.adamw(w0, g0, m0, v0, t, lr, b1, b2, eps, wd)
+        dm = 5 * U * (np.abs(b1 * m0) + np.abs((1 - b1) * g0))
+        dv = 8 * U * v + 2.001 * HALF_STEP
+        assert (np.abs(f64(opt.m) - m) <= dm).all() and (np.abs(f64(opt.v) - v) <= dv).all()
+        left = 1 / np.sqrt(1 - b2 ** t)
+        den, dden = np.sqrt(v) * left + eps, dv / np.sqrt(v) * left
+        assert (dden < 0.05 * den).all()
+        tol = 3 * U * np.abs(w0) + np.abs(up) * (16 * U + dden / (den - dden)) \
+            + lr / (1 - b1 ** t) / (den - dden) * dm
+        assert (np.abs(f64(w) - want) <= tol).all(), (t, np.max(np.abs(f64(w) - want)))
+
+
+def test_smallest_eps_beside_8_bit_moments():
+    """eps 2^-40 is taken: blocks of second moments that became zeros, here of gradients
+    2^-48, leave m over eps and the new gradient's root, not more."""
+    w, g = torch.zeros(256, device=DEV), torch.full((256,), 2.0 ** -48, device=DEV)
+    opt = srg.AdamW([w], [g], bits=8)
+    for t in range(1, 5):
+        before = w.clone()
+        srg.lora_adamw_step(opt, 1.0, eps=2.0 ** -40, weight_decay=0.0)
+        assert not opt.v.any() and opt.m.any()
+        # at most the step that eps alone leaves: |m| / (1 - b1^t) = 2^-48 but for the codes
+        assert (before - w).abs().max() <= 2.0 ** -8 * 1.05
