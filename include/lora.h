@@ -600,7 +600,9 @@ lora_status lora_experts_gemm_backward(const void *dY, int64_t lddy, const void 
  *
  * Tensor i's moments start at element start(i), the sum of the earlier tensors'
  * numel, each rounded up to whole blocks; m and v hold lora_adamw_state_numel
- * elements, the scales one value a block.  Elements between tensors are scratch.
+ * elements, the scales one value a block.  Moments, scales and step counts are zeros
+ * before a tensor's first step.  Elements between tensors are scratch: what stands
+ * there does not count, and a step may write it.
  *
  * lora_adamw_table fills a HOST table of lora_adamw_table_bytes bytes from a HOST
  * array of tensors, and checks them: a NULL tensor or gradient of numel > 0

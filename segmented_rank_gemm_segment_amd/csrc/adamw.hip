@@ -104,6 +104,11 @@ __device__ __forceinline__ void store_some(T *p, int count, const float (&x)[kVe
 __device__ __forceinline__ uint32_t byte_of(const uint2 &q, int e) {
   return ((e < 4 ? q.x : q.y) >> (8 * (e & 3))) & 0xffu;
 }
+// The first `count` codes (any number, a tensor's last ones), zeros behind.
+__device__ __forceinline__ uint2 some_codes(uint2 q, int count) {
+  const uint64_t keep = count <= 0 ? 0ull : count >= kVec ? ~0ull : ~(~0ull << (8 * count));
+  return make_uint2(q.x & (uint32_t)keep, q.y & (uint32_t)(keep >> 32));
+}
 // c |c| and c^4 of the codes: the moments are these times the unit scales below.  Second
 // moments are formed 2^8 times as large, kLift, beside 8-bit codes: the unit of a scale near
 // 2^-100 is then a normal number, its reciprocal's 255^4 in range, and the root of what is
@@ -215,8 +220,8 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(AdamwArgs a) {
     const AdamwTensor t = a.tensors[ti];
     const int64_t base = (chunk - t.first_chunk) * kAdamwChunk;
     // Every step's loads go out before the first step's arithmetic.  A block's lanes stay
-    // together: lanes past the tensor's end, in its last block, hold zeros, and the
-    // moments' buffers hold whole blocks.
+    // together: the moments' buffers hold whole blocks, and lanes past the tensor's end, in its
+    // last block, hold zeros (32-bit moments: anything, which meets no other element).
     using W = typename std::conditional<MASTER, float, P>::type;
     Raw<G> graw[kSteps];
     Raw<W> wraw[kSteps];
@@ -269,6 +274,10 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(AdamwArgs a) {
       graw[s].values(g);
       wraw[s].values(w);
       if constexpr (EIGHT) {
+        if (e0 + kVec > n) {              // (what stands behind the tensor is no part of its block)
+          mq[s] = some_codes(mq[s], n - e0);
+          vq[s] = some_codes(vq[s], n - e0);
+        }
         powers_m(mq[s], m);
         powers_v(vq[s], v);
         mb *= ms[s] * kUnitM;

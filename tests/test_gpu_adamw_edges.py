@@ -90,3 +90,34 @@ def test_smallest_eps_beside_8_bit_moments():
         assert not opt.v.any() and opt.m.any()
         # at most the step that eps alone leaves: |m| / (1 - b1^t) = 2^-48 but for the codes
         assert (before - w).abs().max() <= 2.0 ** -8 * 1.05
+
+
+@pytest.mark.parametrize("p,g,masters", [(torch.float32, torch.float32, None),
+                                         (torch.bfloat16, torch.bfloat16, True)])
+def test_codes_between_tensors_do_not_count(p, g, masters):
+    """What stands in the 8-bit moments behind a tensor's last element, in its last block,
+    changes neither the block's scale nor the tensor's own codes."""
+    sizes = [1, 7, 8, 9, 255, 256, 257, 4091, 5000]
+    opts = []
+    for _ in range(2):
+        gen = torch.Generator().manual_seed(23)
+        opts.append(srg.AdamW([(torch.randn(n, generator=gen) * 0.1).to(p).to(DEV) for n in sizes],
+                              [torch.zeros(n, dtype=g, device=DEV) for n in sizes], bits=8,
+                              masters=masters))
+    a, b = opts
+    inside = torch.zeros(a.numel, dtype=torch.bool, device=DEV)
+    for at, n in zip(a.starts, sizes):
+        inside[at:at + n] = True
+    gen = torch.Generator().manual_seed(24)
+    for step in range(4):
+        for x, y in zip(a.grads, b.grads):
+            # (small ones behind the first step, beside which a large code's value shows)
+            x.copy_(torch.randn(x.shape, generator=gen) * 10.0 ** -step)
+            y.copy_(x)
+        b.m.masked_fill_(~inside, 127 if step % 2 else -128)
+        b.v.masked_fill_(~inside, 255)
+        for o in opts:
+            srg.lora_adamw_step(o, 1e-2, beta1=0.5, beta2=0.9, seed=step)
+        assert torch.equal(a.m_scale, b.m_scale) and torch.equal(a.v_scale, b.v_scale), step
+        assert torch.equal(a.m[inside], b.m[inside]) and torch.equal(a.v[inside], b.v[inside]), step
+        assert all(torch.equal(x, y) for x, y in zip(a.params, b.params)), step
