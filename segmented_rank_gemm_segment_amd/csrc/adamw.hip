@@ -157,6 +157,11 @@ __device__ __forceinline__ float over_scale(float top, float scale) {
   return scale > 0.f ? top / scale : 0.f;             // (NaN: 0, and codes of 0)
 }
 
+// 1 for what is above 0 (by 2^-126 or more), 0 for the rest: a product that is held to [0, 1]
+__device__ __forceinline__ float one_above(float x) {
+  return __builtin_amdgcn_fmed3f(x * 0x1p126f, 0.f, 1.f);
+}
+
 // The codes of first moments: z = 127^2 |x| / scale lies between c^2 and (c + 1)^2, and
 // u (2 c + 1) < z - c^2 takes the upper one; u comes in 2^-16ths.  An error of the root
 // changes c beside a whole number only, where the other c with the other share is the same.
@@ -170,7 +175,7 @@ __device__ __forceinline__ uint2 codes_m(const float (&x)[kVec], float scale,
   for (int e = 0; e < kVec; ++e) {
     const float z = fabsf(x[e]) * inv;
     float c = fminf(floorf(__builtin_amdgcn_sqrtf(z)), 126.f);
-    c += u[e] * fmaf(c, 0x1p-15f, 0x1p-16f) < fmaf(-c, c, z) ? 1.f : 0.f;
+    c += one_above(fmaf(-u[e], fmaf(c, 0x1p-15f, 0x1p-16f), fmaf(-c, c, z)));
     // a byte of c + 128, rounded (exact), less 128 by its upper bit
     q[e / 4] = __builtin_amdgcn_cvt_pk_u8_f32(copysignf(c, x[e]) + 128.f, e & 3, q[e / 4]);
   }
@@ -187,8 +192,8 @@ __device__ __forceinline__ uint2 codes_v(const float (&x)[kVec], const float (&r
     const float z = x[e] * inv;
     float c = floorf(__builtin_amdgcn_sqrtf(root[e] * rinv));
     const float c2 = c * c, t = c + c + 1.f;
-    c += u[e] * fmaf(c, 0x1p-15f, 0x1p-16f) * fmaf(c2, 2.f, t) < fmaf(-c2, c2, z) ? 1.f : 0.f;
-    c = fmaxf(c, __builtin_amdgcn_fmed3f(z * 0x1p126f, 0.f, 1.f));        // (1 if z > 0)
+    c += one_above(fmaf(-u[e] * fmaf(c, 0x1p-15f, 0x1p-16f), fmaf(c2, 2.f, t), fmaf(-c2, c2, z)));
+    c = fmaxf(c, one_above(z));
     q[e / 4] = __builtin_amdgcn_cvt_pk_u8_f32(c, e & 3, q[e / 4]);        // (held to 255)
   }
   return inv > 0.f ? make_uint2(q[0], q[1]) : make_uint2(0u, 0u);
