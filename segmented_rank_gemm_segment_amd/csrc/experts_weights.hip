@@ -298,12 +298,7 @@ __global__ __launch_bounds__(WM *WN *kWave, WM *WN *PER_CU / 4) void experts_wei
 }
 
 template <bool F32OUT, bool GATHER> void launch_weights(const ExpertGemmArgs &g, hipStream_t stream) {
-  // As long as the CUs do not all get one of the large tiles, tiles of 128 x 128, two
-  // workgroups a CU (large / 128, us: 8 experts of 64 rows, 1032 x 520, 16 / 13, of 1024 rows
-  // 67 / 50; 2 of 256 rows, 1024 x 1024, 18 / 11; but 8 of 256, 4096 x 14336, 410 / 493, 128
-  // of 64, 2048 x 1536, 232 / 304).
-  const int64_t tiles = (int64_t)((g.M + 255) / 256) * ((g.N + 255) / 256) * g.n_experts;
-  if (tiles > kCUs)
+  if (experts_weights_large(g.M, g.N, g.n_experts))
     hipLaunchKernelGGL((experts_weights_kernel<256, 256, 2, 4, 1, F32OUT, GATHER>), dim3(kCUs), dim3(512),
                        0, stream, g);
   else

@@ -178,4 +178,12 @@ inline ExpertsKernel experts_kernel_of(int n_choices, int n_experts, int K, int 
   return few < mid && few < large ? kExpertsFew : mid <= large ? kExpertsMid : kExpertsLarge;
 }
 
+// Their weights' gradients [M][N] (experts_weights.hip): 256 x 256 tiles, or, as long as the
+// CUs do not all get one of those, 128 x 128, two workgroups a CU (large / 128, us: 8 experts
+// of 64 rows, 1032 x 520, 16 / 13, of 1024 rows 67 / 50; 2 of 256 rows, 1024 x 1024, 18 / 11;
+// but 8 of 256, 4096 x 14336, 410 / 493, 128 of 64, 2048 x 1536, 232 / 304).
+inline bool experts_weights_large(int M, int N, int n_experts) {
+  return (int64_t)((M + 255) / 256) * ((N + 255) / 256) * n_experts > kCUs;
+}
+
 }  // namespace lora
