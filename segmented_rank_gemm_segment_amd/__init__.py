@@ -1142,7 +1142,10 @@ def lora_adamw_step(opt: AdamW, lr, beta1: float = 0.9, beta2: float = 0.999, ep
     runs (a captured step then follows a schedule).  grad_scale: float32 device
     tensor of one element that multiplies every gradient (a clipping factor).
     active: int32 device tensor [n_tensors]; tensors with 0 are left as they are,
-    their moments and step counts too.  seed: of the 8-bit moments' rounding.  eps:
+    their moments and step counts too.  Adapters without rows in the batch need it:
+    lora_linear_backward leaves their old gradients in place.  From the rows' slots,
+    without the host: live.zero_().index_fill_(0, torch.where((slot >= 0) & (slot < S),
+    slot, S).long(), 1), live int32 [S + 1], of which the first S count.  seed: of the 8-bit moments' rounding.  eps:
     2^-126 at least, 2^-40 (9.1e-13) with 8-bit moments."""
     for t, what in ((lr if isinstance(lr, torch.Tensor) else None, "lr"),
                     (grad_scale, "grad_scale")):
