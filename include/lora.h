@@ -29,7 +29,8 @@
  * - Data errors found on the device (a row's slot outside [-1, n_slots) or
  *   a slot rank outside [0, r_max]) never alias memory: the row is treated
  *   as base-only and counted in `*status` by lora_build_segments.
- * - Calls that share output buffers and overlap on one device race.
+ * - An output's memory is no other argument's, unless the call says so.  Calls that
+ *   share output buffers and overlap on one device race.
  */
 #ifndef LORA_H_
 #define LORA_H_
@@ -593,10 +594,11 @@ lora_status lora_experts_gemm_backward(const void *dY, int64_t lddy, const void 
  * consecutive elements of a tensor share an fp32 scale, their largest magnitude; m
  * holds int8 codes c of values scale (c / 127) |c / 127|, v uint8 codes of values
  * scale (c / 255)^4.  A value between two codes takes the upper one with the
- * probability that makes the expectation the value itself, by a hash of (seed, t,
- * tensor, element): the same call gives the same codes.  A v above 0 takes code 1
- * at least.  A block whose largest is below 2^-100 becomes zeros; one with a NaN or
- * an infinity, an m of 2^126 or a v of 2^118 and more, gets a NaN scale and codes 0.
+ * probability (a multiple of 2^-16) that makes the expectation the value itself, by
+ * a hash of (seed, t, tensor, element): the same call gives the same codes.  A v
+ * above 0 takes code 1 at least.  A block whose largest is below 2^-100 becomes zeros;
+ * one with a NaN or an infinity, an m of 2^126 or a v of 2^118 and more, gets a NaN
+ * scale and codes 0.
  *
  * Tensor i's moments start at element start(i), the sum of the earlier tensors'
  * numel, each rounded up to whole blocks; m and v hold lora_adamw_state_numel

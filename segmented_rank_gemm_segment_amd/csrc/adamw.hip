@@ -7,8 +7,8 @@
 // with t the tensor's own step count.  Bound by memory: each of w, m and v is read
 // and written once and g read once.  Measured: 201 M bf16 elements with fp32 masters and
 // moments (28 bytes an element) 1052 us, 5.4 TB/s, what a copy of 1 GiB reaches (5.2);
-// 176 M with 8-bit moments (10 bytes) 405 us, 4.3 TB/s, where the codes' arithmetic
-// shows; 8.4 M of 16.8 M taking part 58 us, 4.3 TB/s; 18 k elements of 9 tensors 9 to
+// 176 M with 8-bit moments (10 bytes) 380 us, 4.6 TB/s, where the codes' arithmetic
+// shows; 8.4 M of 16.8 M taking part 58 us, 4.3 TB/s; 18 k elements of 9 tensors 8 to
 // 13 us, the launches' latency.  The factors of a tensor are formed by each of its
 // workgroups: a launch of its own before this one took 3 to 5 us, which this hides.
 //
@@ -44,8 +44,9 @@ __host__ __device__ inline uint32_t mix32(uint32_t x) {
 }
 
 // The factors of a tensor's step, by two lanes.  The bias corrections are formed in 64
-// bits, as 1 - b^t of the first steps is a small difference, and b^t by squaring: at
-// most 62 products, so within 2^-46 of it.
+// bits, as 1 - b^t of the first steps is a small difference, and b^t by squaring.  A square
+// doubles the relative error of its factor, so b^t is off by t 2^-53 of it at most and 1 - b^t,
+// at least b^t t (1 - b), by 2^-53 / (1 - b) of it: what b's own last bit is to 1 - b.
 struct Factors {
   float rate, root, keep;
   uint32_t key;

@@ -23,7 +23,7 @@
 // past the barrier: 2%.)
 // Short segments: 128 x 128 tiles, two workgroups a CU, or the kernel for few rows below
 // (tile_choice.h), bound by W's bytes.  64 x 8 choices on 128 experts of 2048 -> 1536 in 144
-// to 156 us, 5.2 to 5.6 TB/s; one token's 8 choices in 13.6, half of a copy's rate.
+// to 156 us, 5.2 to 5.6 TB/s; one token's 8 choices, 50 MB, in 13.6, 3.7 TB/s.
 #include <type_traits>
 
 #include "experts_tiles.cuh"
